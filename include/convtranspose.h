@@ -38,6 +38,11 @@
  * the process ends (freed scratch stays in that pool for later calls; the device's
  * default pool is not touched).
  *
+ * Next to the convolution the library holds the other operators of a decoder layer:
+ * channels-last group norm with an activation (group_norm_nd and its gradient), dropout
+ * from a counter-based generator (dropout_nd, its own gradient) and the embedding lookup
+ * (embedding_nd and its gradient).  They also serve bfloat16.
+ *
  * Thread safety: every call is re-entrant; the error text is per host thread.
  */
 #ifndef CONVTRANSPOSE_H
@@ -58,9 +63,18 @@ typedef enum {
     CT_EDEVICE = 4        /* the HIP runtime reported an error at launch                */
 } ct_status;
 
-/* element types: the float types serve the float entry points, the 8-bit integer types
- * the quantized one (qlinear_convtranspose_nd) */
-typedef enum { CT_FLOAT32 = 0, CT_FLOAT16 = 1, CT_INT8 = 2, CT_UINT8 = 3 } ct_dtype;
+/* element types: float32 and float16 serve the float entry points, the 8-bit integer types
+ * the quantized one (qlinear_convtranspose_nd); bfloat16 serves group norm, dropout and the
+ * embedding only, int32 and int64 the embedding's ids */
+typedef enum {
+    CT_FLOAT32 = 0,
+    CT_FLOAT16 = 1,
+    CT_INT8 = 2,
+    CT_UINT8 = 3,
+    CT_BFLOAT16 = 4,
+    CT_INT32 = 5,
+    CT_INT64 = 6
+} ct_dtype;
 
 typedef enum { CT_NOTSET = 0, CT_SAME_UPPER = 1, CT_SAME_LOWER = 2, CT_VALID = 3 } ct_auto_pad;
 
@@ -82,12 +96,15 @@ typedef enum {
  *   CT_ACT_RELU        v > 0 ? v : 0
  *   CT_ACT_LEAKY_RELU  v >= 0 ? v : p0 * v          (p0 = slope, finite)
  *   CT_ACT_CLIP        v < p0 ? p0 : (v > p1 ? p1 : v)   (p0 <= p1, both finite)
+ * and, for group_norm_nd and its gradient only (the convolutions refuse it):
+ *   CT_ACT_SILU        v / (1 + exp(-v))
  */
 typedef enum {
     CT_ACT_IDENTITY = 0,
     CT_ACT_RELU = 1,
     CT_ACT_LEAKY_RELU = 2,
-    CT_ACT_CLIP = 3
+    CT_ACT_CLIP = 3,
+    CT_ACT_SILU = 4
 } ct_activation;
 
 /*
@@ -374,6 +391,118 @@ ct_status convtranspose_set_igemm_tile(int tile);
 
 /* The current setting of convtranspose_set_igemm_tile (-1: automatic). */
 int convtranspose_igemm_tile(void);
+
+/*
+ * Group norm with an activation and dropout, channels-last, enqueued on a HIP stream:
+ *   mean[n, g] = average, rstd[n, g] = 1 / sqrt(variance + eps) of the C/groups channels of
+ *                group g at all positions of image n (the variance divides by the count)
+ *   y = drop(act((x - mean) * rstd * gamma[c] + beta[c]))
+ * computed in float32 and rounded once into y.
+ *   dtype          CT_FLOAT32, CT_FLOAT16 or CT_BFLOAT16: the type of x and y
+ *   nsp            spatial rank, 1..3
+ *   x, y           device pointers, stored (N, D1..Dn, C), dense; y may be x itself and
+ *                  must not overlap it otherwise
+ *   x_shape        logical {N, C, D1..Dn}
+ *   groups         divides C
+ *   param_dtype    type of gamma and beta: dtype or CT_FLOAT32
+ *   gamma, beta    device arrays of C values, or NULL (1 and 0)
+ *   eps            finite, not negative
+ *   activation     any ct_activation; act_p0 / act_p1 as for convtranspose_nd_fused
+ *   dropout_p, seed, offset, step   dropout of the activation's output, as dropout_nd with
+ *                  the elements numbered in y's storage order; 0 for none
+ *   mean, rstd     device float32 arrays of N * groups values that receive the statistics
+ *                  (the gradient takes them), or NULL where nobody needs them
+ *   workspace      device scratch of workspace_bytes bytes (group_norm_workspace_size), 16-byte
+ *                  aligned, not in use by other work until this call's kernels have finished;
+ *                  NULL: stream-ordered scratch from the library's pool.  Its contents
+ *                  before the call do not matter.
+ * Validation comes first: on any error nothing is launched and the outputs are untouched.
+ * An empty x returns CT_OK and writes nothing.  The result does not depend on timing: the
+ * same inputs give the same bits.
+ */
+ct_status group_norm_nd(ct_dtype dtype, int nsp, const void *x, const int64_t *x_shape, int64_t groups,
+                        ct_dtype param_dtype, const void *gamma, const void *beta, float eps,
+                        ct_activation activation, float act_p0, float act_p1, double dropout_p, uint64_t seed,
+                        uint64_t offset, const uint64_t *step, void *y, float *mean, float *rstd,
+                        void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Its gradient: with xhat = (x - mean) * rstd, z = xhat * gamma + beta and
+ * dz = drop(dy) * act'(z) (the same dropout as the forward call's),
+ *   dbeta[c] = sum of dz, dgamma[c] = sum of dz * xhat   over images and positions
+ *   dx = rstd * (dz * gamma - average(dz * gamma) - xhat * average(dz * gamma * xhat)),
+ * the averages over the group.  act' at a kink: ReLU 0 at 0, leaky ReLU 1 at 0, clip 1 at
+ * both bounds.
+ *   dy, x, dx      stored as for group_norm_nd; dx may be dy or x itself
+ *   mean, rstd     what group_norm_nd wrote for this x
+ *   dgamma, dbeta  device arrays of C values of param_dtype, or NULL; with an empty x they
+ *                  are set to 0
+ * The other arguments and the errors as for group_norm_nd.
+ */
+ct_status group_norm_backward_nd(ct_dtype dtype, int nsp, const void *dy, const void *x, const int64_t *x_shape,
+                                 int64_t groups, const float *mean, const float *rstd, ct_dtype param_dtype,
+                                 const void *gamma, const void *beta, ct_activation activation, float act_p0,
+                                 float act_p1, double dropout_p, uint64_t seed, uint64_t offset,
+                                 const uint64_t *step, void *dx, void *dgamma, void *dbeta, void *workspace,
+                                 size_t workspace_bytes, void *stream);
+
+/* Workspace bytes of group_norm_nd (backward 0) or group_norm_backward_nd (1).  Host only. */
+ct_status group_norm_workspace_size(ct_dtype dtype, int nsp, const int64_t *x_shape, int64_t groups, int backward,
+                                    size_t *bytes_out);
+
+/*
+ * Dropout with a counter-based generator, enqueued on a HIP stream:
+ *   y[i] = (residual[i] +) (keep(i) ? factor * x[i] : 0),   i in storage order
+ * Element i takes the 16-bit field i % 8 (low half of each word first) of the
+ * Philox4x32-10 block (Salmon et al., SC 2011) of counter (i / 8, offset + *step), 64 bits
+ * each, under the 64-bit key seed.  With T = round(65536 p) (halves up) it is dropped
+ * when the field is below T, and factor = 65536 / (65536 - T), so the expectation of y is
+ * that of no dropout; p below 2^-17 drops nothing, p = 1 everything.  The mask is a function
+ * of (seed, offset + *step, i) and is never stored: the gradient of x is this call on the
+ * gradient of y (without residual), that of the residual the gradient of y itself.  Calls
+ * that shall be independent take different offsets (or seeds).
+ *   dtype          CT_FLOAT32, CT_FLOAT16 or CT_BFLOAT16
+ *   count          elements; x, residual and y are dense and stored in the same order
+ *   residual       device pointer, or NULL
+ *   y              may be x or residual itself, and must not overlap them otherwise
+ *   p              in [0, 1]
+ *   step           device pointer to one uint64 that is read when the kernel runs and added
+ *                  to offset, or NULL: a captured graph or a prepared call draws anew each
+ *                  time when the program counts it up
+ * Dropped elements are 0 even where x is not finite.  One rounding into y.
+ */
+ct_status dropout_nd(ct_dtype dtype, int64_t count, const void *x, const void *residual, void *y, double p,
+                     uint64_t seed, uint64_t offset, const uint64_t *step, void *stream);
+
+/*
+ * Embedding lookup, enqueued on a HIP stream: y[t, :] = scale * table[ids[t], :].
+ *   dtype          type of table and y: CT_FLOAT32, CT_FLOAT16 or CT_BFLOAT16
+ *   index_dtype    type of ids: CT_INT32 or CT_INT64
+ *   ids            device array of `tokens` row numbers
+ *   table, y       dense (rows, width) and (tokens, width); y must not overlap table
+ *   scale          finite, applied in float32 before the one rounding
+ * An id outside [0, rows) gives a row of zeros.  y is (tokens, width): for tokens of an
+ * (N, D1..Dn) grid that is the channels-last storage of (N, width, D1..Dn).
+ */
+ct_status embedding_nd(ct_dtype dtype, ct_dtype index_dtype, int64_t tokens, const void *ids, int64_t rows,
+                       int64_t width, const void *table, float scale, void *y, void *stream);
+
+/*
+ * Its gradient: dtable[v, :] = scale * sum of dy[t, :] over the tokens with ids[t] = v, in
+ * float32, tokens sorted by id; rows no token names are set to 0.  The sum's order is
+ * fixed by the ids, so the same inputs give the same bits.
+ *   dtype, grad_dtype   type of dy, and of dtable (dtype or CT_FLOAT32)
+ *   padding_idx    a row that takes no gradient (it becomes 0), or -1
+ *   workspace      as for group_norm_nd (embedding_workspace_size bytes)
+ * An id outside [0, rows) takes no part.  dtable must not overlap dy or ids.
+ */
+ct_status embedding_backward_nd(ct_dtype dtype, ct_dtype index_dtype, int64_t tokens, const void *ids, int64_t rows,
+                                int64_t width, const void *dy, float scale, int64_t padding_idx,
+                                ct_dtype grad_dtype, void *dtable, void *workspace, size_t workspace_bytes,
+                                void *stream);
+
+/* Workspace bytes of embedding_backward_nd.  Host only. */
+ct_status embedding_workspace_size(int64_t tokens, int64_t rows, int64_t width, size_t *bytes_out);
 
 /* Text of the last error on the calling host thread ("" after a successful call).
  * The pointer stays valid until the next library call on that thread. */

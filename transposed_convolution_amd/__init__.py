@@ -13,6 +13,7 @@ Outputs, Attributes, Type constraints); channels-last input/output as on the Cli
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional, Sequence, Tuple
@@ -25,6 +26,8 @@ __all__ = [
     "convtranspose_kernel_name", "library_path", "load_library", "channels_last_empty",
     "to_channels_last", "KERNELS", "ACTIVATIONS", "convolution_nd", "convolution_output_shape",
     "IGEMM_TILES", "set_igemm_tile", "igemm_tile", "qlinear_convtranspose_nd", "PreparedCall",
+    "NORM_ACTIVATIONS", "group_norm_nd", "group_norm_backward_nd", "dropout_nd", "embedding_nd",
+    "embedding_backward_nd",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -36,7 +39,12 @@ KERNELS = {"auto": 0, "direct": 1, "grouped": 2, "igemm": 3, "none": 4}
 # output activation fused into the kernels' output stage (ct_activation), with the number
 # of parameters each takes: leaky_relu (slope,), clip (lower, upper)
 ACTIVATIONS = {"identity": (0, 0), "relu": (1, 0), "leaky_relu": (2, 1), "clip": (3, 2)}
+# group norm's activations: the same and SiLU
+NORM_ACTIVATIONS = {**ACTIVATIONS, "silu": (4, 0)}
 _DTYPES = {torch.float32: 0, torch.float16: 1}
+# group norm, dropout and the embedding
+_LAYER_DTYPES = {**_DTYPES, torch.bfloat16: 4}
+_INDEX_DTYPES = {torch.int32: 5, torch.int64: 6}
 _STATUS = {0: "CT_OK", 1: "CT_EINVAL", 2: "CT_ESHAPE", 3: "CT_EUNSUPPORTED", 4: "CT_EDEVICE"}
 _lib = None
 
@@ -101,6 +109,22 @@ def load_library():
                                              c_i32, vp, ctypes.c_int, i64p, vp, vp, ctypes.c_int64, vp, vp,
                                              ctypes.c_int, i64p, c_f32, c_i32] + attrs + [vp]
     lib.qlinear_convtranspose_nd.restype = ctypes.c_int
+    c_int, c_i64, c_u64, c_size = ctypes.c_int, ctypes.c_int64, ctypes.c_uint64, ctypes.c_size_t
+    drop = [ctypes.c_double, c_u64, c_u64, vp]
+    act = [c_int, c_f32, c_f32]
+    lib.group_norm_nd.argtypes = [c_int, c_int, vp, i64p, c_i64, c_int, vp, vp, c_f32] + act + drop + [
+        vp, vp, vp, vp, c_size, vp]
+    lib.group_norm_backward_nd.argtypes = [c_int, c_int, vp, vp, i64p, c_i64, vp, vp, c_int, vp, vp] + act + drop + [
+        vp, vp, vp, vp, c_size, vp]
+    lib.group_norm_workspace_size.argtypes = [c_int, c_int, i64p, c_i64, c_int, ctypes.POINTER(c_size)]
+    lib.dropout_nd.argtypes = [c_int, c_i64, vp, vp, vp] + drop + [vp]
+    lib.embedding_nd.argtypes = [c_int, c_int, c_i64, vp, c_i64, c_i64, vp, c_f32, vp, vp]
+    lib.embedding_backward_nd.argtypes = [c_int, c_int, c_i64, vp, c_i64, c_i64, vp, c_f32, c_i64, c_int, vp, vp, c_size,
+                                          vp]
+    lib.embedding_workspace_size.argtypes = [c_i64, c_i64, c_i64, ctypes.POINTER(c_size)]
+    for fn in ("group_norm_nd", "group_norm_backward_nd", "group_norm_workspace_size", "dropout_nd", "embedding_nd",
+               "embedding_backward_nd", "embedding_workspace_size"):
+        getattr(lib, fn).restype = ctypes.c_int
     lib.convtranspose_set_igemm_tile.argtypes = [ctypes.c_int]
     lib.convtranspose_set_igemm_tile.restype = ctypes.c_int
     lib.convtranspose_igemm_tile.argtypes = []
@@ -555,19 +579,305 @@ def qlinear_convtranspose_nd(x: torch.Tensor, x_scale: float, x_zero_point: int,
     return out
 
 
+# ------------------------------------------------------------------------------------
+# The other operators of a decoder layer: group norm with an activation, dropout, embedding
+# ------------------------------------------------------------------------------------
+def _ptr(t: Optional[torch.Tensor]):
+    return None if t is None else ctypes.c_void_p(t.data_ptr())
+
+
+def _call(fn, args, out, keep, prepare_only):
+    """Run a marshalled C call, or hand it to PreparedCall with what it keeps alive."""
+    if prepare_only:
+        return fn, args, out, keep
+    first = out[0] if isinstance(out, tuple) else out
+    with torch.cuda.device(first.device):
+        st = fn(*args)
+    if st:
+        _raise(st)
+    return out
+
+
+def _scratch(nbytes: int, device, prepare_only):
+    """A prepared call's own workspace; a direct call takes the library's pool."""
+    if not prepare_only or not nbytes:
+        return None, 0
+    return torch.empty(nbytes, dtype=torch.uint8, device=device), nbytes
+
+
+def _on(stream):
+    """Memory of new outputs comes from the stream that writes them: torch may hand out what
+    the current stream still uses."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _stream_ptr(stream, device):
+    return ctypes.c_void_p((stream if stream is not None else torch.cuda.current_stream(device)).cuda_stream)
+
+
+def _dropout_args(p, seed, offset, step, device):
+    if not 0.0 <= float(p) <= 1.0:
+        raise ConvTransposeError(1, "the dropout probability must lie in [0, 1]")
+    for name, v in (("seed", seed), ("offset", offset)):
+        if not 0 <= int(v) < 1 << 64:
+            raise ConvTransposeError(1, f"{name} must be an unsigned 64-bit number")
+    if step is not None:
+        _check_tensor("step", step, device, torch.int64)
+        if step.numel() != 1:
+            raise ConvTransposeError(1, "step must hold one int64")
+    return [float(p), int(seed), int(offset), _ptr(step)]
+
+
+def _norm_args(x, groups, gamma, beta, activation, act_params):
+    """Checks both directions of group norm share; (type code of the parameters, act arguments)."""
+    if x.dtype not in _LAYER_DTYPES:
+        raise ConvTransposeError(3, f"dtype {x.dtype} is not served (float32, float16, bfloat16)")
+    if x.dim() < 3 or x.dim() > 5:
+        raise ConvTransposeError(1, "x must have rank 3, 4 or 5")
+    _check_tensor("x", x, x.device, x.dtype)
+    if not _dense(x, True):
+        raise ConvTransposeError(1, "x is not dense channels-last")
+    if int(groups) < 1 or x.shape[1] % int(groups):
+        raise ConvTransposeError(1, "groups must be at least 1 and divide the channels")
+    if activation not in NORM_ACTIVATIONS:
+        raise ConvTransposeError(1, f"unknown activation {activation!r}")
+    kind, n = NORM_ACTIVATIONS[activation]
+    if len(act_params) != n:
+        raise ConvTransposeError(1, f"{activation} takes {n} parameter(s)")
+    ptype = next((t.dtype for t in (gamma, beta) if t is not None), torch.float32)
+    if ptype not in (x.dtype, torch.float32):
+        raise ConvTransposeError(3, f"gamma and beta must be float32 or {x.dtype} (got {ptype})")
+    for name, t in (("gamma", gamma), ("beta", beta)):
+        if t is not None:
+            _check_tensor(name, t, x.device, ptype)
+            if t.dim() != 1 or not t.is_contiguous() or t.shape[0] != x.shape[1]:
+                raise ConvTransposeError(1, f"{name} must be a dense 1-D tensor with one value a channel")
+    return _LAYER_DTYPES[ptype], [kind] + [float(v) for v in act_params] + [0.0] * (2 - n)
+
+
+def _norm_workspace(x, groups, backward):
+    nbytes = ctypes.c_size_t(0)
+    st = load_library().group_norm_workspace_size(_LAYER_DTYPES[x.dtype], x.dim() - 2, _i64(x.shape), int(groups),
+                                                  int(backward), ctypes.byref(nbytes))
+    if st:
+        _raise(st)
+    return nbytes.value
+
+
+def _channels_last_like(name, t, x):
+    """A caller's output (None: a new one) with x's shape, type and channels-last storage."""
+    if t is None:
+        return channels_last_empty(tuple(x.shape), x.dtype, x.device)
+    _check_tensor(name, t, x.device, x.dtype)
+    if t.shape != x.shape:
+        raise ConvTransposeError(2, f"{name} has shape {tuple(t.shape)}, expected {tuple(x.shape)}")
+    if not _dense(t, True):
+        raise ConvTransposeError(1, f"{name} is not dense channels-last")
+    return t
+
+
+def group_norm_nd(x: torch.Tensor, groups: int, gamma: Optional[torch.Tensor] = None,
+                  beta: Optional[torch.Tensor] = None, *, eps: float = 1e-5, activation: str = "identity",
+                  act_params: Sequence[float] = (), dropout_p: float = 0.0, seed: int = 0, offset: int = 0,
+                  step: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                  stream: Optional[torch.cuda.Stream] = None,
+                  _prepare_only: bool = False) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """(y, mean, rstd): group norm over ``groups`` channel groups, an activation and dropout, in
+    one call, channels-last.
+
+    x: logical (N, C, D1..Dn) float32/float16/bfloat16, dense N, D.., C storage.  gamma, beta:
+    (C,) in x's type or float32, or None.  ``activation``: a name from NORM_ACTIVATIONS.
+    ``dropout_p``, ``seed``, ``offset``, ``step``: dropout of the activation's output as by
+    ``dropout_nd`` (elements in storage order).  y has x's layout (``out``: the caller's, may
+    be x); mean and rstd are (N, groups) float32, for ``group_norm_backward_nd``."""
+    lib = load_library()
+    ptype, act = _norm_args(x, groups, gamma, beta, activation, act_params)
+    drop = _dropout_args(dropout_p, seed, offset, step, x.device)
+    nbytes = _norm_workspace(x, groups, False) if _prepare_only else 0
+    with _on(stream):
+        out = _channels_last_like("out", out, x)
+        new = torch.empty if x.numel() else torch.zeros
+        mean, rstd = new((2, x.shape[0], int(groups)), dtype=torch.float32, device=x.device).unbind(0)
+        ws, wsb = _scratch(nbytes, x.device, _prepare_only)
+    args = (_LAYER_DTYPES[x.dtype], x.dim() - 2, _ptr(x), _i64(x.shape), int(groups), ptype, _ptr(gamma), _ptr(beta),
+            float(eps), *act, *drop, _ptr(out), _ptr(mean), _ptr(rstd), _ptr(ws), wsb, _stream_ptr(stream, x.device))
+    return _call(lib.group_norm_nd, args, (out, mean, rstd), ws, _prepare_only)
+
+
+def group_norm_backward_nd(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, rstd: torch.Tensor, groups: int,
+                           gamma: Optional[torch.Tensor] = None, beta: Optional[torch.Tensor] = None, *,
+                           activation: str = "identity", act_params: Sequence[float] = (), dropout_p: float = 0.0,
+                           seed: int = 0, offset: int = 0, step: Optional[torch.Tensor] = None,
+                           out: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None,
+                           _prepare_only: bool = False
+                           ) -> Tuple[torch.Tensor, Optional[torch.Tensor], Optional[torch.Tensor]]:
+    """(dx, dgamma, dbeta): the gradient of ``group_norm_nd`` from y's gradient dy, its input x
+    and the statistics it returned, with the same parameters, activation and dropout.
+    dgamma and dbeta have gamma's and beta's type and are None where those are.  ``out``:
+    the caller's dx (may be dy or x)."""
+    lib = load_library()
+    ptype, act = _norm_args(x, groups, gamma, beta, activation, act_params)
+    drop = _dropout_args(dropout_p, seed, offset, step, x.device)
+    _channels_last_like("dy", dy, x)
+    for name, t in (("mean", mean), ("rstd", rstd)):
+        _check_tensor(name, t, x.device, torch.float32)
+        if tuple(t.shape) != (x.shape[0], int(groups)) or not t.is_contiguous():
+            raise ConvTransposeError(1, f"{name} must be a dense (N, groups) tensor")
+    nbytes = _norm_workspace(x, groups, True) if _prepare_only else 0
+    with _on(stream):
+        out = _channels_last_like("out", out, x)
+        dgamma, dbeta = (None if t is None else torch.empty_like(t) for t in (gamma, beta))
+        ws, wsb = _scratch(nbytes, x.device, _prepare_only)
+    args = (_LAYER_DTYPES[x.dtype], x.dim() - 2, _ptr(dy), _ptr(x), _i64(x.shape), int(groups), _ptr(mean), _ptr(rstd),
+            ptype, _ptr(gamma), _ptr(beta), *act, *drop, _ptr(out), _ptr(dgamma), _ptr(dbeta), _ptr(ws), wsb,
+            _stream_ptr(stream, x.device))
+    return _call(lib.group_norm_backward_nd, args, (out, dgamma, dbeta), ws, _prepare_only)
+
+
+def _storage_order(t: torch.Tensor):
+    """Strides of the axes longer than one when t fills its storage without gaps or overlap,
+    else None."""
+    if t.numel() == 0:
+        return ()
+    axes = sorted((st, sz) for sz, st in zip(t.shape, t.stride()) if sz > 1)
+    acc = 1
+    for st, sz in axes:
+        if st != acc:
+            return None
+        acc *= sz
+    return tuple(st for sz, st in zip(t.shape, t.stride()) if sz > 1)
+
+
+def dropout_nd(x: torch.Tensor, p: float, *, seed: int, offset: int = 0, step: Optional[torch.Tensor] = None,
+               residual: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+               stream: Optional[torch.cuda.Stream] = None, _prepare_only: bool = False) -> torch.Tensor:
+    """y = (residual +) dropout(x): elements drop with probability p (in steps of 2^-16), the
+    others are scaled to keep the expectation.  The mask is a function of (seed, offset,
+    place in storage) and is never stored: the gradient of x is
+    ``dropout_nd(dy, p, seed=seed, offset=offset)``, that of the residual dy itself.
+
+    x: float32/float16/bfloat16 of any rank, dense in some order of its axes; residual and
+    out have x's strides (out may be x or residual).  Calls that shall be independent take
+    different offsets (or seeds).  ``step``: one int64 on the device that is added to the
+    offset when the kernel runs, so a captured or prepared call can draw anew each time."""
+    lib = load_library()
+    if x.dtype not in _LAYER_DTYPES:
+        raise ConvTransposeError(3, f"dtype {x.dtype} is not served (float32, float16, bfloat16)")
+    _check_tensor("x", x, x.device, x.dtype)
+    drop = _dropout_args(p, seed, offset, step, x.device)
+    order = _storage_order(x)
+    if order is None:
+        raise ConvTransposeError(1, "x must be dense")
+    if out is None:
+        with _on(stream):
+            out = torch.empty_like(x)  # keeps a dense tensor's strides
+    for name, t in (("residual", residual), ("out", out)):
+        if t is not None:
+            _check_tensor(name, t, x.device, x.dtype)
+            if t.shape != x.shape:
+                raise ConvTransposeError(2, f"{name} has shape {tuple(t.shape)}, expected {tuple(x.shape)}")
+            if _storage_order(t) != order:
+                raise ConvTransposeError(1, f"{name} must have x's strides")
+    args = (_LAYER_DTYPES[x.dtype], x.numel(), _ptr(x), _ptr(residual), _ptr(out), *drop, _stream_ptr(stream, x.device))
+    return _call(lib.dropout_nd, args, out, None, _prepare_only)
+
+
+def _check_ids(ids, device):
+    if not isinstance(ids, torch.Tensor):
+        raise TypeError("ids must be a torch.Tensor")
+    if ids.dtype not in _INDEX_DTYPES:
+        raise ConvTransposeError(3, f"ids must be int32 or int64 (got {ids.dtype})")
+    _check_tensor("ids", ids, device, ids.dtype)
+    if not ids.is_contiguous():
+        raise ConvTransposeError(1, "ids must be contiguous")
+
+
+def embedding_nd(ids: torch.Tensor, table: torch.Tensor, *, scale: float = 1.0, out: Optional[torch.Tensor] = None,
+                 stream: Optional[torch.cuda.Stream] = None, _prepare_only: bool = False) -> torch.Tensor:
+    """y = scale * table[ids], of shape ids.shape + (width,).  ids: int32/int64 of any rank,
+    contiguous; table: (rows, width) float32/float16/bfloat16, contiguous.  An id outside
+    [0, rows) gives zeros.  For an (N, D1..Dn) grid of ids, ``y.movedim(-1, 1)`` is the
+    channels-last (N, width, D1..Dn) tensor the convolutions take."""
+    lib = load_library()
+    if table.dtype not in _LAYER_DTYPES:
+        raise ConvTransposeError(3, f"dtype {table.dtype} is not served (float32, float16, bfloat16)")
+    _check_tensor("table", table, table.device, table.dtype)
+    if table.dim() != 2 or not table.is_contiguous():
+        raise ConvTransposeError(1, "table must be a dense (rows, width) tensor")
+    _check_ids(ids, table.device)
+    shape = tuple(ids.shape) + (table.shape[1],)
+    if out is None:
+        with _on(stream):
+            out = torch.empty(shape, dtype=table.dtype, device=table.device)
+    else:
+        _check_tensor("out", out, table.device, table.dtype)
+        if tuple(out.shape) != shape or not out.is_contiguous():
+            raise ConvTransposeError(2, f"out must be dense with shape {shape}")
+    args = (_LAYER_DTYPES[table.dtype], _INDEX_DTYPES[ids.dtype], ids.numel(), _ptr(ids), table.shape[0], table.shape[1],
+            _ptr(table), float(scale), _ptr(out), _stream_ptr(stream, table.device))
+    return _call(lib.embedding_nd, args, out, None, _prepare_only)
+
+
+def embedding_backward_nd(dy: torch.Tensor, ids: torch.Tensor, rows: int, *, scale: float = 1.0,
+                          padding_idx: Optional[int] = None, grad_dtype: Optional[torch.dtype] = None,
+                          out: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None,
+                          _prepare_only: bool = False) -> torch.Tensor:
+    """The table's gradient (rows, width) of ``embedding_nd`` from y's gradient dy, of shape
+    ids.shape + (width,), contiguous: the tokens sorted by id, each row's summed in float32
+    in their order (the same bits every time).  ``padding_idx``: a row that takes no
+    gradient.  ``grad_dtype``: dy's type (default) or float32."""
+    lib = load_library()
+    if dy.dtype not in _LAYER_DTYPES:
+        raise ConvTransposeError(3, f"dtype {dy.dtype} is not served (float32, float16, bfloat16)")
+    _check_tensor("dy", dy, dy.device, dy.dtype)
+    _check_ids(ids, dy.device)
+    if dy.dim() != ids.dim() + 1 or tuple(dy.shape[:-1]) != tuple(ids.shape) or not dy.is_contiguous():
+        raise ConvTransposeError(1, "dy must be a dense tensor of shape ids.shape + (width,)")
+    rows, width = int(rows), dy.shape[-1]
+    if rows < 0:
+        raise ConvTransposeError(1, "rows must not be negative")
+    if padding_idx is not None and not 0 <= int(padding_idx) < rows:
+        raise ConvTransposeError(1, "padding_idx must be a row of the table")
+    grad_dtype = dy.dtype if grad_dtype is None else grad_dtype
+    if grad_dtype not in (dy.dtype, torch.float32):
+        raise ConvTransposeError(3, f"grad_dtype must be {dy.dtype} or float32 (got {grad_dtype})")
+    if out is None:
+        with _on(stream):
+            out = torch.empty((rows, width), dtype=grad_dtype, device=dy.device)
+    else:
+        _check_tensor("out", out, dy.device, grad_dtype)
+        if tuple(out.shape) != (rows, width) or not out.is_contiguous():
+            raise ConvTransposeError(2, f"out must be dense with shape {(rows, width)}")
+    nbytes = ctypes.c_size_t(0)
+    if _prepare_only:
+        st = lib.embedding_workspace_size(ids.numel(), rows, width, ctypes.byref(nbytes))
+        if st:
+            _raise(st)
+    with _on(stream):
+        ws, wsb = _scratch(nbytes.value, dy.device, _prepare_only)
+    args = (_LAYER_DTYPES[dy.dtype], _INDEX_DTYPES[ids.dtype], ids.numel(), _ptr(ids), rows, width, _ptr(dy), float(scale),
+            -1 if padding_idx is None else int(padding_idx), _LAYER_DTYPES[grad_dtype], _ptr(out), _ptr(ws), wsb,
+            _stream_ptr(stream, dy.device))
+    return _call(lib.embedding_backward_nd, args, out, ws, _prepare_only)
+
+
 class PreparedCall:
-    """One call of ``convolution_nd`` or ``qlinear_convtranspose_nd`` with its arguments
-    validated and marshalled once: ``PreparedCall(convolution_nd, x, w, ...)`` takes the
-    function's own arguments; each call then enqueues the operation with a single C
-    call, writing the same output tensor (``.out``).  Repeated calls must be ordered on
+    """One call of ``convolution_nd``, ``qlinear_convtranspose_nd``, ``group_norm_nd``,
+    ``group_norm_backward_nd``, ``dropout_nd``, ``embedding_nd`` or
+    ``embedding_backward_nd`` with its arguments validated and marshalled once (and its
+    workspace, where it takes one, allocated): ``PreparedCall(convolution_nd, x, w, ...)``
+    takes the function's own arguments; each call then enqueues the operation with a single
+    C call, writing the same output tensors (``.out``).  Repeated calls must be ordered on
     one stream; the tensors must outlive the object."""
 
     def __init__(self, fn, *args, **kwargs):
-        if fn not in (convolution_nd, qlinear_convtranspose_nd):
-            raise TypeError("PreparedCall serves convolution_nd and qlinear_convtranspose_nd")
-        self._fn, self._args, self.out = fn(*args, _prepare_only=True, **kwargs)
-        self._keep = (args, kwargs)  # the pointers stay valid while the object lives
-        self.device = self.out.device
+        if fn not in (convolution_nd, qlinear_convtranspose_nd, group_norm_nd, group_norm_backward_nd, dropout_nd,
+                      embedding_nd, embedding_backward_nd):
+            raise TypeError("PreparedCall serves the package's functions that take tensors and return new ones, "
+                            "except convtranspose_nd (ConvTransposePlan)")
+        self._fn, self._args, self.out, *keep = fn(*args, _prepare_only=True, **kwargs)
+        self._keep = (args, kwargs, keep)  # the pointers stay valid while the object lives
+        self.device = (self.out[0] if isinstance(self.out, tuple) else self.out).device
 
     def __call__(self) -> torch.Tensor:
         with torch.cuda.device(self.device):
