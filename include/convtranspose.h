@@ -451,6 +451,19 @@ ct_status group_norm_workspace_size(ct_dtype dtype, int nsp, const int64_t *x_sh
                                     size_t *bytes_out);
 
 /*
+ * Control of both directions' kernels for tests and tuning, process-wide like
+ * convtranspose_set_igemm_tile: a call whose images each fit the chip's registers is served
+ * in one pass over x, its blocks exchanging partial sums; other calls, and calls in place,
+ * read their input twice.
+ *   one_pass    -1: by that rule (the default); 0: never one pass
+ *   wait_limit  looks at another block's partial sums before a block computes them itself
+ *               (so that no wait depends on what else runs): -1 for the default
+ * Returns CT_OK, or CT_EINVAL for other values.  No setting changes a result by more than
+ * the order of float32 sums; wait_limit changes none.
+ */
+ct_status group_norm_set_control(int one_pass, int wait_limit);
+
+/*
  * Dropout with a counter-based generator, enqueued on a HIP stream:
  *   y[i] = (residual[i] +) (keep(i) ? factor * x[i] : 0),   i in storage order
  * Element i takes the 16-bit field i % 8 (low half of each word first) of the

@@ -35,6 +35,15 @@ def rows_of(t):
     return host(t.movedim(1, -1).reshape(t.shape[0], -1, t.shape[1]))
 
 
+@pytest.fixture(params=["one_pass", "two_passes", "no_waiting"])
+def path(T, request):
+    """How group norm is computed: held in registers where it fits, read twice, or held with
+    every block computing at once what it would wait for."""
+    T.set_group_norm_control(request.param != "two_passes", 0 if request.param == "no_waiting" else None)
+    yield request.param
+    T.set_group_norm_control()
+
+
 def norm_inputs(n, c, dims, dtype, params, seed, mean=0.5, spread=1.0):
     rng = np.random.default_rng(seed)
     x = rng.normal(size=(n,) + dims + (c,)) * spread * rng.uniform(0.5, 1.5, c) + mean * rng.normal(size=c)
@@ -59,12 +68,12 @@ ACTS = [("silu", ()), ("identity", ()), ("relu", ()), ("leaky_relu", (0.2,)), ("
 
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
 @pytest.mark.parametrize("case", range(len(SHAPES)))
-def test_group_norm(T, case, dtype):
+def test_group_norm(T, path, case, dtype):
     n, c, dims, groups = SHAPES[case]
     kind, params = ACTS[case % len(ACTS)]
     p = (0.0, 0.3)[case % 2]
     ptype = "f32" if case % 3 else dtype
-    print(f"[case] group_norm {SHAPES[case]} {dtype} {kind} p={p} params {ptype}", flush=True)
+    print(f"[case] group_norm {SHAPES[case]} {dtype} {kind} p={p} params {ptype} {path}", flush=True)
     x, xv, _, _, ga, gav, be, bev = norm_inputs(n, c, dims, dtype, ptype, case)
     seed, offset = 0x9E3779B97F4A7C15, (7 << 40) + case
     y, mean, rstd = T.group_norm_nd(x, groups, ga, be, activation=kind, act_params=params, dropout_p=p, seed=seed,
@@ -79,12 +88,12 @@ def test_group_norm(T, case, dtype):
 
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
 @pytest.mark.parametrize("case", range(len(SHAPES)))
-def test_group_norm_gradient(T, case, dtype):
+def test_group_norm_gradient(T, path, case, dtype):
     n, c, dims, groups = SHAPES[case]
     kind, params = ACTS[(case + 2) % len(ACTS)]
     p = (0.3, 0.0)[case % 2]
     ptype = dtype if case % 3 else "f32"
-    print(f"[case] group_norm gradient {SHAPES[case]} {dtype} {kind} p={p} params {ptype}", flush=True)
+    print(f"[case] group_norm gradient {SHAPES[case]} {dtype} {kind} p={p} params {ptype} {path}", flush=True)
     x, xv, dy, dyv, ga, gav, be, bev = norm_inputs(n, c, dims, dtype, ptype, 100 + case)
     (_, mean, rstd), _ = R.group_norm(xv, groups, gav, bev, 1e-5, "identity")
     mean, rstd = (torch.from_numpy(a).float().cuda() for a in (mean, rstd))
@@ -124,7 +133,7 @@ def test_group_norm_absent_parameters(T, given):
 
 
 @pytest.mark.parametrize("shape", [(2, 32, (9, 7), 4), (1, 12, (3001,), 2), (1, 256, (64, 64), 32)])
-def test_group_norm_mean_far_from_zero(T, shape):
+def test_group_norm_mean_far_from_zero(T, path, shape):
     """Values of spread 1 around 4096: the variance is not a difference of large sums."""
     n, c, dims, groups = shape
     x, xv, _, _, ga, gav, be, bev = norm_inputs(n, c, dims, "f32", "f32", 9, mean=0.0)
@@ -138,7 +147,7 @@ def test_group_norm_mean_far_from_zero(T, shape):
     R.assert_close(rows_of(y), want[0], tol[0], "f32", "y")
 
 
-def test_group_norm_constant_and_non_finite_groups(T):
+def test_group_norm_constant_and_non_finite_groups(T, path):
     """A constant group gives beta; NaN and infinities stay inside their own group and image."""
     x, xv, _, _, ga, gav, be, bev = norm_inputs(2, 32, (6, 5), "f16", "f32", 3)
     x = x.clone(memory_format=torch.preserve_format)
@@ -179,10 +188,18 @@ def test_group_norm_unaligned_storage_in_place_and_streams(T):
         assert y is out
         for got, w in ((y, want[0]), (mean, want[1]), (rstd, want[2]), (dx, grads[0]), (dg, grads[1]), (db, grads[2])):
             assert torch.equal(got, w)
+    T.set_group_norm_control(one_pass=False)  # what a call in place takes
+    try:
+        want = [t.clone() for t in T.group_norm_nd(x, groups, ga, be, activation="silu", dropout_p=0.2, seed=5)]
+        grads = [t.clone() for t in T.group_norm_backward_nd(dy, x, want[1], want[2], groups, ga, be, activation="silu",
+                                                             dropout_p=0.2, seed=5)]
+    finally:
+        T.set_group_norm_control()
     for into in ("dy", "x"):
         xs, ds = shifted(x, 0), shifted(dy, 0)
         dx, dg, db = T.group_norm_backward_nd(ds, xs, want[1], want[2], groups, ga, be, activation="silu", dropout_p=0.2,
                                               seed=5, out=ds if into == "dy" else xs)
+        assert dx is (ds if into == "dy" else xs)
         assert torch.equal(dx, grads[0]) and torch.equal(dg, grads[1]) and torch.equal(db, grads[2])
     xs = shifted(x, 0)
     y, _, _ = T.group_norm_nd(xs, groups, ga, be, activation="silu", dropout_p=0.2, seed=5, out=xs)
@@ -190,7 +207,7 @@ def test_group_norm_unaligned_storage_in_place_and_streams(T):
 
 
 @pytest.mark.parametrize("shape", [(2, 16, (6, 7), 4), (1, 64, (33, 31), 8)])
-def test_group_norm_gradient_against_differences(T, shape):
+def test_group_norm_gradient_against_differences(T, path, shape):
     """The directional derivative of sum(w y) by central differences of the forward call."""
     n, c, dims, groups = shape
     x, _, w, wv, ga, _, be, _ = norm_inputs(n, c, dims, "f32", "f32", 77)
@@ -212,6 +229,29 @@ def test_group_norm_gradient_against_differences(T, shape):
         count = x.numel()
         bound = 4 * h * h * count ** 0.5 + 2.0 ** -20 * count ** 0.5 / h
         assert abs(slope - want) <= bound, (k, slope, want, bound)
+
+
+def test_group_norm_waiting_changes_no_bit(T):
+    """Partial sums computed by the block that misses them are the bits the other would send,
+    and one call repeated gives the same bits."""
+    for shape in ((1, 256, (64, 64), 32), (2, 36, (90, 91), 4), (3, 64, (17, 33, 20), 16)):
+        n, c, dims, groups = shape
+        x, _, dy, _, ga, _, be, _ = norm_inputs(n, c, dims, "f16", "f32", 13)
+        kw = dict(activation="silu", dropout_p=0.1, seed=4)
+
+        def both():
+            y, mean, rstd = T.group_norm_nd(x, groups, ga, be, **kw)
+            return [y, mean, rstd, *T.group_norm_backward_nd(dy, x, mean, rstd, groups, ga, be, **kw)]
+
+        want = both()
+        for limit in (None, 0, 1, 0):
+            T.set_group_norm_control(wait_limit=limit)
+            try:
+                got = both()
+                torch.cuda.synchronize()
+            finally:
+                T.set_group_norm_control()
+            assert all(torch.equal(a, b) for a, b in zip(got, want)), (shape, limit)
 
 
 def test_group_norm_empty(T):

@@ -71,6 +71,16 @@ def test_group_norm_workspace(T):
     assert lib.group_norm_workspace_size(1, 2, T._i64((1, 8, 4, 4)), 3, 0, ctypes.byref(n)) == 1
 
 
+def test_group_norm_control(T):
+    lib = T.load_library()
+    try:
+        assert lib.group_norm_set_control(1, -1) == 1 and lib.group_norm_set_control(-2, -1) == 1
+        assert lib.group_norm_set_control(-1, -2) == 1 and T.convtranspose_last_error()
+        assert lib.group_norm_set_control(0, 7) == 0
+    finally:
+        T.set_group_norm_control()
+
+
 def test_dropout_refusals(T):
     def call(dtype=1, count=8, x=P, res=None, y=P, p=0.5, step=None):
         return T.load_library().dropout_nd(dtype, count, x, res, y, p, 1, 2, step, None)

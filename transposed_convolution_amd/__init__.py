@@ -27,7 +27,7 @@ __all__ = [
     "to_channels_last", "KERNELS", "ACTIVATIONS", "convolution_nd", "convolution_output_shape",
     "IGEMM_TILES", "set_igemm_tile", "igemm_tile", "qlinear_convtranspose_nd", "PreparedCall",
     "NORM_ACTIVATIONS", "group_norm_nd", "group_norm_backward_nd", "dropout_nd", "embedding_nd",
-    "embedding_backward_nd",
+    "embedding_backward_nd", "set_group_norm_control",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -117,6 +117,8 @@ def load_library():
     lib.group_norm_backward_nd.argtypes = [c_int, c_int, vp, vp, i64p, c_i64, vp, vp, c_int, vp, vp] + act + drop + [
         vp, vp, vp, vp, c_size, vp]
     lib.group_norm_workspace_size.argtypes = [c_int, c_int, i64p, c_i64, c_int, ctypes.POINTER(c_size)]
+    lib.group_norm_set_control.argtypes = [c_int, c_int]
+    lib.group_norm_set_control.restype = c_int
     lib.dropout_nd.argtypes = [c_int, c_i64, vp, vp, vp] + drop + [vp]
     lib.embedding_nd.argtypes = [c_int, c_int, c_i64, vp, c_i64, c_i64, vp, c_f32, vp, vp]
     lib.embedding_backward_nd.argtypes = [c_int, c_int, c_i64, vp, c_i64, c_i64, vp, c_f32, c_i64, c_int, vp, vp, c_size,
@@ -732,6 +734,15 @@ def group_norm_backward_nd(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor
             ptype, _ptr(gamma), _ptr(beta), *act, *drop, _ptr(out), _ptr(dgamma), _ptr(dbeta), _ptr(ws), wsb,
             _stream_ptr(stream, x.device))
     return _call(lib.group_norm_backward_nd, args, (out, dgamma, dbeta), ws, _prepare_only)
+
+
+def set_group_norm_control(one_pass: bool = True, wait_limit: Optional[int] = None) -> None:
+    """Group norm's kernels, for tests and tuning (process-wide): ``one_pass`` False keeps
+    them from holding an image in registers; ``wait_limit`` is how often a block looks for
+    another's partial sums before it computes them itself (None: the default)."""
+    st = load_library().group_norm_set_control(-1 if one_pass else 0, -1 if wait_limit is None else int(wait_limit))
+    if st:
+        _raise(st)
 
 
 def _storage_order(t: torch.Tensor):

@@ -16,19 +16,23 @@
 // far from zero costs no digits of the spread around it.
 // Everything is float32 between the one load and the one store of an element.
 //
-// Both directions need every value of a group before the first output: a pass that reads
-// for the statistics and one that reads again and writes.
+// Both directions need every value of a group before the first output.  Where an image fits
+// the chip's registers it is read once and held there (ct_groupnorm.hpp); here are the
+// kernels for the others: a pass that reads for the statistics and one that reads again and
+// writes; and the entry points.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <numeric>
 #include <string>
 #include <type_traits>
 
-#include "ct_vec.hpp"
+#include "ct_groupnorm.hpp"
 
 namespace {
 
+using namespace ct::norm;
 using ct::Dropout;
 using ct::Raw;
 
@@ -63,60 +67,6 @@ struct Block {
     }
 };
 
-// (count, mean, sum of squared distances from the mean)
-struct Moments {
-    float n = 0.0f, mean = 0.0f, m2 = 0.0f;
-    __device__ __forceinline__ void join(float bn, float bmean, float bm2)
-    {
-        const float total = n + bn;
-        if (bn > 0.0f) {
-            const float d = bmean - mean, w = bn / total;
-            mean += d * w;
-            m2 += bm2 + d * d * n * w;
-            n = total;
-        }
-    }
-};
-
-// Activation and its derivative, one instance of f per kind.
-struct Silu {
-    __device__ __forceinline__ float y(float z) const { return z * __builtin_amdgcn_rcpf(1.0f + __expf(-z)); }
-    __device__ __forceinline__ float d(float z) const
-    {
-        const float s = __builtin_amdgcn_rcpf(1.0f + __expf(-z));
-        return s * (1.0f + z * (1.0f - s));
-    }
-};
-struct Identity {
-    __device__ __forceinline__ float y(float z) const { return z; }
-    __device__ __forceinline__ float d(float) const { return 1.0f; }
-};
-struct Relu {
-    __device__ __forceinline__ float y(float z) const { return z > 0.0f ? z : 0.0f; }
-    __device__ __forceinline__ float d(float z) const { return z > 0.0f ? 1.0f : 0.0f; }
-};
-struct Leaky {
-    float slope;
-    __device__ __forceinline__ float y(float z) const { return z >= 0.0f ? z : slope * z; }
-    __device__ __forceinline__ float d(float z) const { return z >= 0.0f ? 1.0f : slope; }
-};
-struct Clip {
-    float lo, hi;
-    __device__ __forceinline__ float y(float z) const { return z < lo ? lo : (z > hi ? hi : z); }
-    __device__ __forceinline__ float d(float z) const { return z >= lo && z <= hi ? 1.0f : 0.0f; }
-};
-template <class F>
-__device__ __forceinline__ void with_act(const ct::Act &a, F &&f)
-{
-    switch (a.kind) {
-    case CT_ACT_RELU: f(Relu{}); break;
-    case CT_ACT_LEAKY_RELU: f(Leaky{a.p0}); break;
-    case CT_ACT_CLIP: f(Clip{a.p0, a.p1}); break;
-    case CT_ACT_SILU: f(Silu{}); break;
-    default: f(Identity{}); break;
-    }
-}
-
 // A thread's place in its block's tiles.
 template <int V>
 struct Place {
@@ -133,29 +83,6 @@ struct Place {
         at = (b.chunk * k.tiles_per_chunk * k.rows + row) * k.C + b.c0 + col;
     }
 };
-
-// V elements of which the first `valid` exist.
-template <class T, int V>
-__device__ __forceinline__ Raw<T, V> load_first(const T *p, int valid)
-{
-    if (valid >= V) return *reinterpret_cast<const Raw<T, V> *>(p);
-    Raw<T, V> r{};
-#pragma unroll
-    for (int j = 0; j < V; ++j)
-        if (j < valid) r[j] = p[j];
-    return r;
-}
-template <class T, int V>
-__device__ __forceinline__ void store_first(T *p, const Raw<T, V> &r, int valid)
-{
-    if (valid >= V) {
-        *reinterpret_cast<Raw<T, V> *>(p) = r;
-        return;
-    }
-#pragma unroll
-    for (int j = 0; j < V; ++j)
-        if (j < valid) p[j] = r[j];
-}
 
 // How many of the thread's V elements of the tile at position p0 exist.
 template <int V>
@@ -272,9 +199,9 @@ __global__ __launch_bounds__(kThreads) void finish_kernel(const T *x, const floa
     }
 }
 
-template <class T, int V>
+template <class T, int V, class ACT>
 __global__ __launch_bounds__(kThreads) void apply_kernel(const T *x, Cut k, const float *mean, const float *rstd,
-                                                         ct::Param<T> gamma, ct::Param<T> beta, ct::Act act, Dropout drop,
+                                                         ct::Param<T> gamma, ct::Param<T> beta, ACT f, Dropout drop,
                                                          T *y)
 {
     const Block b(k, blockIdx.x);
@@ -291,22 +218,20 @@ __global__ __launch_bounds__(kThreads) void apply_kernel(const T *x, Cut k, cons
     const int64_t image = b.n * k.P * k.C + pl.at;
     const int64_t step = int64_t(k.rows) * k.C;
     const uint64_t counter = drop.threshold ? drop.counter() : 0;
-    with_act(act, [&](auto f) {
-        int64_t p0 = b.chunk * k.tiles_per_chunk * k.rows, at = image;
-        for (int64_t t = 0; t < k.tiles_per_chunk && p0 < k.P; ++t, p0 += k.rows, at += step) {
-            const int valid = valid_of(k, b, pl, p0);
-            if (valid == 0) continue;
-            const Raw<T, V> v = load_first<T, V>(x + at, valid);
-            const unsigned keep = drop.threshold ? ct::keep_bits<V>(drop, counter, uint64_t(at)) : 0xffu;
-            Raw<T, V> o;
+    int64_t p0 = b.chunk * k.tiles_per_chunk * k.rows, at = image;
+    for (int64_t t = 0; t < k.tiles_per_chunk && p0 < k.P; ++t, p0 += k.rows, at += step) {
+        const int valid = valid_of(k, b, pl, p0);
+        if (valid == 0) continue;
+        const Raw<T, V> v = load_first<T, V>(x + at, valid);
+        const unsigned keep = drop.threshold ? ct::keep_bits<V>(drop, counter, uint64_t(at)) : 0xffu;
+        Raw<T, V> o;
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const float r = f.y((float(v[j]) - mu[j]) * a[j] + sh[j]);
-                o[j] = T((keep >> j) & 1 ? r * drop.factor : 0.0f);
-            }
-            store_first<T, V>(y + at, o, valid);
+        for (int j = 0; j < V; ++j) {
+            const float r = f.y((float(v[j]) - mu[j]) * a[j] + sh[j]);
+            o[j] = T((keep >> j) & 1 ? r * drop.factor : 0.0f);
         }
-    });
+        store_first<T, V>(y + at, o, valid);
+    }
 }
 
 // ------------------------------------------------------------------------------------
@@ -332,10 +257,10 @@ struct Channels {
 };
 
 // sums[n][chunk][c] = (sum dz, sum dz xhat) over the chunk's positions.
-template <class T, int V>
+template <class T, int V, class ACT>
 __global__ __launch_bounds__(kThreads) void grad_stats_kernel(const T *dy, const T *x, Cut k, const float *mean,
                                                               const float *rstd, ct::Param<T> gamma, ct::Param<T> beta,
-                                                              ct::Act act, Dropout drop, float2 *sums)
+                                                              ACT f, Dropout drop, float2 *sums)
 {
     __shared__ float2 lds[kThreads * V];
     const Block b(k, blockIdx.x);
@@ -345,23 +270,21 @@ __global__ __launch_bounds__(kThreads) void grad_stats_kernel(const T *dy, const
     const int64_t step = int64_t(k.rows) * k.C;
     const uint64_t counter = drop.threshold ? drop.counter() : 0;
     float s1[V] = {}, s2[V] = {};
-    with_act(act, [&](auto f) {
-        int64_t p0 = b.chunk * k.tiles_per_chunk * k.rows, at = image;
-        for (int64_t t = 0; t < k.tiles_per_chunk && p0 < k.P; ++t, p0 += k.rows, at += step) {
-            const int valid = valid_of(k, b, pl, p0);
-            if (valid == 0) continue;
-            const Raw<T, V> xv = load_first<T, V>(x + at, valid), dv = load_first<T, V>(dy + at, valid);
-            const unsigned keep = drop.threshold ? ct::keep_bits<V>(drop, counter, uint64_t(at)) : 0xffu;
+    int64_t p0 = b.chunk * k.tiles_per_chunk * k.rows, at = image;
+    for (int64_t t = 0; t < k.tiles_per_chunk && p0 < k.P; ++t, p0 += k.rows, at += step) {
+        const int valid = valid_of(k, b, pl, p0);
+        if (valid == 0) continue;
+        const Raw<T, V> xv = load_first<T, V>(x + at, valid), dv = load_first<T, V>(dy + at, valid);
+        const unsigned keep = drop.threshold ? ct::keep_bits<V>(drop, counter, uint64_t(at)) : 0xffu;
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const float xh = (float(xv[j]) - ch.mu[j]) * ch.rs[j];
-                const float e = (keep >> j) & 1 ? float(dv[j]) * drop.factor : 0.0f;
-                const float dz = e * f.d(xh * ch.ga[j] + ch.be[j]);
-                s1[j] += j < valid ? dz : 0.0f;
-                s2[j] += j < valid ? dz * xh : 0.0f;
-            }
+        for (int j = 0; j < V; ++j) {
+            const float xh = (float(xv[j]) - ch.mu[j]) * ch.rs[j];
+            const float e = (keep >> j) & 1 ? float(dv[j]) * drop.factor : 0.0f;
+            const float dz = e * f.d(xh * ch.ga[j] + ch.be[j]);
+            s1[j] += j < valid ? dz : 0.0f;
+            s2[j] += j < valid ? dz * xh : 0.0f;
         }
-    });
+    }
     if (pl.active)
         for (int j = 0; j < V; ++j) lds[pl.e + j] = make_float2(s1[j], s2[j]);
     __syncthreads();
@@ -451,10 +374,10 @@ __global__ __launch_bounds__(kThreads) void grad_groups_kernel(const float2 *tot
     if (lane == 0) coef[i] = make_float2(a / count, b / count);
 }
 
-template <class T, int V>
+template <class T, int V, class ACT>
 __global__ __launch_bounds__(kThreads) void grad_apply_kernel(const T *dy, const T *x, Cut k, const float *mean,
                                                               const float *rstd, ct::Param<T> gamma, ct::Param<T> beta,
-                                                              ct::Act act, Dropout drop, const float2 *coef, T *dx)
+                                                              ACT f, Dropout drop, const float2 *coef, T *dx)
 {
     const Block b(k, blockIdx.x);
     const Place<V> pl(k, b);
@@ -469,24 +392,60 @@ __global__ __launch_bounds__(kThreads) void grad_apply_kernel(const T *dy, const
     const int64_t image = b.n * k.P * k.C + pl.at;
     const int64_t step = int64_t(k.rows) * k.C;
     const uint64_t counter = drop.threshold ? drop.counter() : 0;
-    with_act(act, [&](auto f) {
-        int64_t p0 = b.chunk * k.tiles_per_chunk * k.rows, at = image;
-        for (int64_t t = 0; t < k.tiles_per_chunk && p0 < k.P; ++t, p0 += k.rows, at += step) {
-            const int valid = valid_of(k, b, pl, p0);
-            if (valid == 0) continue;
-            const Raw<T, V> xv = load_first<T, V>(x + at, valid), dv = load_first<T, V>(dy + at, valid);
-            const unsigned keep = drop.threshold ? ct::keep_bits<V>(drop, counter, uint64_t(at)) : 0xffu;
-            Raw<T, V> o;
+    int64_t p0 = b.chunk * k.tiles_per_chunk * k.rows, at = image;
+    for (int64_t t = 0; t < k.tiles_per_chunk && p0 < k.P; ++t, p0 += k.rows, at += step) {
+        const int valid = valid_of(k, b, pl, p0);
+        if (valid == 0) continue;
+        const Raw<T, V> xv = load_first<T, V>(x + at, valid), dv = load_first<T, V>(dy + at, valid);
+        const unsigned keep = drop.threshold ? ct::keep_bits<V>(drop, counter, uint64_t(at)) : 0xffu;
+        Raw<T, V> o;
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const float xh = (float(xv[j]) - ch.mu[j]) * ch.rs[j];
-                const float e = (keep >> j) & 1 ? float(dv[j]) * drop.factor : 0.0f;
-                const float dz = e * f.d(xh * ch.ga[j] + ch.be[j]);
-                o[j] = T(ch.rs[j] * (dz * ch.ga[j] - c1[j] - xh * c2[j]));
-            }
-            store_first<T, V>(dx + at, o, valid);
+        for (int j = 0; j < V; ++j) {
+            const float xh = (float(xv[j]) - ch.mu[j]) * ch.rs[j];
+            const float e = (keep >> j) & 1 ? float(dv[j]) * drop.factor : 0.0f;
+            const float dz = e * f.d(xh * ch.ga[j] + ch.be[j]);
+            o[j] = T(ch.rs[j] * (dz * ch.ga[j] - c1[j] - xh * c2[j]));
         }
-    });
+        store_first<T, V>(dx + at, o, valid);
+    }
+}
+
+__global__ __launch_bounds__(kThreads) void empty_kernel(unsigned long long *p, int64_t count)
+{
+    for (int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x; i < count; i += int64_t(gridDim.x) * kThreads) p[i] = kEmpty;
+}
+
+// dgamma and dbeta from the chunks' channel sums: 16 channels a block, 16 threads a channel.
+template <class T>
+__global__ __launch_bounds__(kThreads) void held_param_kernel(const float2 *sums, int64_t parts, int C, bool f32, void *dgamma,
+                                                              void *dbeta)
+{
+    __shared__ float2 lds[16][16];
+    const int c = int(blockIdx.x) * 16 + int(threadIdx.x & 15), q = threadIdx.x / 16;
+    float2 s = make_float2(0.0f, 0.0f);
+    if (c < C) {
+#pragma unroll 8
+        for (int64_t i = q; i < parts; i += 16) {
+            const float2 v = sums[i * C + c];
+            s.x += v.x;
+            s.y += v.y;
+        }
+    }
+    lds[q][threadIdx.x & 15] = s;
+    __syncthreads();
+    if (q != 0 || c >= C) return;
+    for (int i = 1; i < 16; ++i) {
+        s.x += lds[i][threadIdx.x].x;
+        s.y += lds[i][threadIdx.x].y;
+    }
+    if (dgamma) {
+        if (f32) static_cast<float *>(dgamma)[c] = s.y;
+        else static_cast<T *>(dgamma)[c] = T(s.y);
+    }
+    if (dbeta) {
+        if (f32) static_cast<float *>(dbeta)[c] = s.x;
+        else static_cast<T *>(dbeta)[c] = T(s.x);
+    }
 }
 
 // ------------------------------------------------------------------------------------
@@ -529,24 +488,98 @@ struct Sizes {
     bool empty() const { return N == 0 || C == 0 || P == 0; }
 };
 
+// Controls for tests and tuning (group_norm_set_control).
+std::atomic<int> g_one_pass{-1}, g_wait_limit{-1};
+constexpr int kWaitLimit = 4096;  // looks, about a microsecond each
+
+// Blocks of kHeld threads the current device holds at once, two a compute unit (the
+// kernels' register bound).
+int64_t resident_blocks()
+{
+    int dev = 0, units = 0;
+    if (hipGetDevice(&dev) != hipSuccess) return 0;
+    if (hipDeviceGetAttribute(&units, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess) return 0;
+    return 2 * int64_t(units);
+}
+
+// The one-pass cut, if there is one.
+bool make_one(const Sizes &s, bool backward, bool in_place, OneCut *k, bool *uni)
+{
+    const int want = g_one_pass.load(std::memory_order_relaxed);
+    if (want == 0 || in_place) return false;
+    const int V = s.dt == CT_FLOAT32 ? 4 : 8;
+    const int64_t Cg = s.C / s.G;
+    *uni = Cg % V == 0;
+    const int64_t K = held_tiles(*uni, backward), threads = backward ? kHeldGrad : kHeld, most = threads * V;  // elements of a tile
+    // groups of the narrowest slab whose rows are whole vectors, or all of them
+    int64_t nb = V / std::gcd(Cg, int64_t(V));
+    if (nb > s.G || s.G % nb) nb = s.G;
+    auto try_slab = [&](int64_t groups, int64_t max_chunks) {
+        const int64_t width = groups * Cg;
+        if (groups > kMostGroups || width > most) return false;
+        const int64_t unit = V / std::gcd(width, int64_t(V));
+        if (unit > 1 && groups != s.G) return false;
+        const int64_t fit = most / width / unit * unit;
+        if (fit < 1 || fit * s.C > (int64_t(1) << 29)) return false;  // 32-bit offsets in a tile
+        const int64_t need = (s.P + unit - 1) / unit * unit;
+        k->rows = int(std::min(fit, need));
+        const int64_t tiles = (s.P + k->rows - 1) / k->rows;
+        const int64_t chunks = (tiles + K - 1) / K;
+        if (chunks > max_chunks) return false;
+        k->tiles = int((tiles + chunks - 1) / chunks);
+        k->chunks = int((tiles + k->tiles - 1) / k->tiles);
+        k->width = int(width);
+        k->groups = int(groups);
+        k->slabs = int(s.G / groups);
+        return true;
+    };
+    k->P = s.P;
+    k->C = int(s.C);
+    k->G = int(s.G);
+    k->Cg = int(Cg);
+    bool ok = try_slab(nb, 1);
+    if (!ok) {
+        // as many groups a slab as fit: whole rows where possible
+        int64_t wide = s.G;
+        while (wide > nb && (wide * Cg > most || wide > kMostGroups || s.G % wide)) --wide;
+        const int64_t room = resident_blocks();
+        ok = try_slab(wide, room / std::max<int64_t>(1, s.G / wide));
+        if (ok && int64_t(k->chunks) * k->slabs > room) ok = false;
+    }
+    if (!ok || s.N > (int64_t(1) << 22) / (int64_t(k->chunks) * k->slabs)) return false;
+    k->lanes = 1;
+    while (k->lanes < 64 && 2 * k->lanes * k->groups <= threads) k->lanes *= 2;
+    const int limit = g_wait_limit.load(std::memory_order_relaxed);
+    k->limit = limit < 0 ? kWaitLimit : limit;
+    return true;
+}
+
 struct Plan {
-    bool vec = true;
+    bool vec = true, one = false, uni = false;
     Cut k;
-    size_t part = 0, stats = 0, total = 0, coef = 0, bytes = 0;
+    OneCut h;
+    size_t part = 0, stats = 0, total = 0, coef = 0, words = 0, bytes = 0;
 };
 
-Plan make_plan(const Sizes &s, bool backward)
+Plan make_plan(const Sizes &s, bool backward, bool in_place)
 {
     Plan p;
     if (s.empty()) return p;
-    p.vec = s.dt == CT_FLOAT32 ? make_cut<4>(s.N, s.P, s.C, s.G, &p.k) : make_cut<8>(s.N, s.P, s.C, s.G, &p.k);
-    if (!p.vec) make_cut<1>(s.N, s.P, s.C, s.G, &p.k);
     size_t at = 0;
     auto place = [&](size_t bytes) {
         const size_t q = at;
         at += (bytes + 255) & ~size_t(255);
         return q;
     };
+    p.one = make_one(s, backward, in_place, &p.h, &p.uni);
+    if (p.one) {
+        p.words = place(p.h.chunks > 1 ? size_t(s.N) * s.G * p.h.chunks * 8 : 0);
+        if (backward) p.part = place(size_t(s.N) * p.h.chunks * s.C * 8);
+        p.bytes = at;
+        return p;
+    }
+    p.vec = s.dt == CT_FLOAT32 ? make_cut<4>(s.N, s.P, s.C, s.G, &p.k) : make_cut<8>(s.N, s.P, s.C, s.G, &p.k);
+    if (!p.vec) make_cut<1>(s.N, s.P, s.C, s.G, &p.k);
     if (backward) {
         p.part = place(size_t(s.N) * p.k.chunks * s.C * 8);
         p.total = place(size_t(s.N) * s.C * 8);
@@ -620,9 +653,27 @@ ct_status check_params(int dt, int pt, const void *gamma, const void *beta)
 
 unsigned blocks_of(int64_t items, int64_t per) { return unsigned((items + per - 1) / per); }
 
+// Empties the exchanged words, if blocks exchange any.
+void empty_words(const Plan &p, const Sizes &s, unsigned long long *words, hipStream_t hs)
+{
+    if (p.h.chunks == 1) return;
+    const int64_t count = s.N * s.G * p.h.chunks;
+    empty_kernel<<<std::min<unsigned>(blocks_of(count, kThreads), 1024), kThreads, 0, hs>>>(words, count);
+}
+
 }  // namespace
 
 extern "C" {
+
+ct_status group_norm_set_control(int one_pass, int wait_limit)
+{
+    ct::set_last_error(std::string());
+    if (one_pass < -1 || one_pass > 0) return fail(CT_EINVAL, "one_pass must be -1 (automatic) or 0 (never)");
+    if (wait_limit < -1) return fail(CT_EINVAL, "wait_limit must be -1 (the default) or a number of looks");
+    g_one_pass.store(one_pass, std::memory_order_relaxed);
+    g_wait_limit.store(wait_limit, std::memory_order_relaxed);
+    return CT_OK;
+}
 
 ct_status group_norm_workspace_size(ct_dtype dtype, int nsp, const int64_t *x_shape, int64_t groups, int backward,
                                     size_t *bytes_out)
@@ -633,7 +684,8 @@ ct_status group_norm_workspace_size(ct_dtype dtype, int nsp, const int64_t *x_sh
     Sizes s;
     const ct_status st = check_sizes(ct::enum_int(dtype), nsp, x_shape, groups, &s);
     if (st != CT_OK) return st;
-    *bytes_out = make_plan(s, backward != 0).bytes;
+    // in place or not, and with any control: the larger
+    *bytes_out = std::max(make_plan(s, backward != 0, false).bytes, make_plan(s, backward != 0, true).bytes);
     return CT_OK;
 }
 
@@ -662,16 +714,38 @@ ct_status group_norm_nd(ct_dtype dtype, int nsp, const void *x, const int64_t *x
     if (workspace && !ct::aligned_to(workspace, 16)) return fail(CT_EINVAL, "workspace must be 16-byte aligned");
     if (s.empty()) return CT_OK;
     if (!x || !y) return fail(CT_EINVAL, "x or y is NULL");
-    const Plan p = make_plan(s, false);
+    const Plan p = make_plan(s, false, x == y);
     const hipStream_t hs = static_cast<hipStream_t>(stream);
     ct::Scratch ws;
     st = ws.take(workspace, workspace_bytes, p.bytes, hs, &err);
     if (st != CT_OK) return fail(st, err);
     char *const base = static_cast<char *>(ws.p);
     float *const part = reinterpret_cast<float *>(base + p.part);
-    if (!mean) mean = reinterpret_cast<float *>(base + p.stats);
-    if (!rstd) rstd = reinterpret_cast<float *>(base + p.stats) + s.N * s.G;
-    const int64_t blocks = s.N * p.k.chunks * p.k.slabs;
+    unsigned long long *const words = reinterpret_cast<unsigned long long *>(base + p.words);
+    if (!p.one && !mean) mean = reinterpret_cast<float *>(base + p.stats);
+    if (!p.one && !rstd) rstd = reinterpret_cast<float *>(base + p.stats) + s.N * s.G;
+    const int64_t blocks = p.one ? s.N * p.h.chunks * p.h.slabs : s.N * p.k.chunks * p.k.slabs;
+    if (p.one) {
+        Call c;
+        c.dt = dt;
+        c.params_f32 = pt == CT_FLOAT32;
+        c.x = x;
+        c.y = y;
+        c.gamma = gamma;
+        c.beta = beta;
+        c.eps = eps;
+        c.mean = mean;
+        c.rstd = rstd;
+        c.act = act;
+        c.drop = drop;
+        c.words = words;
+        empty_words(p, s, words, hs);
+        ct::mark_before(hs);
+        launch_held(c, p.h, p.uni, blocks, hs);
+        ct::mark_after(hs);
+        st = ct::launch_status("group norm launch failed", &err);
+        return st == CT_OK ? CT_OK : fail(st, err);
+    }
     ct::with_type(dt, [&](auto t) {
         using T = decltype(t);
         const T *xp = static_cast<const T *>(x);
@@ -681,8 +755,10 @@ ct_status group_norm_nd(ct_dtype dtype, int nsp, const void *x, const int64_t *x
             stats_kernel<T, V><<<unsigned(blocks), kThreads, 0, hs>>>(xp, p.k, part);
             finish_kernel<T><<<blocks_of(s.N * s.G, kThreads / 64), kThreads, 0, hs>>>(xp, part, p.k, s.N * s.G, eps, mean, rstd);
             ct::mark_before(hs);
-            apply_kernel<T, V><<<unsigned(blocks), kThreads, 0, hs>>>(xp, p.k, mean, rstd, ga, be, act, drop,
-                                                                     static_cast<T *>(y));
+            with_act(act, [&](auto f) {
+                apply_kernel<T, V, decltype(f)>
+                    <<<unsigned(blocks), kThreads, 0, hs>>>(xp, p.k, mean, rstd, ga, be, f, drop, static_cast<T *>(y));
+            });
             ct::mark_after(hs);
         };
         if (p.vec) go(std::integral_constant<int, ct::kVec<T>>{});
@@ -720,7 +796,7 @@ ct_status group_norm_backward_nd(ct_dtype dtype, int nsp, const void *dy, const 
     const hipStream_t hs = static_cast<hipStream_t>(stream);
     if (s.C == 0) return CT_OK;
     if (!s.empty() && (!x || !dy || !dx || !mean || !rstd)) return fail(CT_EINVAL, "x, dy, dx, mean or rstd is NULL");
-    const Plan p = make_plan(s, true);
+    const Plan p = make_plan(s, true, dx == x || dx == dy);
     ct::Scratch ws;
     st = ws.take(workspace, workspace_bytes, p.bytes, hs, &err);
     if (st != CT_OK) return fail(st, err);
@@ -728,19 +804,51 @@ ct_status group_norm_backward_nd(ct_dtype dtype, int nsp, const void *dy, const 
     float2 *const part = reinterpret_cast<float2 *>(base + p.part);
     float2 *const total = reinterpret_cast<float2 *>(base + p.total);
     float2 *const coef = reinterpret_cast<float2 *>(base + p.coef);
-    const int64_t blocks = s.empty() ? 0 : s.N * p.k.chunks * p.k.slabs;
+    unsigned long long *const words = reinterpret_cast<unsigned long long *>(base + p.words);
+    const int64_t blocks = s.empty() ? 0 : p.one ? s.N * p.h.chunks * p.h.slabs : s.N * p.k.chunks * p.k.slabs;
+    if (p.one) {
+        Call c;
+        c.dt = dt;
+        c.params_f32 = pt == CT_FLOAT32;
+        c.x = x;
+        c.dy = dy;
+        c.dx = dx;
+        c.gamma = gamma;
+        c.beta = beta;
+        c.mean = const_cast<float *>(mean);
+        c.rstd = const_cast<float *>(rstd);
+        c.act = act;
+        c.drop = drop;
+        c.words = words;
+        c.sums = part;
+        empty_words(p, s, words, hs);
+        ct::mark_before(hs);
+        launch_held_grad(c, p.h, p.uni, blocks, hs);
+        ct::mark_after(hs);
+    }
     ct::with_type(dt, [&](auto t) {
         using T = decltype(t);
         const T *xp = static_cast<const T *>(x), *dp = static_cast<const T *>(dy);
         const ct::Param<T> ga{gamma, pt == CT_FLOAT32}, be{beta, pt == CT_FLOAT32};
+        if (p.one) {
+            if (dgamma || dbeta)
+                held_param_kernel<T><<<blocks_of(s.C, 16), kThreads, 0, hs>>>(part, s.N * p.h.chunks, int(s.C),
+                                                                             pt == CT_FLOAT32, dgamma, dbeta);
+            return;
+        }
         auto go = [&](auto v) {
             constexpr int V = decltype(v)::value;
-            grad_stats_kernel<T, V><<<unsigned(blocks), kThreads, 0, hs>>>(dp, xp, p.k, mean, rstd, ga, be, act, drop, part);
+            with_act(act, [&](auto f) {
+                grad_stats_kernel<T, V, decltype(f)>
+                    <<<unsigned(blocks), kThreads, 0, hs>>>(dp, xp, p.k, mean, rstd, ga, be, f, drop, part);
+            });
             grad_join_kernel<<<unsigned(s.N * blocks_of(s.C, 64)), 1024, 0, hs>>>(part, p.k, total);
             grad_groups_kernel<T><<<blocks_of(s.N * s.G, kThreads / 64), kThreads, 0, hs>>>(total, p.k, s.N * s.G, ga, coef);
             ct::mark_before(hs);
-            grad_apply_kernel<T, V><<<unsigned(blocks), kThreads, 0, hs>>>(dp, xp, p.k, mean, rstd, ga, be, act, drop, coef,
-                                                                          static_cast<T *>(dx));
+            with_act(act, [&](auto f) {
+                grad_apply_kernel<T, V, decltype(f)><<<unsigned(blocks), kThreads, 0, hs>>>(
+                    dp, xp, p.k, mean, rstd, ga, be, f, drop, coef, static_cast<T *>(dx));
+            });
             ct::mark_after(hs);
         };
         if (!s.empty()) {
