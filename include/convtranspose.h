@@ -452,16 +452,15 @@ ct_status group_norm_workspace_size(ct_dtype dtype, int nsp, const int64_t *x_sh
 
 /*
  * Control of both directions' kernels for tests and tuning, process-wide like
- * convtranspose_set_igemm_tile: a call whose images each fit the chip's registers is served
- * in one pass over x, its blocks exchanging partial sums; other calls, and calls in place,
- * read their input twice.
- *   one_pass    -1: by that rule (the default); 0: never one pass
- *   wait_limit  looks at another block's partial sums before a block computes them itself
- *               (so that no wait depends on what else runs): -1 for the default
- * Returns CT_OK, or CT_EINVAL for other values.  No setting changes a result by more than
- * the order of float32 sums; wait_limit changes none.
+ * convtranspose_set_igemm_tile.  Groups that fit one block's registers are read once; for the
+ * others a first pass makes partial sums, which the blocks of the second pass join
+ * themselves or, where there are many, a kernel between the two.
+ *   one_block   -1: by that rule (the default); 0: always two passes
+ *   join        -1: by that rule (the default); 0: never a kernel between; 1: always
+ * Returns CT_OK, or CT_EINVAL for other values.  A setting changes a result by the order of
+ * float32 sums only.
  */
-ct_status group_norm_set_control(int one_pass, int wait_limit);
+ct_status group_norm_set_control(int one_block, int join);
 
 /*
  * Dropout with a counter-based generator, enqueued on a HIP stream:

@@ -35,11 +35,11 @@ def rows_of(t):
     return host(t.movedim(1, -1).reshape(t.shape[0], -1, t.shape[1]))
 
 
-@pytest.fixture(params=["one_pass", "two_passes", "no_waiting"])
+@pytest.fixture(params=["automatic", "two_passes", "joined_between"])
 def path(T, request):
-    """How group norm is computed: held in registers where it fits, read twice, or held with
-    every block computing at once what it would wait for."""
-    T.set_group_norm_control(request.param != "two_passes", 0 if request.param == "no_waiting" else None)
+    """How group norm is computed: by its own choice, or always in two passes, the partial sums
+    joined in the second one or between them."""
+    T.set_group_norm_control(request.param == "automatic", {"two_passes": False, "joined_between": True}.get(request.param))
     yield request.param
     T.set_group_norm_control()
 
@@ -188,13 +188,6 @@ def test_group_norm_unaligned_storage_in_place_and_streams(T):
         assert y is out
         for got, w in ((y, want[0]), (mean, want[1]), (rstd, want[2]), (dx, grads[0]), (dg, grads[1]), (db, grads[2])):
             assert torch.equal(got, w)
-    T.set_group_norm_control(one_pass=False)  # what a call in place takes
-    try:
-        want = [t.clone() for t in T.group_norm_nd(x, groups, ga, be, activation="silu", dropout_p=0.2, seed=5)]
-        grads = [t.clone() for t in T.group_norm_backward_nd(dy, x, want[1], want[2], groups, ga, be, activation="silu",
-                                                             dropout_p=0.2, seed=5)]
-    finally:
-        T.set_group_norm_control()
     for into in ("dy", "x"):
         xs, ds = shifted(x, 0), shifted(dy, 0)
         dx, dg, db = T.group_norm_backward_nd(ds, xs, want[1], want[2], groups, ga, be, activation="silu", dropout_p=0.2,
@@ -231,9 +224,7 @@ def test_group_norm_gradient_against_differences(T, path, shape):
         assert abs(slope - want) <= bound, (k, slope, want, bound)
 
 
-def test_group_norm_waiting_changes_no_bit(T):
-    """Partial sums computed by the block that misses them are the bits the other would send,
-    and one call repeated gives the same bits."""
+def test_group_norm_repeats_its_bits(T, path):
     for shape in ((1, 256, (64, 64), 32), (2, 36, (90, 91), 4), (3, 64, (17, 33, 20), 16)):
         n, c, dims, groups = shape
         x, _, dy, _, ga, _, be, _ = norm_inputs(n, c, dims, "f16", "f32", 13)
@@ -244,14 +235,8 @@ def test_group_norm_waiting_changes_no_bit(T):
             return [y, mean, rstd, *T.group_norm_backward_nd(dy, x, mean, rstd, groups, ga, be, **kw)]
 
         want = both()
-        for limit in (None, 0, 1, 0):
-            T.set_group_norm_control(wait_limit=limit)
-            try:
-                got = both()
-                torch.cuda.synchronize()
-            finally:
-                T.set_group_norm_control()
-            assert all(torch.equal(a, b) for a, b in zip(got, want)), (shape, limit)
+        for _ in range(3):
+            assert all(torch.equal(a, b) for a, b in zip(both(), want)), shape
 
 
 def test_group_norm_empty(T):

@@ -43,7 +43,7 @@ def test_group_norm_refusals(T):
            (dict(act=2, p0=INF), 1), (dict(act=3, p0=1.0, p1=0.0), 1), (dict(act=3, p0=NAN), 1), (dict(p=-0.1), 1),
            (dict(p=1.01), 1), (dict(p=NAN), 1), (dict(step=ctypes.c_void_p(260)), 1), (dict(x=ODD), 1),
            (dict(mean=ctypes.c_void_p(258)), 1), (dict(x=None), 1), (dict(ws=ctypes.c_void_p(264), wsb=1 << 20), 1),
-           (dict(ws=P, wsb=8), 1), (dict(shape=(1 << 22, 8, 1, 1)), 3), (dict(shape=(2, 1 << 31, 1, 1), groups=1), 3)]
+           (dict(ws=P, wsb=8, shape=(2, 8, 300, 300)), 1), (dict(shape=(1 << 24, 8, 1, 1)), 3), (dict(shape=(2, 1 << 31, 1, 1), groups=1), 3)]
     for kw, want in bad:
         assert _norm(T, **kw) == want, kw
         assert T.convtranspose_last_error(), kw
@@ -64,7 +64,8 @@ def test_group_norm_workspace(T):
         for shape in ((1, 8, 1, 1), (8, 256, 128, 128), (2, 4104, 5, 5), (3, 1001, 9, 9)):
             for backward in (0, 1):
                 assert lib.group_norm_workspace_size(dtype, 2, T._i64(shape), 1, backward, ctypes.byref(n)) == 0
-                assert 0 <= n.value <= 4 * shape[0] * shape[1] * shape[2] * shape[3] + (1 << 16)
+                # at most two float32 sums an element, where a chunk is one position
+                assert 0 <= n.value <= 8 * shape[0] * shape[1] * shape[2] * shape[3] + (1 << 16)
     assert lib.group_norm_workspace_size(1, 2, T._i64((0, 8, 4, 4)), 1, 0, ctypes.byref(n)) == 0 and n.value == 0
     assert lib.group_norm_workspace_size(1, 2, T._i64((1, 8, 4, 4)), 1, 2, ctypes.byref(n)) == 1
     assert lib.group_norm_workspace_size(1, 2, T._i64((1, 8, 4, 4)), 1, 0, None) == 1
@@ -76,7 +77,7 @@ def test_group_norm_control(T):
     try:
         assert lib.group_norm_set_control(1, -1) == 1 and lib.group_norm_set_control(-2, -1) == 1
         assert lib.group_norm_set_control(-1, -2) == 1 and T.convtranspose_last_error()
-        assert lib.group_norm_set_control(0, 7) == 0
+        assert lib.group_norm_set_control(-1, 2) == 1 and lib.group_norm_set_control(0, 1) == 0
     finally:
         T.set_group_norm_control()
 

@@ -736,11 +736,11 @@ def group_norm_backward_nd(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor
     return _call(lib.group_norm_backward_nd, args, (out, dgamma, dbeta), ws, _prepare_only)
 
 
-def set_group_norm_control(one_pass: bool = True, wait_limit: Optional[int] = None) -> None:
-    """Group norm's kernels, for tests and tuning (process-wide): ``one_pass`` False keeps
-    them from holding an image in registers; ``wait_limit`` is how often a block looks for
-    another's partial sums before it computes them itself (None: the default)."""
-    st = load_library().group_norm_set_control(-1 if one_pass else 0, -1 if wait_limit is None else int(wait_limit))
+def set_group_norm_control(one_block: bool = True, join: Optional[bool] = None) -> None:
+    """Group norm's kernels, for tests and tuning (process-wide): ``one_block`` False takes two
+    passes even where a group fits one block; ``join`` True or False joins the first pass's
+    partial sums in a kernel of its own or in the second pass (None: by their number)."""
+    st = load_library().group_norm_set_control(-1 if one_block else 0, -1 if join is None else int(join))
     if st:
         _raise(st)
 

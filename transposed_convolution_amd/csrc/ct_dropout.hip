@@ -7,6 +7,7 @@
 #include <hip/hip_runtime.h>
 
 #include <string>
+#include <type_traits>
 
 #include "ct_vec.hpp"
 
@@ -18,12 +19,14 @@ using ct::Raw;
 constexpr int kThreads = 256;
 
 // One thread makes the eight elements of one generator block.
-template <class T, bool RES>
+template <class T, bool RES, bool DROP>
 __global__ __launch_bounds__(kThreads) void dropout_kernel(const T *x, const T *res, T *y, int64_t count, Dropout d)
 {
+    const uint64_t counter = DROP ? d.counter() : 0;
+    const uint32_t limit = d.limit();
     for (int64_t b = int64_t(blockIdx.x) * kThreads + threadIdx.x; b * 8 < count; b += int64_t(gridDim.x) * kThreads) {
     const int64_t i = b * 8;
-    const unsigned keep = d.threshold ? ct::keep8(d, d.counter(), uint64_t(b)) : 0xffu;
+    const ct::Fields f = DROP ? ct::draw_fields<8, true>(d, counter, uint64_t(i)) : ct::Fields{};
     const int left = count - i < 8 ? int(count - i) : 8;
     if (left == 8) {
         constexpr int V = ct::kVec<T>;
@@ -34,14 +37,16 @@ __global__ __launch_bounds__(kThreads) void dropout_kernel(const T *x, const T *
             if (RES) r = *reinterpret_cast<const Raw<T, V> *>(res + i + h * V);
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                const float t = (keep >> (h * V + j)) & 1 ? float(v[j]) * d.factor : 0.0f;
+                const float t = !DROP ? float(v[j]) : f.stays(h * V + j, limit) ? float(v[j]) * d.factor : 0.0f;
                 o[j] = T(RES ? float(r[j]) + t : t);
             }
             *reinterpret_cast<Raw<T, V> *>(y + i + h * V) = o;
         }
     } else {
-        for (int j = 0; j < left; ++j) {
-            const float t = (keep >> j) & 1 ? float(x[i + j]) * d.factor : 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            if (j >= left) break;
+            const float t = !DROP ? float(x[i + j]) : f.stays(j, limit) ? float(x[i + j]) * d.factor : 0.0f;
             y[i + j] = T(RES ? float(res[i + j]) + t : t);
         }
     }
@@ -79,10 +84,16 @@ extern "C" ct_status dropout_nd(ct_dtype dtype, int64_t count, const void *x, co
     ct::with_type(dt, [&](auto t) {
         using T = decltype(t);
         const T *xp = static_cast<const T *>(x), *rp = static_cast<const T *>(residual);
-        if (residual)
-            dropout_kernel<T, true><<<unsigned(blocks), kThreads, 0, hs>>>(xp, rp, static_cast<T *>(y), count, d);
-        else
-            dropout_kernel<T, false><<<unsigned(blocks), kThreads, 0, hs>>>(xp, rp, static_cast<T *>(y), count, d);
+        auto go = [&](auto r, auto dr) {
+            dropout_kernel<T, decltype(r)::value, decltype(dr)::value>
+                <<<unsigned(blocks), kThreads, 0, hs>>>(xp, rp, static_cast<T *>(y), count, d);
+        };
+        constexpr std::true_type yes{};
+        constexpr std::false_type no{};
+        if (residual && d.threshold) go(yes, yes);
+        else if (residual) go(yes, no);
+        else if (d.threshold) go(no, yes);
+        else go(no, no);
     });
     ct::mark_after(hs);
     const ct_status ls = ct::launch_status("dropout launch failed", &err);

@@ -1,5 +1,5 @@
-// ct_groupnorm.hpp -- what the group norm kernels share: moments, activations, the cut of
-// the one-pass kernels and the exchange between their blocks.
+// ct_groupnorm.hpp -- what the group norm kernels share: moments, activations, how a call
+// is cut into blocks and how a thread finds its elements.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -35,7 +35,7 @@ struct Silu {
     __device__ __forceinline__ float d(float z) const
     {
         const float s = __builtin_amdgcn_rcpf(1.0f + __expf(-z));
-        return s * (1.0f + z * (1.0f - s));
+        return __builtin_fmaf(z * s, 1.0f - s, s);
     }
 };
 struct Identity {
@@ -76,7 +76,7 @@ template <class T, int V>
 __device__ __forceinline__ void store_first(T *p, const Raw<T, V> &r, int valid)
 {
     if (valid >= V) {
-        *reinterpret_cast<Raw<T, V> *>(p) = r;
+        __builtin_nontemporal_store(r, reinterpret_cast<Raw<T, V> *>(p));  // nobody here reads it again
         return;
     }
 #pragma unroll
@@ -85,204 +85,261 @@ __device__ __forceinline__ void store_first(T *p, const Raw<T, V> &r, int valid)
 }
 
 // ------------------------------------------------------------------------------------
-// One pass: every value is read once and held in registers until it is written
+// How (N, P, C) is cut
 // ------------------------------------------------------------------------------------
-// A block holds `tiles` <= K tiles of a slab of whole groups.  When one block holds all
-// positions of its groups (chunks == 1) it finishes alone.  Otherwise the blocks of an
-// image exchange one 64-bit word per group and chunk: two float32 partials, stored and
-// loaded as one relaxed device-scope atomic, so a word that is not kEmpty is complete and
-// no fence or flag is needed.  The words are set to kEmpty by a kernel before.
-//
-// Waiting: a block waits only for blocks of its own image, which are launched next to it,
-// and the host takes this path only when all blocks of an image fit the chip together.  The
-// wait is bounded all the same: after `limit` looks a block computes what is missing
-// itself, from memory, by the same operations (so the result is the same bits).  Every
-// wait therefore ends whatever else runs on the device.
-constexpr unsigned long long kEmpty = ~0ull;
-// Threads of a block: two blocks share a compute unit, so a forward thread has 128 registers
-// (64 of them hold 16 vectors) and a gradient thread 256 (128 hold 16 vectors of x and dy).
-constexpr int kHeld = 512, kHeldGrad = 256;
+// Slabs of whole groups, as many as a tile's row holds (or, where one group is wider than
+// that, of a part of a group), and chunks of `tiles` tiles of `rows` positions.  A thread
+// owns the V consecutive elements at e = V * thread of every tile (a tile's elements run
+// through its rows), so its channels are the same in all of them.  One slab holding all
+// channels may have any width: its tile is contiguous and a vector may run over a row's end.
 constexpr int kMostGroups = 1024;  // groups of a slab
-
-
-constexpr int kSmallHeld = 4;  // tiles held by the instances for short chunks
-constexpr int held_tiles(bool uni, bool backward) { return uni || backward ? 16 : 8; }
-
-struct OneCut {
+struct Cut {
     int64_t P;
     int C, G, Cg;
-    int width, slabs, groups;  // channels and groups of a slab
-    int rows, tiles;
-    int chunks;
+    int width, slabs;  // channels of a slab (the last, or a group's last, may be narrower)
+    int per;           // groups of a slab
+    int split;         // slabs of a group: 1, or more when a group is wider than a slab
+    int rows, tiles, chunks;
     int lanes;  // threads that share a group when partials are joined: a power of two
-    int limit;
+
+    __host__ __device__ int64_t span() const { return int64_t(tiles) * rows; }  // positions of a chunk
 };
 
-// A call of either direction (dy, dx and sums: the gradient).
-struct Call {
-    int dt = CT_FLOAT32;
-    bool params_f32 = true;
-    const void *x = nullptr, *dy = nullptr, *gamma = nullptr, *beta = nullptr;
-    void *y = nullptr, *dx = nullptr;
-    float eps = 0.0f;
-    float *mean = nullptr, *rstd = nullptr;
-    Act act;
-    Dropout drop;
-    unsigned long long *words = nullptr;
-    float2 *sums = nullptr;
-};
-
-// The one-pass kernels over `blocks` blocks; uni: every 16-byte vector lies inside one group.
-void launch_held(const Call &c, const OneCut &k, bool uni, int64_t blocks, hipStream_t st);
-void launch_held_grad(const Call &c, const OneCut &k, bool uni, int64_t blocks, hipStream_t st);
-
-__device__ __forceinline__ unsigned long long pack2(float a, float b)
-{
-    const unsigned long long w =
-        (static_cast<unsigned long long>(__float_as_uint(b)) << 32) | static_cast<unsigned long long>(__float_as_uint(a));
-    return w == kEmpty ? w - 1 : w;  // a pair of NaN of another payload
-}
-__device__ __forceinline__ void publish(unsigned long long *p, float a, float b)
-{
-    __hip_atomic_store(p, pack2(a, b), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-}
-__device__ __forceinline__ unsigned long long look(const unsigned long long *p)
-{
-    return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-}
-__device__ __forceinline__ float low2(unsigned long long w) { return __uint_as_float(unsigned(w)); }
-__device__ __forceinline__ float high2(unsigned long long w) { return __uint_as_float(unsigned(w >> 32)); }
-
-// A block's place: image, chunk, slab, and the thread's vector within a tile.  An address is
+// A block's image, chunk and slab, and the thread's vector within a tile.  An address is
 // kept as a block-uniform tile offset (scalar registers) and the thread's 32-bit offset in
 // the tile: 64-bit addresses of every tile would take the registers that hold the tiles.
 template <int V>
-struct HeldPlace {
+struct Place {
     int64_t n;
-    int chunk, slab, c0;
+    int chunk, sub;
+    int g0, groups;  // groups of the slab
+    int c0, width;   // its channels
     int e, col;
     unsigned off;  // elements
     bool active;
-    __device__ HeldPlace(const OneCut &k, int64_t b)
+    __device__ Place(const Cut &k, unsigned b)
     {
-        slab = int(b % k.slabs);
-        b /= k.slabs;
-        chunk = int(b % k.chunks);
-        n = b / k.chunks;
-        c0 = slab * k.width;
+        const unsigned rest = b / unsigned(k.slabs);
+        const int slab = int(b - rest * unsigned(k.slabs));
+        n = rest / unsigned(k.chunks);
+        chunk = int(rest - unsigned(n) * unsigned(k.chunks));
+        if (k.split == 1) {
+            sub = 0;
+            g0 = slab * k.per;
+            groups = k.G - g0 < k.per ? k.G - g0 : k.per;
+            c0 = g0 * k.Cg;
+            width = groups * k.Cg;
+        } else {
+            g0 = slab / k.split;
+            sub = slab - g0 * k.split;
+            groups = 1;
+            c0 = g0 * k.Cg + sub * k.width;
+            width = k.Cg - sub * k.width < k.width ? k.Cg - sub * k.width : k.width;
+        }
         e = int(threadIdx.x) * V;
-        active = e < k.rows * k.width;
+        active = e < k.rows * width;
         if (!active) e = 0;
-        const int row = e / k.width;
-        col = e - row * k.width;
+        const int row = e / width;
+        col = e - row * width;
         off = unsigned(row) * unsigned(k.C) + unsigned(col);
     }
-    // element offset of tile i of chunk q
-    __device__ __forceinline__ int64_t tile(const OneCut &k, int q, int i) const
+    // element offset of the block's tile i
+    __device__ __forceinline__ int64_t tile(const Cut &k, int i) const
     {
-        return (n * k.P + (int64_t(q) * k.tiles + i) * k.rows) * k.C + c0;
+        return (n * k.P + (int64_t(chunk) * k.tiles + i) * k.rows) * k.C + c0;
     }
-    // how many of the V elements exist in tile i of chunk q
-    __device__ __forceinline__ int valid(const OneCut &k, int q, int i) const
+    // how many of the V elements exist in tile i
+    __device__ __forceinline__ int valid(const Cut &k, int i) const
     {
-        const int64_t left = k.P - (int64_t(q) * k.tiles + i) * k.rows;
-        const int there = i >= k.tiles || left <= 0 ? 0 : int(left < k.rows ? left : k.rows) * k.width;
+        const int64_t left = k.P - (int64_t(chunk) * k.tiles + i) * k.rows;
+        const int there = i >= k.tiles || left <= 0 ? 0 : int(left < k.rows ? left : k.rows) * width;
         const int mine = active ? there - e : 0;
         return mine >= V ? V : mine > 0 ? mine : 0;
     }
-    // all tiles of chunk q hold all their positions
-    __device__ __forceinline__ bool full(const OneCut &k, int q) const
+    // tiles first .. first + count - 1 exist and hold all their positions
+    __device__ __forceinline__ bool full(const Cut &k, int first, int count) const
     {
-        return (int64_t(q) + 1) * k.tiles * k.rows <= k.P;
+        return first + count <= k.tiles && (int64_t(chunk) * k.tiles + first + count) * k.rows <= k.P;
+    }
+    // Calls f(j, channel of the slab, group of the slab) for the thread's V elements; with UNI
+    // the group is the first's.
+    template <bool UNI, class F>
+    __device__ __forceinline__ void each(const Cut &k, F f) const
+    {
+        int c = col, g = k.split > 1 ? 0 : col / k.Cg, left = k.split > 1 ? width : (g + 1) * k.Cg - col;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            f(j, c, g);
+            if (UNI) {
+                ++c;
+                continue;
+            }
+            ++c;
+            if (--left == 0) {
+                ++g;
+                left = k.Cg;
+            }
+            if (c == width) {
+                c = 0;
+                g = 0;
+                left = k.Cg;
+            }
+        }
+    }
+    // The parameter's values of the thread's channels.
+    template <bool UNI, class T>
+    __device__ __forceinline__ void params(float (&out)[V], const Cut &k, const Param<T> &p, float absent) const
+    {
+        if (UNI || width % V == 0) p.template run<V>(out, c0 + col, absent);
+        else each<UNI>(k, [&](int j, int c, int) { out[j] = p.at(c0 + c, absent); });
     }
 };
 
 // UNI: a vector lies inside one group, so the thread keeps one triple for all its values.
 template <bool UNI, int V>
 constexpr int kOwn = UNI ? 1 : V;
-
-// 16 bytes of elements as registers.
+template <bool UNI, int V>
+using OwnMoments = Moments[kOwn<UNI, V>];
+template <bool UNI, int V>
+using OwnFloats = float[kOwn<UNI, V>];
+template <int THREADS, bool UNI, int V>
+using JoinBuffer = float[3][THREADS * kOwn<UNI, V>];
+// A vector as registers: 16 bytes, or a single element.
 using Bits = unsigned __attribute__((ext_vector_type(4)));
+template <int V>
+using Held = std::conditional_t<V == 1, unsigned, Bits>;
+template <class T, int V>
+__device__ __forceinline__ Held<V> hold(const Raw<T, V> &r)
+{
+    Held<V> b{};
+    __builtin_memcpy(&b, &r, sizeof(T) * V);
+    return b;
+}
 // Held registers as a new value: what was computed from them before is computed again
 // after this, and what is computed from them after is not begun before.  Without it the
 // compiler unpacks all held vectors at once, or keeps them unpacked, and spills them.
-template <class T>
-__device__ __forceinline__ Raw<T, ct::kVec<T>> held(Bits &b)
+template <class T, int V>
+__device__ __forceinline__ Raw<T, V> held(Held<V> &b)
 {
     asm volatile("" : "+v"(b));
-    return __builtin_bit_cast(Raw<T, ct::kVec<T>>, b);
+    Raw<T, V> r;
+    __builtin_memcpy(&r, &b, sizeof(T) * V);
+    return r;
 }
 
 // Keeps the compiler from working on several tiles at a time, whose temporaries would not
 // fit the registers; other waves fill the gaps.
 __device__ __forceinline__ void one_by_one() { __builtin_amdgcn_sched_barrier(0); }
 
-// Waits until every chunk's words of the block's groups are there.  use(g, complete word of
-// chunk q, q) sees them in a fixed order per lane, after begin(g) and before end(g); what
-// they made of an incomplete look is thrown away.  make(q) publishes chunk q from memory.
-template <int THREADS, class Begin, class Use, class End, class Make>
-__device__ __forceinline__ void gather_words(const OneCut &k, const unsigned long long *words, Begin begin, Use use, End end,
-                                             Make make)
+// The thread's moments over `tiles` tiles, updated tile by tile: get(i) is tile i's vector,
+// valid(i) how much of it exists.  An element that exists in a tile exists in all tiles
+// before, so the counts are known constants where the loop is unrolled.
+template <class T, int V, bool UNI, int UNROLL, class Get, class Valid>
+__device__ __forceinline__ void own_moments(OwnMoments<UNI, V> &m, const OwnFloats<UNI, V> &pivot, int tiles, Get get,
+                                            Valid valid)
 {
-    const int lane = threadIdx.x & (k.lanes - 1);
-    for (int looks = 0;; ++looks) {
-        bool missing = false;
-        for (int g = int(threadIdx.x) / k.lanes; g < k.groups; g += THREADS / k.lanes) {
-            begin(g);
-            for (int q = lane; q < k.chunks; q += k.lanes) {
-                const unsigned long long w = look(words + int64_t(g) * k.chunks + q);
-                missing |= w == kEmpty;
-                use(g, w, q);
+#pragma unroll UNROLL
+    for (int i = 0; i < tiles; ++i) {
+        const int w = valid(i);
+        const Raw<T, V> r = get(i);
+        if (UNI) {  // all of the vector or nothing of it: its own moments, then joined
+            float v[V], sum = 0.0f, m2 = 0.0f;
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                v[j] = float(r[j]) - pivot[0];
+                sum += v[j];
             }
-            end(g, lane);
+            const float mean = sum * (1.0f / V);
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const float d = v[j] - mean;
+                m2 = __builtin_fmaf(d, d, m2);
+            }
+            const float share = 1.0f / float(i + 1), d = mean - m[0].mean;
+            if (w) {
+                m[0].n = float(V * (i + 1));
+                m[0].mean = __builtin_fmaf(d, share, m[0].mean);
+                m[0].m2 += __builtin_fmaf(d * d, float(V * i) * share, m2);
+            }
+        } else {  // one value of each channel
+            const float share = 1.0f / float(i + 1);
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const int a = UNI ? 0 : j;
+                const float v = float(r[j]) - pivot[a], d = v - m[a].mean;
+                const float mean = __builtin_fmaf(d, share, m[a].mean);
+                m[a].m2 = j < w ? __builtin_fmaf(d, v - mean, m[a].m2) : m[a].m2;
+                m[a].mean = j < w ? mean : m[a].mean;
+                m[a].n = j < w ? float(i + 1) : m[a].n;
+            }
         }
-        // (the second test is never met: the words made below are all there at the next look)
-        if (!__syncthreads_or(missing) || looks > k.limit + 8) return;
-        if (looks < k.limit) {
-            __builtin_amdgcn_s_sleep(8);
-            continue;
-        }
-        for (int q = 0; q < k.chunks; ++q) {
-            bool gone = false;
-            for (int g = threadIdx.x; g < k.groups; g += THREADS) gone |= look(words + int64_t(g) * k.chunks + q) == kEmpty;
-            if (__syncthreads_or(gone)) make(q);
-        }
-        __threadfence();  // the words made here have arrived before anybody looks again
-        __syncthreads();
     }
 }
 
-// Which elements of the thread's K vectors stay, V bits a vector, four vectors a word.  The
-// words' loops are not unrolled further: sixteen copies of the generator are slower to fetch
-// than to run.
-template <int V, int K, class First>
-__device__ __forceinline__ void draw(unsigned (&keep)[K / 4], const Dropout &drop, First first)
+// K tiles from `first` on as registers.
+template <class T, int K, int V>
+__device__ __forceinline__ void load_tiles(Held<V> (&raw)[K], const T *x, const Cut &k, const Place<V> &pl, int first)
 {
+    if (pl.full(k, first, K)) {
 #pragma unroll
-    for (int w = 0; w < K / 4; ++w) keep[w] = ~0u;
-    if (!drop.threshold) return;
-    const uint64_t counter = drop.counter();
+        for (int i = 0; i < K; ++i) raw[i] = hold<T, V>(*reinterpret_cast<const Raw<T, V> *>(x + pl.tile(k, first + i) + pl.off));
+    } else {
 #pragma unroll
-    for (int w = 0; w < K / 4; ++w) {
-        unsigned bits = 0;
-#pragma unroll 1
-        for (int i = 0; i < 4; ++i)
-            bits |= (keep_bits<V>(drop, counter, uint64_t(first(4 * w + i))) & ((1u << V) - 1)) << (8 * i);
-        keep[w] = bits;
+        for (int i = 0; i < K; ++i)
+            raw[i] = hold<T, V>(load_first<T, V>(x + pl.tile(k, first + i) + pl.off, pl.valid(k, first + i)));
     }
 }
-__device__ __forceinline__ bool stays(const unsigned *keep, int i, int j) { return (keep[i / 4] >> (8 * (i % 4) + j)) & 1; }
 
-// Calls launch(vector inside a group?, tiles held) with the instance for the cut.
-template <bool BACKWARD, class F>
-void with_instance(const OneCut &k, bool uni, F &&launch)
+// ------------------------------------------------------------------------------------
+// A call and its plan
+// ------------------------------------------------------------------------------------
+// A call of either direction (dy, dx, dgamma and dbeta: the gradient).
+struct Call {
+    int64_t N = 0;
+    int dt = CT_FLOAT32;
+    bool params_f32 = true;
+    const void *x = nullptr, *dy = nullptr, *gamma = nullptr, *beta = nullptr;
+    void *y = nullptr, *dx = nullptr, *dgamma = nullptr, *dbeta = nullptr;
+    float eps = 0.0f;
+    float *mean = nullptr, *rstd = nullptr;
+    Act act;
+    Dropout drop;
+};
+
+// Threads of a block and tiles held at once.  Statistics: 512 threads of 128 registers, 64 of
+// which hold 16 vectors, so a compute unit has 256 KB of x on its way.  `one`: the kernels
+// in which a block has all positions of its groups.
+constexpr int kStatThreads = 512, kStatTiles = 16;
+constexpr int kApplyThreads = 256, kApplyTiles = 4;
+constexpr int kOneThreads = 512, kOneShort = 4;
+constexpr int one_tiles(bool uni) { return uni ? 16 : 8; }
+constexpr int kGradThreads = 256, kGradTiles = 4;
+constexpr int kOneGradThreads = 256;
+constexpr int one_grad_tiles(int V) { return V == 8 ? 12 : 16; }
+
+struct Plan {
+    bool vec = true;   // 16-byte vectors, else single elements
+    bool uni = true;   // every vector lies inside one group
+    bool one = false;  // a block has all positions of its groups: one kernel
+    bool finish = false;  // many parts a group: a kernel joins them before the second pass
+    Cut s, a;          // the pass for the statistics, the pass that writes (or the only one)
+    // places in the workspace (bytes)
+    size_t part = 0, pivot = 0, stats = 0, sums = 0, bytes = 0;
+};
+
+void launch_forward(const Call &c, const Plan &p, char *ws, hipStream_t st);
+void launch_gradient(const Call &c, const Plan &p, char *ws, hipStream_t st);
+void launch_no_gradient(int dt, bool params_f32, int C, void *dgamma, void *dbeta, hipStream_t st);  // zeros
+
+// Calls f(vector width, vector inside a group?) with the instance for the plan.
+template <class T, class F>
+void with_vector(const Plan &p, F &&f)
 {
     constexpr std::true_type yes{};
     constexpr std::false_type no{};
-    if (uni && k.tiles <= kSmallHeld) launch(yes, std::integral_constant<int, kSmallHeld>{});
-    else if (uni) launch(yes, std::integral_constant<int, held_tiles(true, BACKWARD)>{});
-    else if (k.tiles <= kSmallHeld) launch(no, std::integral_constant<int, kSmallHeld>{});
-    else launch(no, std::integral_constant<int, held_tiles(false, BACKWARD)>{});
+    if (!p.vec) f(std::integral_constant<int, 1>{}, yes);
+    else if (p.uni) f(std::integral_constant<int, kVec<T>>{}, yes);
+    else f(std::integral_constant<int, kVec<T>>{}, no);
 }
 
 }  // namespace norm

@@ -1,0 +1,307 @@
+// ct_groupnorm_fwd.hip -- the kernels of group norm with an activation and dropout (what they
+// share is in ct_groupnorm.hpp, the entry points are in ct_groupnorm.hip).
+#include <hip/hip_runtime.h>
+
+#include <type_traits>
+
+#include "ct_groupnorm.hpp"
+
+namespace {
+
+using namespace ct::norm;
+using ct::Dropout;
+using ct::Raw;
+
+// What a group's moments are relative to: its first value.
+template <class T>
+__device__ __forceinline__ float pivot_of(const T *x, const Cut &k, int64_t n, int g)
+{
+    return float(x[n * k.P * k.C + int64_t(g) * k.Cg]);
+}
+
+// Joins the block's triples of each group of the slab and calls out(group of the slab,
+// moments), on one thread a group.
+template <int THREADS, int V, bool UNI, class Out>
+__device__ __forceinline__ void join_block(const Cut &k, const Place<V> &pl, const OwnMoments<UNI, V> &m,
+                                           JoinBuffer<THREADS, UNI, V> &lds, Out out)
+{
+    constexpr int A = kOwn<UNI, V>, unit = UNI ? V : 1;  // elements a triple stands for
+    if (pl.active) {
+#pragma unroll
+        for (int a = 0; a < A; ++a) {
+            lds[0][threadIdx.x * A + a] = m[a].n;
+            lds[1][threadIdx.x * A + a] = m[a].mean;
+            lds[2][threadIdx.x * A + a] = m[a].m2;
+        }
+    }
+    __syncthreads();
+    const int per = (k.split > 1 ? pl.width : k.Cg) / unit, row = pl.width / unit, lane = threadIdx.x & (k.lanes - 1);
+    for (int g = int(threadIdx.x) / k.lanes; g < pl.groups; g += THREADS / k.lanes) {
+        Moments s;
+        for (int i = lane; i < per * k.rows; i += k.lanes) {
+            const int r = i / per, at = r * row + g * per + (i - r * per);
+            s.join(lds[0][at], lds[1][at], lds[2][at]);
+        }
+        for (int o = 1; o < k.lanes; o *= 2) s.join(__shfl_xor(s.n, o), __shfl_xor(s.mean, o), __shfl_xor(s.m2, o));
+        if (lane == 0) out(g, s);
+    }
+}
+
+template <class T, int V, bool UNI>
+__device__ __forceinline__ void load_pivots(OwnFloats<UNI, V> &pivot, const T *x, const Cut &k, const Place<V> &pl)
+{
+    pl.template each<UNI>(k, [&](int j, int, int g) {
+        if (j < kOwn<UNI, V>) pivot[j] = pivot_of(x, k, pl.n, pl.g0 + g);
+    });
+}
+
+// y of one tile from its x.
+template <class T, int V, bool UNI, class ACT>
+__device__ __forceinline__ Raw<T, V> outputs(const Raw<T, V> &v, const OwnFloats<UNI, V> &mu, const float (&a)[V],
+                                             const float (&be)[V], const ACT &f, const Dropout &drop, uint64_t counter,
+                                             int64_t first)
+{
+    Raw<T, V> o;
+    float r[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) r[j] = f.y(__builtin_fmaf(float(v[j]) - mu[UNI ? 0 : j], a[j], be[j]));
+    if (drop.threshold) {
+        const ct::Fields keep = ct::draw_fields<V, UNI && V != 1>(drop, counter, uint64_t(first));
+#pragma unroll
+        for (int j = 0; j < V; ++j) r[j] = keep.stays(j, drop.limit()) ? r[j] * drop.factor : 0.0f;
+    }
+#pragma unroll
+    for (int j = 0; j < V; ++j) o[j] = T(r[j]);
+    return o;
+}
+
+// The constants of a thread's channels, z = (x - mu) a + be, from a = gamma and the groups'
+// statistics.
+template <int V, bool UNI>
+__device__ __forceinline__ void channel_constants(OwnFloats<UNI, V> &mu, float (&a)[V], const Cut &k, const Place<V> &pl,
+                                                  const float2 *stat)
+{
+    float rs[kOwn<UNI, V>];
+    pl.template each<UNI>(k, [&](int j, int, int g) {
+        if (j >= kOwn<UNI, V>) return;
+        const float2 v = stat[g];
+        mu[j] = v.x;
+        rs[j] = v.y;
+    });
+#pragma unroll
+    for (int j = 0; j < V; ++j) a[j] *= rs[UNI ? 0 : j];
+}
+
+// One block has all positions of its groups: x is read once and held in registers.
+template <class T, int V, bool UNI, int K, class ACT>
+__global__ __launch_bounds__(kOneThreads, 4) void one_kernel(const T *x, Cut k, float eps, ct::Param<T> gamma,
+                                                             ct::Param<T> beta, ACT f, Dropout drop, T *y, float *mean,
+                                                             float *rstd)
+{
+    constexpr int A = kOwn<UNI, V>;
+    __shared__ float lds[3][kOneThreads * A];
+    __shared__ float2 stat[kMostGroups];
+    const Place<V> pl(k, blockIdx.x);
+    Held<V> raw[K];
+    load_tiles<T, K, V>(raw, x, k, pl, 0);
+    const bool full = pl.full(k, 0, K);
+    float pivot[A], a[V], be[V];
+    load_pivots<T, V, UNI>(pivot, x, k, pl);
+    pl.template params<UNI>(a, k, gamma, 1.0f);
+    pl.template params<UNI>(be, k, beta, 0.0f);
+    Moments m[A];
+    own_moments<T, V, UNI, K>(m, pivot, K, [&](int i) { return held<T, V>(raw[i]); },
+                              [&](int i) { return full ? (pl.active ? V : 0) : pl.valid(k, i); });
+    join_block<kOneThreads, V, UNI>(k, pl, m, lds, [&](int g, const Moments &s) {
+        const float mu = pivot_of(x, k, pl.n, pl.g0 + g) + s.mean, r = 1.0f / sqrtf(s.m2 / s.n + eps);
+        stat[g] = make_float2(mu, r);
+        const int64_t at = pl.n * k.G + pl.g0 + g;
+        if (mean) mean[at] = mu;
+        if (rstd) rstd[at] = r;
+    });
+    __syncthreads();
+    if (!pl.active) return;
+    float mu[A];
+    channel_constants<V, UNI>(mu, a, k, pl, stat);
+    const uint64_t counter = drop.threshold ? drop.counter() : 0;
+#pragma unroll
+    for (int i = 0; i < K; ++i) {
+        const int valid = full ? V : pl.valid(k, i);
+        if (valid == 0) continue;
+        const int64_t at = pl.tile(k, i) + pl.off;
+        store_first<T, V>(y + at, outputs<T, V, UNI>(held<T, V>(raw[i]), mu, a, be, f, drop, counter, at), valid);
+        one_by_one();
+    }
+}
+
+// part[n][g][chunk][slab of the group] = (mean relative to the pivot, m2); the counts follow
+// from the cut.  The pivots are written down too: a call in place overwrites the values.
+template <class T, int V, bool UNI>
+__global__ __launch_bounds__(kStatThreads, 4) void stats_kernel(const T *x, Cut k, float2 *part, float *pivots)
+{
+    constexpr int A = kOwn<UNI, V>, K = kStatTiles;
+    __shared__ float lds[3][kStatThreads * A];
+    const Place<V> pl(k, blockIdx.x);
+    float pivot[A];
+    load_pivots<T, V, UNI>(pivot, x, k, pl);
+    Moments m[A];
+    for (int first = 0; first < k.tiles; first += K) {
+        Held<V> raw[K];
+        load_tiles<T, K, V>(raw, x, k, pl, first);
+        const bool full = pl.full(k, first, K);
+        Moments t[A];
+        own_moments<T, V, UNI, K>(t, pivot, K, [&](int i) { return held<T, V>(raw[i]); },
+                                  [&](int i) { return full ? (pl.active ? V : 0) : pl.valid(k, first + i); });
+#pragma unroll
+        for (int a = 0; a < A; ++a) m[a].join(t[a].n, t[a].mean, t[a].m2);
+    }
+    join_block<kStatThreads, V, UNI>(k, pl, m, lds, [&](int g, const Moments &s) {
+        const int64_t group = pl.n * k.G + pl.g0 + g;
+        part[(group * k.chunks + pl.chunk) * k.split + pl.sub] = make_float2(s.mean, s.m2);
+        if (pl.chunk == 0 && pl.sub == 0) pivots[group] = pivot_of(x, k, pl.n, pl.g0 + g);
+    });
+}
+
+// Joins the parts of one group, `lanes` threads together; the moments on every one of them.
+__device__ __forceinline__ Moments join_parts(const float2 *part, const Cut &s, int64_t group, int lane, int lanes)
+{
+    constexpr int kAtOnce = 4;
+    const float2 *p = part + group * s.chunks * s.split;
+    const int count = s.chunks * s.split;
+    Moments m;
+    for (int q = lane; q < count; q += kAtOnce * lanes) {
+        float2 v[kAtOnce];
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j) v[j] = p[q + j * lanes < count ? q + j * lanes : q];
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j) {
+            const int at = q + j * lanes;
+            if (at >= count) break;
+            const int chunk = at / s.split, sub = at - chunk * s.split;
+            const int64_t left = s.P - chunk * s.span();
+            const int channels = s.split == 1 ? s.Cg : s.Cg - sub * s.width < s.width ? s.Cg - sub * s.width : s.width;
+            m.join(float(channels) * float(left < s.span() ? left : s.span()), v[j].x, v[j].y);
+        }
+    }
+    for (int o = 1; o < lanes; o *= 2) m.join(__shfl_xor(m.n, o), __shfl_xor(m.mean, o), __shfl_xor(m.m2, o));
+    return m;
+}
+
+// mean and rstd of every group, one wave a group.
+__global__ __launch_bounds__(256) void finish_kernel(const float2 *part, const float *pivots, Cut s, int64_t groups, float eps,
+                                                     float *mean, float *rstd)
+{
+    const int64_t g = (int64_t(blockIdx.x) * 256 + threadIdx.x) / 64;
+    if (g >= groups) return;
+    const Moments m = join_parts(part, s, g, threadIdx.x & 63, 64);
+    if ((threadIdx.x & 63) == 0) {
+        mean[g] = pivots[g] + m.mean;
+        rstd[g] = 1.0f / sqrtf(m.m2 / m.n + eps);
+    }
+}
+
+// The second pass.  finished: mean and rstd are there; else every block joins the parts of its
+// groups while its values are on their way, and the first chunk's blocks write them down.
+template <class T, int V, bool UNI, class ACT>
+__global__ __launch_bounds__(kApplyThreads, 4) void apply_kernel(const T *x, Cut k, Cut s, const float2 *part,
+                                                                 const float *pivots, bool finished, float eps,
+                                                                 ct::Param<T> gamma, ct::Param<T> beta, ACT f, Dropout drop,
+                                                                 T *y, float *mean, float *rstd)
+{
+    constexpr int A = kOwn<UNI, V>, K = kApplyTiles;
+    __shared__ float2 stat[kMostGroups];
+    const Place<V> pl(k, blockIdx.x);
+    Held<V> raw[K];
+    load_tiles<T, K, V>(raw, x, k, pl, 0);
+    float a[V], be[V];
+    pl.template params<UNI>(a, k, gamma, 1.0f);
+    pl.template params<UNI>(be, k, beta, 0.0f);
+    if (finished) {
+        for (int g = threadIdx.x; g < pl.groups; g += kApplyThreads) {
+            const int64_t at = pl.n * k.G + pl.g0 + g;
+            stat[g] = make_float2(mean[at], rstd[at]);
+        }
+    } else {
+        const int lane = threadIdx.x & (k.lanes - 1);
+        for (int g = int(threadIdx.x) / k.lanes; g < pl.groups; g += kApplyThreads / k.lanes) {
+            const int64_t group = pl.n * k.G + pl.g0 + g;
+            const Moments m = join_parts(part, s, group, lane, k.lanes);
+            if (lane == 0) {
+                const float mu = pivots[group] + m.mean, r = 1.0f / sqrtf(m.m2 / m.n + eps);
+                stat[g] = make_float2(mu, r);
+                if (pl.chunk == 0 && pl.sub == 0) {
+                    if (mean) mean[group] = mu;
+                    if (rstd) rstd[group] = r;
+                }
+            }
+        }
+    }
+    __syncthreads();
+    if (!pl.active) return;
+    float mu[A];
+    channel_constants<V, UNI>(mu, a, k, pl, stat);
+    const uint64_t counter = drop.threshold ? drop.counter() : 0;
+    for (int first = 0;;) {
+#pragma unroll
+        for (int i = 0; i < K; ++i) {
+            const int valid = pl.valid(k, first + i);
+            if (valid == 0) continue;
+            const int64_t at = pl.tile(k, first + i) + pl.off;
+            store_first<T, V>(y + at, outputs<T, V, UNI>(held<T, V>(raw[i]), mu, a, be, f, drop, counter, at), valid);
+        }
+        first += K;
+        if (first >= k.tiles) break;
+        load_tiles<T, K, V>(raw, x, k, pl, first);
+    }
+}
+
+}  // namespace
+
+void ct::norm::launch_forward(const Call &c, const Plan &p, char *ws, hipStream_t st)
+{
+    float2 *const part = reinterpret_cast<float2 *>(ws + p.part);
+    float *const pivots = reinterpret_cast<float *>(ws + p.pivot);
+    float *const stats = reinterpret_cast<float *>(ws + p.stats);
+    const int64_t groups = c.N * p.a.G, blocks = c.N * p.a.chunks * p.a.slabs;
+    with_type(c.dt, [&](auto t) {
+        using T = decltype(t);
+        const T *const x = static_cast<const T *>(c.x);
+        T *const y = static_cast<T *>(c.y);
+        const Param<T> gamma{c.gamma, c.params_f32}, beta{c.beta, c.params_f32};
+        if (p.one) {
+            with_act(c.act, [&](auto f) {
+                auto go = [&](auto uni, auto tiles) {
+                    one_kernel<T, kVec<T>, decltype(uni)::value, decltype(tiles)::value, decltype(f)>
+                        <<<unsigned(blocks), kOneThreads, 0, st>>>(x, p.a, c.eps, gamma, beta, f, c.drop, y, c.mean, c.rstd);
+                };
+                constexpr std::true_type yes{};
+                constexpr std::false_type no{};
+                mark_before(st);
+                if (p.uni && p.a.tiles <= kOneShort) go(yes, std::integral_constant<int, kOneShort>{});
+                else if (p.uni) go(yes, std::integral_constant<int, one_tiles(true)>{});
+                else if (p.a.tiles <= kOneShort) go(no, std::integral_constant<int, kOneShort>{});
+                else go(no, std::integral_constant<int, one_tiles(false)>{});
+                mark_after(st);
+            });
+            return;
+        }
+        with_vector<T>(p, [&](auto v, auto uni) {
+            constexpr int V = decltype(v)::value;
+            constexpr bool UNI = decltype(uni)::value;
+            stats_kernel<T, V, UNI><<<unsigned(c.N * p.s.chunks * p.s.slabs), kStatThreads, 0, st>>>(x, p.s, part, pivots);
+            float *mean = c.mean, *rstd = c.rstd;
+            if (p.finish) {
+                if (!mean) mean = stats;
+                if (!rstd) rstd = stats + groups;
+                finish_kernel<<<unsigned((groups + 3) / 4), 256, 0, st>>>(part, pivots, p.s, groups, c.eps, mean, rstd);
+            }
+            mark_before(st);
+            with_act(c.act, [&](auto f) {
+                using F = decltype(f);
+                apply_kernel<T, V, UNI, F><<<unsigned(blocks), kApplyThreads, 0, st>>>(
+                    x, p.a, p.s, part, pivots, p.finish, c.eps, gamma, beta, f, c.drop, y, mean, rstd);
+            });
+            mark_after(st);
+        });
+    });
+}

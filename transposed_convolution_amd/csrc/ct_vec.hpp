@@ -89,6 +89,24 @@ struct Param {
         if (!p) return absent;
         return f32 ? static_cast<const float *>(p)[i] : float(static_cast<const T *>(p)[i]);
     }
+    // V consecutive values: one choice of type and one wide load, where V calls of at() would
+    // be V branches with a wait in each.
+    template <int V>
+    __device__ __forceinline__ void run(float (&out)[V], int64_t i, float absent) const
+    {
+        if (!p) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) out[j] = absent;
+        } else if (f32) {
+            const Raw<float, V> r = *reinterpret_cast<const Raw<float, V> *>(static_cast<const float *>(p) + i);
+#pragma unroll
+            for (int j = 0; j < V; ++j) out[j] = r[j];
+        } else {
+            const Raw<T, V> r = *reinterpret_cast<const Raw<T, V> *>(static_cast<const T *>(p) + i);
+#pragma unroll
+            for (int j = 0; j < V; ++j) out[j] = float(r[j]);
+        }
+    }
 };
 
 // ------------------------------------------------------------------------------------
@@ -107,6 +125,7 @@ struct Dropout {
     float factor = 1.0f;             // 0 when everything is dropped
     uint64_t seed = 0, offset = 0;
     const uint64_t *step = nullptr;  // device value added to offset when the kernel runs
+    __device__ __forceinline__ uint32_t limit() const { return threshold - 1; }  // with dropout only
     __device__ __forceinline__ uint64_t counter() const { return step ? offset + *step : offset; }
 };
 
@@ -150,29 +169,46 @@ __device__ __forceinline__ void philox(uint64_t block, uint64_t offset, uint64_t
     w[3] = c3;
 }
 
-// The eight elements of block `block`: bit j set when element 8 * block + j stays.
-__device__ __forceinline__ unsigned keep8(const Dropout &d, uint64_t counter, uint64_t block)
-{
+// The fields of V elements, in the places the generator's words have them: element j is
+// field j.  It stays when its field is above `limit` = threshold - 1, which fits 16 bits, so
+// a low half is compared as it stands and a high half by the whole word.
+struct Fields {
     uint32_t w[4];
-    philox(block, counter, d.seed, w);
-    unsigned m = 0;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const uint32_t field = (j & 1) ? w[j >> 1] >> 16 : w[j >> 1] & 0xffffu;
-        m |= (field >= d.threshold ? 1u : 0u) << j;
+    __device__ __forceinline__ bool stays(int j, uint32_t limit) const
+    {
+        return j & 1 ? w[j >> 1] > (limit << 16 | 0xffffu) : uint16_t(w[j >> 1]) > uint16_t(limit);
     }
-    return m;
-}
+};
 
-// Elements first .. first + V - 1: bit j set when element first + j stays.
-template <int V>
-__device__ __forceinline__ unsigned keep_bits(const Dropout &d, uint64_t counter, uint64_t first)
+// The fields of elements first .. first + V - 1; ALIGNED: first is known to be a multiple of V.
+template <int V, bool ALIGNED>
+__device__ __forceinline__ Fields draw_fields(const Dropout &d, uint64_t counter, uint64_t first)
 {
     static_assert(V <= 8, "at most two blocks are looked at");
+    Fields f;
+    philox(first >> 3, counter, d.seed, f.w);
     const int sh = int(first & 7);
-    unsigned m = keep8(d, counter, first >> 3) >> sh;
-    if (sh + V > 8) m |= keep8(d, counter, (first >> 3) + 1) << (8 - sh);
-    return m;
+    if (V == 4) {
+        f.w[0] = sh == 4 ? f.w[2] : f.w[0];
+        f.w[1] = sh == 4 ? f.w[3] : f.w[1];
+    }
+    if (ALIGNED || sh == 0 || (V == 4 && sh == 4)) return f;
+    // a vector that starts inside a block: field sh + j, of this block or the next
+    Fields next = f, out;
+    if (sh + V > 8) philox((first >> 3) + 1, counter, d.seed, next.w);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) out.w[j] = 0;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+#pragma unroll
+        for (int s = 1; s < 8; ++s) {
+            const int at = s + j;
+            const uint32_t word = at < 8 ? f.w[(at & 7) >> 1] : next.w[(at & 7) >> 1];
+            const uint32_t field = at & 1 ? word >> 16 : word & 0xffffu;
+            out.w[j >> 1] |= s == sh ? field << (16 * (j & 1)) : 0u;
+        }
+    }
+    return out;
 }
 
 }  // namespace ct
