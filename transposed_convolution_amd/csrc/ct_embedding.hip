@@ -19,6 +19,15 @@ using ct::Raw;
 constexpr int kThreads = 256;
 constexpr int kWave = 64;
 
+template <int V>
+__device__ __forceinline__ Raw<float, V> as_floats(const float (&a)[V])
+{
+    Raw<float, V> r;
+#pragma unroll
+    for (int j = 0; j < V; ++j) r[j] = a[j];
+    return r;
+}
+
 // A row of `width` elements as whole vectors and then single elements: slot s < full is
 // vector s, the others are elements full * V + (s - full).
 struct RowSlots {
@@ -114,6 +123,25 @@ __device__ __forceinline__ void wave_fence()
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 }
 
+// Where the lane's token goes: the next place of its digit after the lanes before it with the
+// same digit.  off[digit] is the wave's next place of each digit and moves on.
+__device__ __forceinline__ uint32_t place_in_order(uint32_t *off, uint32_t digit, bool in, int lane)
+{
+    unsigned long long same = __ballot(in);
+#pragma unroll
+    for (int bit = 0; bit < 8; ++bit) {
+        const unsigned long long set = __ballot((digit >> bit) & 1);
+        same &= (digit >> bit) & 1 ? set : ~set;
+    }
+    const int rank = __popcll(same & ((1ull << lane) - 1));
+    uint32_t at = 0;
+    if (in) at = off[digit] + uint32_t(rank);
+    wave_fence();
+    if (in && rank == 0) off[digit] += uint32_t(__popcll(same));
+    wave_fence();
+    return at;
+}
+
 template <class I>
 __global__ __launch_bounds__(kThreads) void scatter_kernel(Source<I> src, int64_t count, int per_block, int shift,
                                                            const uint32_t *hist, uint32_t *keys_out, uint32_t *toks_out)
@@ -124,6 +152,7 @@ __global__ __launch_bounds__(kThreads) void scatter_kernel(Source<I> src, int64_
     const int d = threadIdx.x, lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
     // where this block's tokens of digit d start: all smaller digits, then d in earlier blocks
     uint32_t total = 0, before = 0;
+#pragma unroll 16
     for (int b = 0; b < int(gridDim.x); ++b) {
         const uint32_t v = hist[b * kDigits + d];
         before += b < int(blockIdx.x) ? v : 0u;
@@ -158,23 +187,91 @@ __global__ __launch_bounds__(kThreads) void scatter_kernel(Source<I> src, int64_
         const int64_t i = first + r + lane;
         const bool in = i < count;
         const uint32_t key = in ? src.key(i) : 0u;
-        const uint32_t digit = (key >> shift) & (kDigits - 1);
-        unsigned long long same = __ballot(in);
-#pragma unroll
-        for (int bit = 0; bit < 8; ++bit) {
-            const unsigned long long set = __ballot((digit >> bit) & 1);
-            same &= (digit >> bit) & 1 ? set : ~set;
-        }
-        const int rank = __popcll(same & ((1ull << lane) - 1));
-        uint32_t at = 0;
-        if (in) at = off[wave][digit] + uint32_t(rank);
-        wave_fence();
-        if (in && rank == 0) off[wave][digit] += uint32_t(__popcll(same));
-        wave_fence();
+        const uint32_t at = place_in_order(off[wave], (key >> shift) & (kDigits - 1), in, lane);
         if (in) {
             keys_out[at] = key;
             toks_out[at] = src.tok(i);
         }
+    }
+}
+
+// Where each row's tokens begin and end in the sorted order, written by the thread that sees
+// the border.  Rows without tokens are not written: who reads a row's begin looks whether
+// the row is there.
+struct Bounds {
+    uint32_t *begin, *end;
+    __device__ __forceinline__ void mark(const uint32_t *keys, int64_t i, int64_t count, int64_t rows) const
+    {
+        const uint32_t k = keys[i];
+        if (k >= uint32_t(rows)) return;
+        if (i == 0 || keys[i - 1] != k) begin[k] = uint32_t(i);
+        if (i + 1 == count || keys[i + 1] != k) end[k] = uint32_t(i + 1);
+    }
+};
+
+// Up to kOneSort tokens: the whole sort in one block's LDS, one launch instead of two a pass.
+constexpr int kOneSort = 4096, kSortThreads = 1024;
+template <class I>
+__global__ __launch_bounds__(kSortThreads) void one_sort_kernel(Source<I> src, int count, int passes, bool mark, Bounds bounds,
+                                                                uint32_t *keys_out, uint32_t *toks_out)
+{
+    constexpr int kWaves = kSortThreads / kWave;
+    __shared__ uint32_t keys[2][kOneSort], toks[2][kOneSort];
+    __shared__ uint32_t off[kWaves][kDigits], scan[kDigits];
+    const int t = threadIdx.x, lane = t & (kWave - 1), wave = t / kWave;
+    for (int i = t; i < count; i += kSortThreads) {
+        keys[0][i] = src.key(i);
+        toks[0][i] = uint32_t(i);
+    }
+    const int per_wave = (count + kWaves * kWave - 1) / (kWaves * kWave) * kWave;  // consecutive tokens of a wave
+    for (int p = 0; p < passes; ++p) {
+        const uint32_t *const key = keys[p & 1], *const tok = toks[p & 1];
+        uint32_t *const key_to = keys[1 - (p & 1)], *const tok_to = toks[1 - (p & 1)];
+        const int shift = 8 * p;
+        for (int i = t; i < kWaves * kDigits; i += kSortThreads) (&off[0][0])[i] = 0;
+        __syncthreads();
+        for (int r = 0; r < per_wave; r += kWave) {
+            const int i = wave * per_wave + r + lane;
+            if (i < count) atomicAdd(&off[wave][(key[i] >> shift) & (kDigits - 1)], 1u);
+        }
+        __syncthreads();
+        uint32_t total = 0;
+        if (t < kDigits) {
+            for (int w = 0; w < kWaves; ++w) total += off[w][t];
+            scan[t] = total;
+        }
+        __syncthreads();
+        for (int d = 1; d < kDigits; d *= 2) {
+            const uint32_t v = t < kDigits && t >= d ? scan[t - d] : 0u;
+            __syncthreads();
+            if (t < kDigits) scan[t] += v;
+            __syncthreads();
+        }
+        if (t < kDigits) {
+            uint32_t sum = scan[t] - total;
+            for (int w = 0; w < kWaves; ++w) {
+                const uint32_t v = off[w][t];
+                off[w][t] = sum;
+                sum += v;
+            }
+        }
+        __syncthreads();
+        for (int r = 0; r < per_wave; r += kWave) {
+            const int i = wave * per_wave + r + lane;
+            const bool in = i < count;
+            const uint32_t k = in ? key[i] : 0u;
+            const uint32_t at = place_in_order(off[wave], (k >> shift) & (kDigits - 1), in, lane);
+            if (in) {
+                key_to[at] = k;
+                tok_to[at] = tok[i];
+            }
+        }
+        __syncthreads();
+    }
+    for (int i = t; i < count; i += kSortThreads) {
+        keys_out[i] = keys[passes & 1][i];
+        toks_out[i] = toks[passes & 1][i];
+        if (mark) bounds.mark(keys[passes & 1], i, count, src.rows);
     }
 }
 
@@ -190,91 +287,199 @@ __device__ __forceinline__ int64_t lower_bound(const uint32_t *keys, int64_t cou
     return lo;
 }
 
-// Adds dy[toks[i]] for i in [begin, end) into acc, slot s of the row.
-template <class T, int V>
+// Adds dy[toks[i]] for i in [begin, end) into acc, slot s of the row: kAtOnce tokens' loads at
+// a time, added in order.
+template <int kAtOnce, class T, int V>
 __device__ __forceinline__ void add_rows(float (&acc)[V], const T *dy, const uint32_t *toks, int64_t begin, int64_t end,
                                          const RowSlots &rs, int64_t s)
 {
     if (s < rs.full) {
-#pragma unroll 4
-        for (int64_t i = begin; i < end; ++i) {
-            const Raw<T, V> v = *reinterpret_cast<const Raw<T, V> *>(dy + int64_t(toks[i]) * rs.width + s * V);
+        const T *const src = dy + s * V;
+        int64_t i = begin;
+        for (; i + kAtOnce <= end; i += kAtOnce) {
+            uint32_t tok[kAtOnce];
+            Raw<T, V> v[kAtOnce];
 #pragma unroll
-            for (int j = 0; j < V; ++j) acc[j] += float(v[j]);
+            for (int q = 0; q < kAtOnce; ++q) tok[q] = toks[i + q];
+#pragma unroll
+            for (int q = 0; q < kAtOnce; ++q) v[q] = *reinterpret_cast<const Raw<T, V> *>(src + int64_t(tok[q]) * rs.width);
+#pragma unroll
+            for (int q = 0; q < kAtOnce; ++q)
+#pragma unroll
+                for (int j = 0; j < V; ++j) acc[j] += float(v[q][j]);
+        }
+        if (i < end) {  // the rest together too: what is past the end is the last token, not added
+            uint32_t tok[kAtOnce];
+            Raw<T, V> v[kAtOnce];
+#pragma unroll
+            for (int q = 0; q < kAtOnce; ++q) tok[q] = toks[i + q < end ? i + q : end - 1];
+#pragma unroll
+            for (int q = 0; q < kAtOnce; ++q)
+                if (q == 0 || i + q < end) v[q] = *reinterpret_cast<const Raw<T, V> *>(src + int64_t(tok[q]) * rs.width);
+#pragma unroll
+            for (int q = 0; q < kAtOnce; ++q)
+#pragma unroll
+                for (int j = 0; j < V; ++j) acc[j] += i + q < end ? float(v[q][j]) : 0.0f;
         }
     } else {
         const int64_t e = rs.full * V + (s - rs.full);
+#pragma unroll 4
         for (int64_t i = begin; i < end; ++i) acc[0] += float(dy[int64_t(toks[i]) * rs.width + e]);
+    }
+}
+
+// Adds the partial sums of chunks from .. to - 1 of a row that begins in chunk `first`, there
+// in slot `head`, slot s of the row.
+template <int V>
+__device__ __forceinline__ void add_partials(float (&acc)[V], const float *partial, int from, int to, int first, int head,
+                                             const RowSlots &rs, int64_t s)
+{
+    const bool vec = s < rs.full;
+    const float *const src = partial + (vec ? s * V : rs.full * V + (s - rs.full));
+    if (vec) {
+#pragma unroll 4
+        for (int c = from; c < to; ++c) {
+            const Raw<float, V> p =
+                *reinterpret_cast<const Raw<float, V> *>(src + (int64_t(c) * 2 + (c == first ? head : 0)) * rs.width);
+#pragma unroll
+            for (int j = 0; j < V; ++j) acc[j] += p[j];
+        }
+    } else {
+#pragma unroll 4
+        for (int c = from; c < to; ++c) acc[0] += src[(int64_t(c) * 2 + (c == first ? head : 0)) * rs.width];
     }
 }
 
 // The sorted tokens in chunks: a row inside one chunk is summed by the kernel that writes
 // the rows; of a row that crosses a chunk's border every chunk makes a partial sum here,
-// slot 0 for the row at its start and slot 1 for the one at its end.
+// slot 0 for the row at its start and slot 1 for the one at its end.  The block's groups of
+// lanes take consecutive shares of the row's tokens, joined in their order.
 template <class T>
 __global__ __launch_bounds__(kThreads) void partial_kernel(const T *dy, const uint32_t *keys, const uint32_t *toks,
-                                                           int64_t count, int64_t rows, int chunk, RowSlots rs,
+                                                           int64_t count, int64_t rows, int chunk, RowSlots rs, Bounds bounds,
                                                            float *partial)
 {
     constexpr int V = ct::kVec<T>;
+    __shared__ float lds[kThreads * V];
     const int64_t a = int64_t(blockIdx.x) * chunk, b = a + chunk < count ? a + chunk : count;
+    for (int64_t i = a + threadIdx.x; i < b; i += kThreads) bounds.mark(keys, i, count, rows);
     const uint32_t first = keys[a], last = keys[b - 1];
-    const int per = kThreads / rs.lanes;  // 1 < rows of lanes: they share nothing, only the first works
-    if (int(threadIdx.x) / rs.lanes > 0 && per > 1) return;
-    const int lane = threadIdx.x & (rs.lanes - 1);
-    for (int slot = 0; slot < 2; ++slot) {
+    const int groups = kThreads / rs.lanes, group = threadIdx.x / rs.lanes, lane = threadIdx.x & (rs.lanes - 1);
+    for (int slot = 0; slot < 2; ++slot) {  // everything that steers here is the same on all threads
         const uint32_t key = slot ? last : first;
         if (key >= uint32_t(rows) || (slot && first == last)) continue;
+        const bool crosses = slot || first == last ? (b < count && keys[b] == key) || (!slot && a > 0 && keys[a - 1] == key)
+                                                   : a > 0 && keys[a - 1] == key;
+        if (!crosses) continue;
         const int64_t lo = slot ? a + lower_bound(keys + a, b - a, key) : a;
         const int64_t hi = slot ? b : a + lower_bound(keys + a, b - a, key + 1);
-        const bool crosses = (lo == a && a > 0 && keys[a - 1] == key) || (hi == b && b < count && keys[b] == key);
-        if (!crosses) continue;
-        float *out = partial + (int64_t(blockIdx.x) * 2 + slot) * rs.width;
-        for (int64_t s = lane; s < rs.slots; s += rs.lanes) {
+        const int64_t share = (hi - lo + groups - 1) / groups;
+        const int64_t from = lo + group * share < hi ? lo + group * share : hi, to = from + share < hi ? from + share : hi;
+        float *const out = partial + (int64_t(blockIdx.x) * 2 + slot) * rs.width;
+        for (int64_t s0 = 0; s0 < rs.slots; s0 += rs.lanes) {
+            const int64_t s = s0 + lane;
             float acc[V] = {};
-            add_rows<T, V>(acc, dy, toks, lo, hi, rs, s);
-            if (s < rs.full) {
-                for (int j = 0; j < V; ++j) out[s * V + j] = acc[j];
-            } else {
-                out[rs.full * V + (s - rs.full)] = acc[0];
+            if (s < rs.slots && from < to) add_rows<8, T, V>(acc, dy, toks, from, to, rs, s);
+            __syncthreads();
+#pragma unroll
+            for (int j = 0; j < V; ++j) lds[threadIdx.x * V + j] = acc[j];
+            __syncthreads();
+            if (group == 0 && s < rs.slots) {
+                for (int g = 1; g < groups; ++g)
+#pragma unroll
+                    for (int j = 0; j < V; ++j) acc[j] += lds[(g * rs.lanes + lane) * V + j];
+                if (s < rs.full) {
+                    *reinterpret_cast<Raw<float, V> *>(out + s * V) = as_floats(acc);
+                } else {
+                    out[rs.full * V + (s - rs.full)] = acc[0];
+                }
             }
         }
     }
 }
 
+// Stores slot s of a table row.
+template <class G, int V>
+__device__ __forceinline__ void store_slot(G *dst, const RowSlots &rs, int64_t s, const float (&acc)[V], float scale)
+{
+    if (s < rs.full) {
+        Raw<G, V> o;
+#pragma unroll
+        for (int j = 0; j < V; ++j) o[j] = G(acc[j] * scale);
+        *reinterpret_cast<Raw<G, V> *>(dst + s * V) = o;
+    } else {
+        dst[rs.full * V + (s - rs.full)] = G(acc[0] * scale);
+    }
+}
+
+// The table's rows, one by each `lanes` threads: the sum of its tokens, or of the chunks'
+// partial sums of it.  Many partial sums (a frequent row) are shared out over the block:
+// consecutive ones to each group of lanes, joined in their order.
+constexpr int kFewPartials = 4;
 template <class T, class G>
 __global__ __launch_bounds__(kThreads) void rows_kernel(const T *dy, const uint32_t *keys, const uint32_t *toks,
-                                                        int64_t count, int64_t rows, int chunk, RowSlots rs,
+                                                        int64_t count, int64_t rows, int chunk, RowSlots rs, Bounds bounds,
                                                         const float *partial, float scale, G *dtable)
 {
     constexpr int V = ct::kVec<T>;
-    const int lane = threadIdx.x & (rs.lanes - 1);
-    const int per = kThreads / rs.lanes;
-    for (int64_t v = int64_t(blockIdx.x) * per + threadIdx.x / rs.lanes; v < rows; v += int64_t(gridDim.x) * per) {
-        const int64_t lo = lower_bound(keys, count, uint32_t(v)), hi = lower_bound(keys, count, uint32_t(v) + 1);
-        const int64_t c0 = lo / chunk, c1 = (hi - 1) / chunk;
-        G *dst = dtable + v * rs.width;
-        for (int64_t s = lane; s < rs.slots; s += rs.lanes) {
-            float acc[V] = {};
-            const bool vec = s < rs.full;
-            const int64_t e = vec ? s * V : rs.full * V + (s - rs.full);
-            if (hi > lo && c0 == c1) {
-                add_rows<T, V>(acc, dy, toks, lo, hi, rs, s);
-            } else if (hi > lo) {
-                for (int64_t c = c0; c <= c1; ++c) {
-                    const float *src = partial + (c * 2 + (c == c0 && lo > c0 * chunk ? 1 : 0)) * rs.width + e;
-                    for (int j = 0; j < (vec ? V : 1); ++j) acc[j] += src[j];
-                }
-            }
-            if (vec) {
-                Raw<G, V> o;
-#pragma unroll
-                for (int j = 0; j < V; ++j) o[j] = G(acc[j] * scale);
-                *reinterpret_cast<Raw<G, V> *>(dst + e) = o;
-            } else {
-                dst[e] = G(acc[0] * scale);
+    __shared__ float lds[kThreads * V];
+    __shared__ int many[kThreads][3];  // row of the block, first and last chunk; then whether slot 1 is the first's
+    __shared__ int head_of[kThreads], found;
+    const int lane = threadIdx.x & (rs.lanes - 1), group = threadIdx.x / rs.lanes;
+    const int groups = kThreads / rs.lanes;
+    for (int64_t v0 = int64_t(blockIdx.x) * groups; v0 < rows; v0 += int64_t(gridDim.x) * groups) {
+        const int64_t v = v0 + group;
+        int64_t lo = 0, hi = 0;
+        if (count > 0 && v < rows) {
+            const uint32_t begin = bounds.begin[v], end = bounds.end[v];
+            if (begin < uint32_t(count) && keys[begin] == uint32_t(v)) {
+                lo = begin;
+                hi = end;
             }
         }
+        const int c0 = int(lo / chunk), c1 = hi > lo ? int((hi - 1) / chunk) : c0;
+        const int head = lo > int64_t(c0) * chunk ? 1 : 0;
+        const bool shared = c1 - c0 >= kFewPartials;
+        if (threadIdx.x == 0) found = 0;
+        __syncthreads();
+        if (shared && lane == 0) {
+            const int at = atomicAdd(&found, 1);  // any order: each row is summed by itself
+            many[at][0] = group;
+            many[at][1] = c0;
+            many[at][2] = c1;
+            head_of[at] = head;
+        }
+        if (v < rows && !shared) {
+            G *const dst = dtable + v * rs.width;
+            for (int64_t s = lane; s < rs.slots; s += rs.lanes) {
+                float acc[V] = {};
+                if (hi > lo && c0 == c1) add_rows<4, T, V>(acc, dy, toks, lo, hi, rs, s);
+                else if (hi > lo) add_partials<V>(acc, partial, c0, c1 + 1, c0, head, rs, s);
+                store_slot<G, V>(dst, rs, s, acc, scale);
+            }
+        }
+        __syncthreads();
+        for (int m = 0; m < found; ++m) {
+            const int first = many[m][1], n = many[m][2] - first + 1, share = (n + groups - 1) / groups;
+            const int from = group * share < n ? group * share : n, to = from + share < n ? from + share : n;
+            G *const dst = dtable + (v0 + many[m][0]) * rs.width;
+            for (int64_t s0 = 0; s0 < rs.slots; s0 += rs.lanes) {
+                const int64_t s = s0 + lane;
+                float acc[V] = {};
+                if (s < rs.slots) add_partials<V>(acc, partial, first + from, first + to, first, head_of[m], rs, s);
+                __syncthreads();
+#pragma unroll
+                for (int j = 0; j < V; ++j) lds[threadIdx.x * V + j] = acc[j];
+                __syncthreads();
+                if (group == 0 && s < rs.slots) {
+                    for (int g = 1; g < groups; ++g)
+#pragma unroll
+                        for (int j = 0; j < V; ++j) acc[j] += lds[(g * rs.lanes + lane) * V + j];
+                    store_slot<G, V>(dst, rs, s, acc, scale);
+                }
+            }
+        }
+        __syncthreads();
     }
 }
 
@@ -283,7 +488,8 @@ struct GradPlan {
     int64_t tokens = 0, rows = 0, width = 0;
     int passes = 0, sort_blocks = 0, per_block = 0, chunk = 0;
     int64_t chunks = 0;
-    size_t keys[2] = {}, toks[2] = {}, hist = 0, partial = 0, bytes = 0;
+    bool one_sort = false;
+    size_t keys[2] = {}, toks[2] = {}, hist = 0, begin = 0, end = 0, partial = 0, bytes = 0;
 };
 
 GradPlan grad_plan(int64_t tokens, int64_t rows, int64_t width)
@@ -294,12 +500,19 @@ GradPlan grad_plan(int64_t tokens, int64_t rows, int64_t width)
     g.width = width;
     while (g.passes < 4 && (uint64_t(rows) >> (8 * g.passes)) != 0) ++g.passes;  // keys run from 0 to rows
     if (g.passes == 0) g.passes = 1;
-    int64_t per = 4 * kThreads;
+    int64_t per = 2 * kThreads;  // tokens of a sorting block (60000 tokens: 54.5, 48.0, 51.4 us for 1, 2, 4 a thread)
     while ((tokens + per - 1) / per > kMaxSortBlocks) per *= 2;
     g.per_block = int(per);
     g.sort_blocks = int((tokens + per - 1) / per);
+    g.one_sort = tokens <= kOneSort;
+    // Short chunks spread a frequent row over many blocks, long ones leave fewer partial sums of
+    // it to add (float16, ids by 1/rank, us at 32 / 64 / 128 / 256 tokens a chunk: 32768 tokens x
+    // 512 46.4 / 47.8 / 54.9 / 67.7, 60000 x 256 55.2 / 51.4 / 55.7 / 70.8, 400000 x 64 168 /
+    // 132 / 114 / -).  Up to 512 tokens a row's sum is left to the threads of that row (257
+    // tokens x 77: 11.8 against 14.6 with chunks of 64).
     g.chunk = 64;
-    while (int64_t(g.chunk) * g.chunk < tokens) g.chunk *= 2;
+    while (int64_t(g.chunk) * g.chunk * 32 < tokens) g.chunk *= 2;
+    if (tokens <= 512) g.chunk = 512;
     g.chunks = (tokens + g.chunk - 1) / g.chunk;
     size_t at = 0;
     auto place = [&](size_t bytes) {
@@ -312,6 +525,8 @@ GradPlan grad_plan(int64_t tokens, int64_t rows, int64_t width)
         g.toks[k] = place(size_t(tokens) * 4);
     }
     g.hist = place(size_t(g.sort_blocks) * kDigits * 4);
+    g.begin = place(size_t(rows) * 4);
+    g.end = place(size_t(rows) * 4);
     g.partial = place(g.chunks > 1 ? size_t(g.chunks) * 2 * size_t(width) * 4 : 0);
     g.bytes = at;
     return g;
@@ -420,13 +635,20 @@ ct_status embedding_backward_nd(ct_dtype dtype, ct_dtype index_dtype, int64_t to
     st = ws.take(workspace, workspace_bytes, tokens > 0 ? g.bytes : 0, hs, &err);
     if (st != CT_OK) return fail(st, err);
     char *const base = static_cast<char *>(ws.p);
-    auto words = [&](size_t at) { return reinterpret_cast<uint32_t *>(base + at); };
+    auto words = [&](size_t at) { return base ? reinterpret_cast<uint32_t *>(base + at) : nullptr; };
+    const Bounds bounds{words(g.begin), words(g.end)};
     const uint32_t *keys = nullptr, *toks = nullptr;
     if (tokens > 0) {
         with_index(index, [&](auto i) {
             using I = decltype(i);
             Source<I> src{static_cast<const I *>(ids), nullptr, nullptr, rows, padding_idx};
-            for (int p = 0; p < g.passes; ++p) {
+            if (g.one_sort) {
+                one_sort_kernel<I><<<1, kSortThreads, 0, hs>>>(src, int(tokens), g.passes, g.chunks == 1, bounds,
+                                                              words(g.keys[0]), words(g.toks[0]));
+                src.keys = words(g.keys[0]);
+                src.toks = words(g.toks[0]);
+            }
+            for (int p = 0; p < g.passes && !g.one_sort; ++p) {
                 histogram_kernel<I><<<g.sort_blocks, kThreads, 0, hs>>>(src, tokens, g.per_block, 8 * p, words(g.hist));
                 scatter_kernel<I><<<g.sort_blocks, kThreads, 0, hs>>>(src, tokens, g.per_block, 8 * p, words(g.hist),
                                                                      words(g.keys[p & 1]), words(g.toks[p & 1]));
@@ -440,17 +662,17 @@ ct_status embedding_backward_nd(ct_dtype dtype, ct_dtype index_dtype, int64_t to
     ct::with_type(dt, [&](auto t) {
         using T = decltype(t);
         const RowSlots rs = row_slots<ct::kVec<T>>(width);
-        float *const partial = reinterpret_cast<float *>(base + g.partial);
+        float *const partial = reinterpret_cast<float *>(words(g.partial));
         const T *const dyp = static_cast<const T *>(dy);
-        if (tokens > 0 && g.chunks > 1)
-            partial_kernel<T><<<unsigned(g.chunks), kThreads, 0, hs>>>(dyp, keys, toks, tokens, rows, g.chunk, rs, partial);
+        if (g.chunks > 1)
+            partial_kernel<T><<<unsigned(g.chunks), kThreads, 0, hs>>>(dyp, keys, toks, tokens, rows, g.chunk, rs, bounds, partial);
         const unsigned blocks = blocks_for(rows, kThreads / rs.lanes);
         ct::mark_before(hs);
         if (gt == CT_FLOAT32)
-            rows_kernel<T, float><<<blocks, kThreads, 0, hs>>>(dyp, keys, toks, tokens, rows, g.chunk, rs, partial, scale,
+            rows_kernel<T, float><<<blocks, kThreads, 0, hs>>>(dyp, keys, toks, tokens, rows, g.chunk, rs, bounds, partial, scale,
                                                               static_cast<float *>(dtable));
         else
-            rows_kernel<T, T><<<blocks, kThreads, 0, hs>>>(dyp, keys, toks, tokens, rows, g.chunk, rs, partial, scale,
+            rows_kernel<T, T><<<blocks, kThreads, 0, hs>>>(dyp, keys, toks, tokens, rows, g.chunk, rs, bounds, partial, scale,
                                                           static_cast<T *>(dtable));
         ct::mark_after(hs);
     });
