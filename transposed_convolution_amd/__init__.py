@@ -891,8 +891,11 @@ class PreparedCall:
         self.device = (self.out[0] if isinstance(self.out, tuple) else self.out).device
 
     def __call__(self) -> torch.Tensor:
-        with torch.cuda.device(self.device):
+        if torch.cuda.current_device() == self.device.index:  # entering the device costs a microsecond
             st = self._fn(*self._args)
+        else:
+            with torch.cuda.device(self.device):
+                st = self._fn(*self._args)
         if st:
             _raise(st)
         return self.out

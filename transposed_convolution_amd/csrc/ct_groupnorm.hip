@@ -114,13 +114,13 @@ Plan make_plan(const Sizes &s, bool backward)
         at += (bytes + 255) & ~size_t(255);
         return q;
     };
-    p.uni = Cg % V == 0;
+    p.run = Cg % V == 0 ? V : Cg % 4 == 0 && s.C % V == 0 ? 4 : 1;
     // one block for all positions of as few groups as make whole vectors
     const int want_one = g_one_block.load(std::memory_order_relaxed);
     if (want_one != 0) {
         const int64_t step = V / std::gcd(Cg, int64_t(V));
         const int threads = backward ? kOneGradThreads : kOneThreads;
-        const int64_t held = backward ? one_grad_tiles(V) : one_tiles(p.uni);
+        const int64_t held = backward ? one_grad_tiles(V) : one_tiles(p.run);
         if (cut_tiles(s, V, threads, step, &p.a) && p.a.split == 1 && tiles_of(p.a) <= held) {
             p.one = true;
             cut_chunks(&p.a, held);
@@ -133,7 +133,6 @@ Plan make_plan(const Sizes &s, bool backward)
     const int stat_threads = backward ? kGradThreads : kStatThreads;
     p.vec = cut_tiles(s, V, kApplyThreads, kMostGroups, &p.a) && cut_tiles(s, V, stat_threads, kMostGroups, &p.s);
     if (!p.vec) {
-        p.uni = true;
         cut_tiles(s, 1, kApplyThreads, kMostGroups, &p.a);
         cut_tiles(s, 1, stat_threads, kMostGroups, &p.s);
     }

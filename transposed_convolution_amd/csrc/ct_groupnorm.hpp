@@ -19,7 +19,7 @@ struct Moments {
     {
         const float total = n + bn;
         if (bn > 0.0f) {
-            const float d = bmean - mean, w = bn / total;
+            const float d = bmean - mean, w = bn * __builtin_amdgcn_rcpf(total);  // counts: one rounding more is nothing
             mean += d * w;
             m2 += bm2 + d * d * n * w;
             n = total;
@@ -27,8 +27,8 @@ struct Moments {
     }
 };
 
-// Activation and its derivative.  Kernels are compiled for SiLU, for none and for the
-// piecewise linear kinds, which are told apart by selects: a switch inside a kernel made
+// Activation and its derivative.  Kernels are compiled for SiLU and for the piecewise linear
+// kinds (none among them), which are told apart by selects: a switch inside a kernel made
 // the compiler hoist the unpacking of every held value above it, into spilled registers.
 struct Silu {
     __device__ __forceinline__ float y(float z) const { return z * __builtin_amdgcn_rcpf(1.0f + __expf(-z)); }
@@ -38,10 +38,6 @@ struct Silu {
         return __builtin_fmaf(z * s, 1.0f - s, s);
     }
 };
-struct Identity {
-    __device__ __forceinline__ float y(float z) const { return z; }
-    __device__ __forceinline__ float d(float) const { return 1.0f; }
-};
 struct Piecewise {
     ct::Act a;
     __device__ __forceinline__ float y(float z) const { return a(z); }
@@ -50,15 +46,33 @@ struct Piecewise {
         const float relu = z > 0.0f ? 1.0f : 0.0f;
         const float leaky = z >= 0.0f ? 1.0f : a.p0;
         const float clip = z >= a.p0 && z <= a.p1 ? 1.0f : 0.0f;
-        return a.kind == CT_ACT_RELU ? relu : a.kind == CT_ACT_LEAKY_RELU ? leaky : clip;
+        return a.kind == CT_ACT_RELU ? relu : a.kind == CT_ACT_LEAKY_RELU ? leaky : a.kind == CT_ACT_CLIP ? clip : 1.0f;
     }
 };
 template <class F>
 void with_act(const ct::Act &a, F &&f)
 {
     if (a.kind == CT_ACT_SILU) f(Silu{});
-    else if (a.kind == CT_ACT_IDENTITY) f(Identity{});
     else f(Piecewise{a});
+}
+
+// x - mu, and x * f: the value times an opaque 1 (or f) plus a term, which for float16 is one
+// mixed-precision FMA on the packed half where the plain forms unpack it first.
+__device__ __forceinline__ float opaque_one()
+{
+    float one = 1.0f;
+    asm("" : "+v"(one));
+    return one;
+}
+template <class T>
+__device__ __forceinline__ float minus(T x, float mu, float one)
+{
+    return __builtin_fmaf(float(x), one, -mu);
+}
+template <class T>
+__device__ __forceinline__ float times(T x, float f)
+{
+    return __builtin_fmaf(float(x), f, 0.0f);
 }
 
 // V elements of which the first `valid` exist.
@@ -161,21 +175,17 @@ struct Place {
     {
         return first + count <= k.tiles && (int64_t(chunk) * k.tiles + first + count) * k.rows <= k.P;
     }
-    // Calls f(j, channel of the slab, group of the slab) for the thread's V elements; with UNI
-    // the group is the first's.
-    template <bool UNI, class F>
+    // Calls f(i, channel of the slab, group of the slab) for the first of each S elements.
+    template <int S, class F>
     __device__ __forceinline__ void each(const Cut &k, F f) const
     {
         int c = col, g = k.split > 1 ? 0 : col / k.Cg, left = k.split > 1 ? width : (g + 1) * k.Cg - col;
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            f(j, c, g);
-            if (UNI) {
-                ++c;
-                continue;
-            }
-            ++c;
-            if (--left == 0) {
+        for (int i = 0; i < V / S; ++i) {
+            f(i, c, g);
+            c += S;
+            left -= S;
+            if (left == 0) {
                 ++g;
                 left = k.Cg;
             }
@@ -187,23 +197,25 @@ struct Place {
         }
     }
     // The parameter's values of the thread's channels.
-    template <bool UNI, class T>
+    template <class T>
     __device__ __forceinline__ void params(float (&out)[V], const Cut &k, const Param<T> &p, float absent) const
     {
-        if (UNI || width % V == 0) p.template run<V>(out, c0 + col, absent);
-        else each<UNI>(k, [&](int j, int c, int) { out[j] = p.at(c0 + c, absent); });
+        if (width % V == 0) p.template run<V>(out, c0 + col, absent);
+        else each<1>(k, [&](int j, int c, int) { out[j] = p.at(c0 + c, absent); });
     }
 };
 
-// UNI: a vector lies inside one group, so the thread keeps one triple for all its values.
-template <bool UNI, int V>
-constexpr int kOwn = UNI ? 1 : V;
-template <bool UNI, int V>
-using OwnMoments = Moments[kOwn<UNI, V>];
-template <bool UNI, int V>
-using OwnFloats = float[kOwn<UNI, V>];
-template <int THREADS, bool UNI, int V>
-using JoinBuffer = float[3][THREADS * kOwn<UNI, V>];
+// S: so many consecutive elements of a vector are known to share a group (V, 4 or 1), so the
+// thread keeps V / S triples, means and the like.  With S > 1 every vector starts at a
+// multiple of V elements.
+template <int S, int V>
+constexpr int kOwn = V / S;
+template <int S, int V>
+using OwnMoments = Moments[kOwn<S, V>];
+template <int S, int V>
+using OwnFloats = float[kOwn<S, V>];
+template <int THREADS, int S, int V>
+using JoinBuffer = float[3][THREADS * kOwn<S, V>];
 // A vector as registers: 16 bytes, or a single element.
 using Bits = unsigned __attribute__((ext_vector_type(4)));
 template <int V>
@@ -234,44 +246,36 @@ __device__ __forceinline__ void one_by_one() { __builtin_amdgcn_sched_barrier(0)
 // The thread's moments over `tiles` tiles, updated tile by tile: get(i) is tile i's vector,
 // valid(i) how much of it exists.  An element that exists in a tile exists in all tiles
 // before, so the counts are known constants where the loop is unrolled.
-template <class T, int V, bool UNI, int UNROLL, class Get, class Valid>
-__device__ __forceinline__ void own_moments(OwnMoments<UNI, V> &m, const OwnFloats<UNI, V> &pivot, int tiles, Get get,
-                                            Valid valid)
+template <class T, int V, int S, int UNROLL, class Get, class Valid>
+__device__ __forceinline__ void own_moments(OwnMoments<S, V> &m, const OwnFloats<S, V> &pivot, int tiles, Get get, Valid valid)
 {
+    const float one = opaque_one();
 #pragma unroll UNROLL
     for (int i = 0; i < tiles; ++i) {
         const int w = valid(i);
         const Raw<T, V> r = get(i);
-        if (UNI) {  // all of the vector or nothing of it: its own moments, then joined
-            float v[V], sum = 0.0f, m2 = 0.0f;
+        const float share = 1.0f / float(i + 1);
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                v[j] = float(r[j]) - pivot[0];
+        for (int a = 0; a < V / S; ++a) {
+            // the run's own moments (all of it exists or nothing), then joined
+            float v[S], sum = 0.0f, m2 = 0.0f;
+#pragma unroll
+            for (int j = 0; j < S; ++j) {
+                v[j] = minus(r[a * S + j], pivot[a], one);
                 sum += v[j];
             }
-            const float mean = sum * (1.0f / V);
+            const float mean = sum * (1.0f / S), d = mean - m[a].mean;
+            if (S > 1) {
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const float d = v[j] - mean;
-                m2 = __builtin_fmaf(d, d, m2);
+                for (int j = 0; j < S; ++j) {
+                    const float e = v[j] - mean;
+                    m2 = __builtin_fmaf(e, e, m2);
+                }
             }
-            const float share = 1.0f / float(i + 1), d = mean - m[0].mean;
-            if (w) {
-                m[0].n = float(V * (i + 1));
-                m[0].mean = __builtin_fmaf(d, share, m[0].mean);
-                m[0].m2 += __builtin_fmaf(d * d, float(V * i) * share, m2);
-            }
-        } else {  // one value of each channel
-            const float share = 1.0f / float(i + 1);
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const int a = UNI ? 0 : j;
-                const float v = float(r[j]) - pivot[a], d = v - m[a].mean;
-                const float mean = __builtin_fmaf(d, share, m[a].mean);
-                m[a].m2 = j < w ? __builtin_fmaf(d, v - mean, m[a].m2) : m[a].m2;
-                m[a].mean = j < w ? mean : m[a].mean;
-                m[a].n = j < w ? float(i + 1) : m[a].n;
-            }
+            const bool in = a * S < w;
+            m[a].n = in ? float(S * (i + 1)) : m[a].n;
+            m[a].mean = in ? __builtin_fmaf(d, share, m[a].mean) : m[a].mean;
+            m[a].m2 = in ? m[a].m2 + __builtin_fmaf(d * d, float(S * i) * share, m2) : m[a].m2;
         }
     }
 }
@@ -283,10 +287,14 @@ __device__ __forceinline__ void load_tiles(Held<V> (&raw)[K], const T *x, const 
     if (pl.full(k, first, K)) {
 #pragma unroll
         for (int i = 0; i < K; ++i) raw[i] = hold<T, V>(*reinterpret_cast<const Raw<T, V> *>(x + pl.tile(k, first + i) + pl.off));
-    } else {
+    } else {  // whole tiles, then at most one that ends inside, then none
 #pragma unroll
-        for (int i = 0; i < K; ++i)
-            raw[i] = hold<T, V>(load_first<T, V>(x + pl.tile(k, first + i) + pl.off, pl.valid(k, first + i)));
+        for (int i = 0; i < K; ++i) {
+            const T *const p = x + pl.tile(k, first + i) + pl.off;
+            raw[i] = Held<V>{};
+            if (pl.full(k, first + i, 1)) raw[i] = hold<T, V>(*reinterpret_cast<const Raw<T, V> *>(p));
+            else if (first + i < k.tiles) raw[i] = hold<T, V>(load_first<T, V>(p, pl.valid(k, first + i)));
+        }
     }
 }
 
@@ -309,17 +317,17 @@ struct Call {
 // Threads of a block and tiles held at once.  Statistics: 512 threads of 128 registers, 64 of
 // which hold 16 vectors, so a compute unit has 256 KB of x on its way.  `one`: the kernels
 // in which a block has all positions of its groups.
-constexpr int kStatThreads = 512, kStatTiles = 16;
+constexpr int kStatThreads = 512, kStatTiles = 16, kStatShort = 4;
 constexpr int kApplyThreads = 256, kApplyTiles = 4;
 constexpr int kOneThreads = 512, kOneShort = 4;
-constexpr int one_tiles(bool uni) { return uni ? 16 : 8; }
+constexpr int one_tiles(int S) { return S > 1 ? 16 : 8; }
 constexpr int kGradThreads = 256, kGradTiles = 4;
 constexpr int kOneGradThreads = 256;
 constexpr int one_grad_tiles(int V) { return V == 8 ? 12 : 16; }
 
 struct Plan {
     bool vec = true;   // 16-byte vectors, else single elements
-    bool uni = true;   // every vector lies inside one group
+    int run = 1;       // consecutive elements of a vector that share a group: all, 4 or 1
     bool one = false;  // a block has all positions of its groups: one kernel
     bool finish = false;  // many parts a group: a kernel joins them before the second pass
     Cut s, a;          // the pass for the statistics, the pass that writes (or the only one)
@@ -331,15 +339,15 @@ void launch_forward(const Call &c, const Plan &p, char *ws, hipStream_t st);
 void launch_gradient(const Call &c, const Plan &p, char *ws, hipStream_t st);
 void launch_no_gradient(int dt, bool params_f32, int C, void *dgamma, void *dbeta, hipStream_t st);  // zeros
 
-// Calls f(vector width, vector inside a group?) with the instance for the plan.
+// Calls f(vector width, run) with the instance for the plan.
 template <class T, class F>
 void with_vector(const Plan &p, F &&f)
 {
-    constexpr std::true_type yes{};
-    constexpr std::false_type no{};
-    if (!p.vec) f(std::integral_constant<int, 1>{}, yes);
-    else if (p.uni) f(std::integral_constant<int, kVec<T>>{}, yes);
-    else f(std::integral_constant<int, kVec<T>>{}, no);
+    constexpr int V = kVec<T>;
+    if (!p.vec) f(std::integral_constant<int, 1>{}, std::integral_constant<int, 1>{});
+    else if (p.run == V) f(std::integral_constant<int, V>{}, std::integral_constant<int, V>{});
+    else if (p.run == 4) f(std::integral_constant<int, V>{}, std::integral_constant<int, 4>{});
+    else f(std::integral_constant<int, V>{}, std::integral_constant<int, 1>{});
 }
 
 }  // namespace norm

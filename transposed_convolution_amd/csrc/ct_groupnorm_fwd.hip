@@ -21,11 +21,11 @@ __device__ __forceinline__ float pivot_of(const T *x, const Cut &k, int64_t n, i
 
 // Joins the block's triples of each group of the slab and calls out(group of the slab,
 // moments), on one thread a group.
-template <int THREADS, int V, bool UNI, class Out>
-__device__ __forceinline__ void join_block(const Cut &k, const Place<V> &pl, const OwnMoments<UNI, V> &m,
-                                           JoinBuffer<THREADS, UNI, V> &lds, Out out)
+template <int THREADS, int V, int S, class Out>
+__device__ __forceinline__ void join_block(const Cut &k, const Place<V> &pl, const OwnMoments<S, V> &m,
+                                           JoinBuffer<THREADS, S, V> &lds, Out out)
 {
-    constexpr int A = kOwn<UNI, V>, unit = UNI ? V : 1;  // elements a triple stands for
+    constexpr int A = kOwn<S, V>, unit = S;  // elements a triple stands for
     if (pl.active) {
 #pragma unroll
         for (int a = 0; a < A; ++a) {
@@ -47,26 +47,27 @@ __device__ __forceinline__ void join_block(const Cut &k, const Place<V> &pl, con
     }
 }
 
-template <class T, int V, bool UNI>
-__device__ __forceinline__ void load_pivots(OwnFloats<UNI, V> &pivot, const T *x, const Cut &k, const Place<V> &pl)
+template <class T, int V, int S>
+__device__ __forceinline__ void load_pivots(OwnFloats<S, V> &pivot, const T *x, const Cut &k, const Place<V> &pl)
 {
-    pl.template each<UNI>(k, [&](int j, int, int g) {
-        if (j < kOwn<UNI, V>) pivot[j] = pivot_of(x, k, pl.n, pl.g0 + g);
+    pl.template each<S>(k, [&](int j, int, int g) {
+        pivot[j] = pivot_of(x, k, pl.n, pl.g0 + g);
     });
 }
 
 // y of one tile from its x.
-template <class T, int V, bool UNI, class ACT>
-__device__ __forceinline__ Raw<T, V> outputs(const Raw<T, V> &v, const OwnFloats<UNI, V> &mu, const float (&a)[V],
+template <class T, int V, int S, class ACT>
+__device__ __forceinline__ Raw<T, V> outputs(const Raw<T, V> &v, const OwnFloats<S, V> &mu, const float (&a)[V],
                                              const float (&be)[V], const ACT &f, const Dropout &drop, uint64_t counter,
                                              int64_t first)
 {
+    const float one = opaque_one();
     Raw<T, V> o;
     float r[V];
 #pragma unroll
-    for (int j = 0; j < V; ++j) r[j] = f.y(__builtin_fmaf(float(v[j]) - mu[UNI ? 0 : j], a[j], be[j]));
+    for (int j = 0; j < V; ++j) r[j] = f.y(__builtin_fmaf(minus(v[j], mu[j / S], one), a[j], be[j]));
     if (drop.threshold) {
-        const ct::Fields keep = ct::draw_fields<V, UNI && V != 1>(drop, counter, uint64_t(first));
+        const ct::Fields keep = ct::draw_fields<V, (S > 1)>(drop, counter, uint64_t(first));
 #pragma unroll
         for (int j = 0; j < V; ++j) r[j] = keep.stays(j, drop.limit()) ? r[j] * drop.factor : 0.0f;
     }
@@ -77,28 +78,27 @@ __device__ __forceinline__ Raw<T, V> outputs(const Raw<T, V> &v, const OwnFloats
 
 // The constants of a thread's channels, z = (x - mu) a + be, from a = gamma and the groups'
 // statistics.
-template <int V, bool UNI>
-__device__ __forceinline__ void channel_constants(OwnFloats<UNI, V> &mu, float (&a)[V], const Cut &k, const Place<V> &pl,
+template <int V, int S>
+__device__ __forceinline__ void channel_constants(OwnFloats<S, V> &mu, float (&a)[V], const Cut &k, const Place<V> &pl,
                                                   const float2 *stat)
 {
-    float rs[kOwn<UNI, V>];
-    pl.template each<UNI>(k, [&](int j, int, int g) {
-        if (j >= kOwn<UNI, V>) return;
+    float rs[kOwn<S, V>];
+    pl.template each<S>(k, [&](int j, int, int g) {
         const float2 v = stat[g];
         mu[j] = v.x;
         rs[j] = v.y;
     });
 #pragma unroll
-    for (int j = 0; j < V; ++j) a[j] *= rs[UNI ? 0 : j];
+    for (int j = 0; j < V; ++j) a[j] *= rs[j / S];
 }
 
 // One block has all positions of its groups: x is read once and held in registers.
-template <class T, int V, bool UNI, int K, class ACT>
+template <class T, int V, int S, int K, class ACT>
 __global__ __launch_bounds__(kOneThreads, 4) void one_kernel(const T *x, Cut k, float eps, ct::Param<T> gamma,
                                                              ct::Param<T> beta, ACT f, Dropout drop, T *y, float *mean,
                                                              float *rstd)
 {
-    constexpr int A = kOwn<UNI, V>;
+    constexpr int A = kOwn<S, V>;
     __shared__ float lds[3][kOneThreads * A];
     __shared__ float2 stat[kMostGroups];
     const Place<V> pl(k, blockIdx.x);
@@ -106,13 +106,13 @@ __global__ __launch_bounds__(kOneThreads, 4) void one_kernel(const T *x, Cut k, 
     load_tiles<T, K, V>(raw, x, k, pl, 0);
     const bool full = pl.full(k, 0, K);
     float pivot[A], a[V], be[V];
-    load_pivots<T, V, UNI>(pivot, x, k, pl);
-    pl.template params<UNI>(a, k, gamma, 1.0f);
-    pl.template params<UNI>(be, k, beta, 0.0f);
+    load_pivots<T, V, S>(pivot, x, k, pl);
+    pl.params(a, k, gamma, 1.0f);
+    pl.params(be, k, beta, 0.0f);
     Moments m[A];
-    own_moments<T, V, UNI, K>(m, pivot, K, [&](int i) { return held<T, V>(raw[i]); },
+    own_moments<T, V, S, K>(m, pivot, K, [&](int i) { return held<T, V>(raw[i]); },
                               [&](int i) { return full ? (pl.active ? V : 0) : pl.valid(k, i); });
-    join_block<kOneThreads, V, UNI>(k, pl, m, lds, [&](int g, const Moments &s) {
+    join_block<kOneThreads, V, S>(k, pl, m, lds, [&](int g, const Moments &s) {
         const float mu = pivot_of(x, k, pl.n, pl.g0 + g) + s.mean, r = 1.0f / sqrtf(s.m2 / s.n + eps);
         stat[g] = make_float2(mu, r);
         const int64_t at = pl.n * k.G + pl.g0 + g;
@@ -122,40 +122,40 @@ __global__ __launch_bounds__(kOneThreads, 4) void one_kernel(const T *x, Cut k, 
     __syncthreads();
     if (!pl.active) return;
     float mu[A];
-    channel_constants<V, UNI>(mu, a, k, pl, stat);
+    channel_constants<V, S>(mu, a, k, pl, stat);
     const uint64_t counter = drop.threshold ? drop.counter() : 0;
 #pragma unroll
     for (int i = 0; i < K; ++i) {
         const int valid = full ? V : pl.valid(k, i);
         if (valid == 0) continue;
         const int64_t at = pl.tile(k, i) + pl.off;
-        store_first<T, V>(y + at, outputs<T, V, UNI>(held<T, V>(raw[i]), mu, a, be, f, drop, counter, at), valid);
+        store_first<T, V>(y + at, outputs<T, V, S>(held<T, V>(raw[i]), mu, a, be, f, drop, counter, at), valid);
         one_by_one();
     }
 }
 
 // part[n][g][chunk][slab of the group] = (mean relative to the pivot, m2); the counts follow
 // from the cut.  The pivots are written down too: a call in place overwrites the values.
-template <class T, int V, bool UNI>
+template <class T, int V, int S, int K>
 __global__ __launch_bounds__(kStatThreads, 4) void stats_kernel(const T *x, Cut k, float2 *part, float *pivots)
 {
-    constexpr int A = kOwn<UNI, V>, K = kStatTiles;
+    constexpr int A = kOwn<S, V>;
     __shared__ float lds[3][kStatThreads * A];
     const Place<V> pl(k, blockIdx.x);
     float pivot[A];
-    load_pivots<T, V, UNI>(pivot, x, k, pl);
+    load_pivots<T, V, S>(pivot, x, k, pl);
     Moments m[A];
     for (int first = 0; first < k.tiles; first += K) {
         Held<V> raw[K];
         load_tiles<T, K, V>(raw, x, k, pl, first);
         const bool full = pl.full(k, first, K);
         Moments t[A];
-        own_moments<T, V, UNI, K>(t, pivot, K, [&](int i) { return held<T, V>(raw[i]); },
+        own_moments<T, V, S, K>(t, pivot, K, [&](int i) { return held<T, V>(raw[i]); },
                                   [&](int i) { return full ? (pl.active ? V : 0) : pl.valid(k, first + i); });
 #pragma unroll
         for (int a = 0; a < A; ++a) m[a].join(t[a].n, t[a].mean, t[a].m2);
     }
-    join_block<kStatThreads, V, UNI>(k, pl, m, lds, [&](int g, const Moments &s) {
+    join_block<kStatThreads, V, S>(k, pl, m, lds, [&](int g, const Moments &s) {
         const int64_t group = pl.n * k.G + pl.g0 + g;
         part[(group * k.chunks + pl.chunk) * k.split + pl.sub] = make_float2(s.mean, s.m2);
         if (pl.chunk == 0 && pl.sub == 0) pivots[group] = pivot_of(x, k, pl.n, pl.g0 + g);
@@ -202,20 +202,20 @@ __global__ __launch_bounds__(256) void finish_kernel(const float2 *part, const f
 
 // The second pass.  finished: mean and rstd are there; else every block joins the parts of its
 // groups while its values are on their way, and the first chunk's blocks write them down.
-template <class T, int V, bool UNI, class ACT>
+template <class T, int V, int S, class ACT>
 __global__ __launch_bounds__(kApplyThreads, 4) void apply_kernel(const T *x, Cut k, Cut s, const float2 *part,
                                                                  const float *pivots, bool finished, float eps,
                                                                  ct::Param<T> gamma, ct::Param<T> beta, ACT f, Dropout drop,
                                                                  T *y, float *mean, float *rstd)
 {
-    constexpr int A = kOwn<UNI, V>, K = kApplyTiles;
+    constexpr int A = kOwn<S, V>, K = kApplyTiles;
     __shared__ float2 stat[kMostGroups];
     const Place<V> pl(k, blockIdx.x);
     Held<V> raw[K];
     load_tiles<T, K, V>(raw, x, k, pl, 0);
     float a[V], be[V];
-    pl.template params<UNI>(a, k, gamma, 1.0f);
-    pl.template params<UNI>(be, k, beta, 0.0f);
+    pl.params(a, k, gamma, 1.0f);
+    pl.params(be, k, beta, 0.0f);
     if (finished) {
         for (int g = threadIdx.x; g < pl.groups; g += kApplyThreads) {
             const int64_t at = pl.n * k.G + pl.g0 + g;
@@ -239,7 +239,7 @@ __global__ __launch_bounds__(kApplyThreads, 4) void apply_kernel(const T *x, Cut
     __syncthreads();
     if (!pl.active) return;
     float mu[A];
-    channel_constants<V, UNI>(mu, a, k, pl, stat);
+    channel_constants<V, S>(mu, a, k, pl, stat);
     const uint64_t counter = drop.threshold ? drop.counter() : 0;
     for (int first = 0;;) {
 #pragma unroll
@@ -247,7 +247,7 @@ __global__ __launch_bounds__(kApplyThreads, 4) void apply_kernel(const T *x, Cut
             const int valid = pl.valid(k, first + i);
             if (valid == 0) continue;
             const int64_t at = pl.tile(k, first + i) + pl.off;
-            store_first<T, V>(y + at, outputs<T, V, UNI>(held<T, V>(raw[i]), mu, a, be, f, drop, counter, at), valid);
+            store_first<T, V>(y + at, outputs<T, V, S>(held<T, V>(raw[i]), mu, a, be, f, drop, counter, at), valid);
         }
         first += K;
         if (first >= k.tiles) break;
@@ -269,26 +269,30 @@ void ct::norm::launch_forward(const Call &c, const Plan &p, char *ws, hipStream_
         T *const y = static_cast<T *>(c.y);
         const Param<T> gamma{c.gamma, c.params_f32}, beta{c.beta, c.params_f32};
         if (p.one) {
-            with_act(c.act, [&](auto f) {
-                auto go = [&](auto uni, auto tiles) {
-                    one_kernel<T, kVec<T>, decltype(uni)::value, decltype(tiles)::value, decltype(f)>
-                        <<<unsigned(blocks), kOneThreads, 0, st>>>(x, p.a, c.eps, gamma, beta, f, c.drop, y, c.mean, c.rstd);
-                };
-                constexpr std::true_type yes{};
-                constexpr std::false_type no{};
-                mark_before(st);
-                if (p.uni && p.a.tiles <= kOneShort) go(yes, std::integral_constant<int, kOneShort>{});
-                else if (p.uni) go(yes, std::integral_constant<int, one_tiles(true)>{});
-                else if (p.a.tiles <= kOneShort) go(no, std::integral_constant<int, kOneShort>{});
-                else go(no, std::integral_constant<int, one_tiles(false)>{});
-                mark_after(st);
+            with_vector<T>(p, [&](auto v, auto run) {
+                constexpr int V = decltype(v)::value, S = decltype(run)::value;
+                if constexpr (V == kVec<T>)
+                    with_act(c.act, [&](auto f) {
+                        using F = decltype(f);
+                        mark_before(st);
+                        if (p.a.tiles <= kOneShort)
+                            one_kernel<T, V, S, kOneShort, F><<<unsigned(blocks), kOneThreads, 0, st>>>(
+                                x, p.a, c.eps, gamma, beta, f, c.drop, y, c.mean, c.rstd);
+                        else
+                            one_kernel<T, V, S, one_tiles(S), F><<<unsigned(blocks), kOneThreads, 0, st>>>(
+                                x, p.a, c.eps, gamma, beta, f, c.drop, y, c.mean, c.rstd);
+                        mark_after(st);
+                    });
             });
             return;
         }
-        with_vector<T>(p, [&](auto v, auto uni) {
+        with_vector<T>(p, [&](auto v, auto run) {
             constexpr int V = decltype(v)::value;
-            constexpr bool UNI = decltype(uni)::value;
-            stats_kernel<T, V, UNI><<<unsigned(c.N * p.s.chunks * p.s.slabs), kStatThreads, 0, st>>>(x, p.s, part, pivots);
+            constexpr int S = decltype(run)::value;
+            const unsigned stat_blocks = unsigned(c.N * p.s.chunks * p.s.slabs);
+            if (p.s.tiles <= kStatShort)
+                stats_kernel<T, V, S, kStatShort><<<stat_blocks, kStatThreads, 0, st>>>(x, p.s, part, pivots);
+            else stats_kernel<T, V, S, kStatTiles><<<stat_blocks, kStatThreads, 0, st>>>(x, p.s, part, pivots);
             float *mean = c.mean, *rstd = c.rstd;
             if (p.finish) {
                 if (!mean) mean = stats;
@@ -298,7 +302,7 @@ void ct::norm::launch_forward(const Call &c, const Plan &p, char *ws, hipStream_
             mark_before(st);
             with_act(c.act, [&](auto f) {
                 using F = decltype(f);
-                apply_kernel<T, V, UNI, F><<<unsigned(blocks), kApplyThreads, 0, st>>>(
+                apply_kernel<T, V, S, F><<<unsigned(blocks), kApplyThreads, 0, st>>>(
                     x, p.a, p.s, part, pivots, p.finish, c.eps, gamma, beta, f, c.drop, y, mean, rstd);
             });
             mark_after(st);

@@ -13,42 +13,40 @@ using ct::Dropout;
 using ct::Raw;
 
 // The constants of a thread's channels: z = (x - mu) a + be, a = rstd gamma.
-template <class T, int V, bool UNI>
+template <class T, int V, int S>
 struct Constants {
-    float mu[kOwn<UNI, V>], rs[kOwn<UNI, V>], a[V], be[V];
+    float mu[kOwn<S, V>], rs[kOwn<S, V>], a[V], be[V];
     __device__ Constants(const Cut &k, const Place<V> &pl, const float *mean, const float *rstd, const ct::Param<T> &gamma,
                          const ct::Param<T> &beta)
     {
-        pl.template params<UNI>(a, k, gamma, 1.0f);
-        pl.template params<UNI>(be, k, beta, 0.0f);
+        pl.params(a, k, gamma, 1.0f);
+        pl.params(be, k, beta, 0.0f);
         const int64_t first = pl.n * k.G + pl.g0;
-        pl.template each<UNI>(k, [&](int j, int, int g) {
-            if (j >= kOwn<UNI, V>) return;
-            mu[j] = mean[first + g];
+        pl.template each<S>(k, [&](int j, int, int g) {
+                mu[j] = mean[first + g];
             rs[j] = rstd[first + g];
         });
 #pragma unroll
-        for (int j = 0; j < V; ++j) a[j] *= rs[UNI ? 0 : j];
+        for (int j = 0; j < V; ++j) a[j] *= rs[j / S];
     }
 };
 
 // dz of one tile, before the dropout factor.
-template <class T, int V, bool UNI, class ACT>
+template <class T, int V, int S, class ACT>
 __device__ __forceinline__ void tile_dz(float (&dz)[V], float (&d)[V], const Raw<T, V> &xv, const Raw<T, V> &dv,
-                                        const Constants<T, V, UNI> &ch, const ACT &f, const Dropout &drop, uint64_t counter,
+                                        const Constants<T, V, S> &ch, const ACT &f, const Dropout &drop, uint64_t counter,
                                         int64_t first)
 {
-#pragma unroll
-    for (int j = 0; j < V; ++j) dz[j] = float(dv[j]);
-    if (drop.threshold) {
-        const ct::Fields keep = ct::draw_fields<V, UNI && V != 1>(drop, counter, uint64_t(first));
-#pragma unroll
-        for (int j = 0; j < V; ++j) dz[j] = keep.stays(j, drop.limit()) ? dz[j] : 0.0f;
-    }
+    const float one = opaque_one();
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-        d[j] = float(xv[j]) - ch.mu[UNI ? 0 : j];
-        dz[j] *= f.d(__builtin_fmaf(d[j], ch.a[j], ch.be[j]));
+        d[j] = minus(xv[j], ch.mu[j / S], one);
+        dz[j] = times(dv[j], f.d(__builtin_fmaf(d[j], ch.a[j], ch.be[j])));
+    }
+    if (drop.threshold) {  // a select: a dropped dy may be anything
+        const ct::Fields keep = ct::draw_fields<V, (S > 1)>(drop, counter, uint64_t(first));
+#pragma unroll
+        for (int j = 0; j < V; ++j) dz[j] = keep.stays(j, drop.limit()) ? dz[j] : 0.0f;
     }
 }
 
@@ -93,24 +91,23 @@ __device__ __forceinline__ void join_sums(const Cut &k, const Place<V> &pl, cons
 
 // dx = rstd (dz gamma - c1 - xhat c2) = dz a - k1 - (x - mu) k2, from coef = (c1, c2) of the
 // slab's groups; a gets the dropout factor.
-template <class T, int V, bool UNI>
-__device__ __forceinline__ void output_constants(OwnFloats<UNI, V> &k1, OwnFloats<UNI, V> &k2,
-                                                 Constants<T, V, UNI> &ch, const Cut &k, const Place<V> &pl, const float2 *coef,
-                                                 const Dropout &drop)
+template <class T, int V, int S>
+__device__ __forceinline__ void output_constants(OwnFloats<S, V> &k1, OwnFloats<S, V> &k2,
+                                                 Constants<T, V, S> &ch, const Cut &k, const Place<V> &pl, const float2 *coef,
+                                                 float factor)
 {
-    pl.template each<UNI>(k, [&](int j, int, int g) {
-        if (j >= kOwn<UNI, V>) return;
+    pl.template each<S>(k, [&](int j, int, int g) {
         const float2 v = coef[g];
         k1[j] = v.x * ch.rs[j];
         k2[j] = v.y * ch.rs[j] * ch.rs[j];
     });
 #pragma unroll
-    for (int j = 0; j < V; ++j) ch.a[j] *= drop.factor;
+    for (int j = 0; j < V; ++j) ch.a[j] *= factor;
 }
 
 // One block has all positions of its groups: x and dy are read once, x is held in registers
 // and so is dz, in float32.  sums[n][c] = (sum dz, sum dz xhat).
-template <class T, int V, bool UNI, int K, class ACT>
+template <class T, int V, int S, int K, class ACT>
 __global__ __launch_bounds__(kOneGradThreads, 2) void one_grad_kernel(const T *dy, const T *x, Cut k, const float *mean,
                                                                       const float *rstd, ct::Param<T> gamma,
                                                                       ct::Param<T> beta, ACT f, Dropout drop, float2 *sums,
@@ -123,14 +120,14 @@ __global__ __launch_bounds__(kOneGradThreads, 2) void one_grad_kernel(const T *d
     load_tiles<T, K, V>(xr, x, k, pl, 0);
     load_tiles<T, K, V>(dr, dy, k, pl, 0);
     const bool full = pl.full(k, 0, K);
-    Constants<T, V, UNI> ch(k, pl, mean, rstd, gamma, beta);
+    Constants<T, V, S> ch(k, pl, mean, rstd, gamma, beta);
     const uint64_t counter = drop.threshold ? drop.counter() : 0;
     // elements that do not exist are zeros in dy and add nothing
     float s1[V] = {}, s2[V] = {}, dz[K][V];
 #pragma unroll
     for (int i = 0; i < K; ++i) {
         float d[V];
-        tile_dz<T, V, UNI>(dz[i], d, held<T, V>(xr[i]), held<T, V>(dr[i]), ch, f, drop, counter, pl.tile(k, i) + pl.off);
+        tile_dz<T, V, S>(dz[i], d, held<T, V>(xr[i]), held<T, V>(dr[i]), ch, f, drop, counter, pl.tile(k, i) + pl.off);
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             s1[j] += dz[i][j];
@@ -141,7 +138,7 @@ __global__ __launch_bounds__(kOneGradThreads, 2) void one_grad_kernel(const T *d
 #pragma unroll
     for (int j = 0; j < V; ++j) {
         s1[j] *= drop.factor;
-        s2[j] *= drop.factor * ch.rs[UNI ? 0 : j];
+        s2[j] *= drop.factor * ch.rs[j / S];
     }
     const float count = float(k.P) * float(k.Cg);
     join_sums<kOneGradThreads, T, V>(
@@ -149,8 +146,8 @@ __global__ __launch_bounds__(kOneGradThreads, 2) void one_grad_kernel(const T *d
         [&](int g, float a, float b) { coef[g] = make_float2(a / count, b / count); });
     __syncthreads();
     if (!pl.active) return;
-    float k1[kOwn<UNI, V>], k2[kOwn<UNI, V>];
-    output_constants<T, V, UNI>(k1, k2, ch, k, pl, coef, drop);
+    float k1[kOwn<S, V>], k2[kOwn<S, V>];
+    output_constants<T, V, S>(k1, k2, ch, k, pl, coef, drop.factor);
 #pragma unroll
     for (int i = 0; i < K; ++i) {
         const int valid = full ? V : pl.valid(k, i);
@@ -159,7 +156,7 @@ __global__ __launch_bounds__(kOneGradThreads, 2) void one_grad_kernel(const T *d
         Raw<T, V> o;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            const int q = UNI ? 0 : j;
+            const int q = j / S;
             o[j] = T(__builtin_fmaf(dz[i][j], ch.a[j], __builtin_fmaf(ch.mu[q] - float(xv[j]), k2[q], -k1[q])));
         }
         store_first<T, V>(dx + pl.tile(k, i) + pl.off, o, valid);
@@ -169,8 +166,8 @@ __global__ __launch_bounds__(kOneGradThreads, 2) void one_grad_kernel(const T *d
 
 // part[n][g][chunk][slab of the group] = (sum dz gamma, sum dz gamma xhat),
 // sums[n][chunk][c] = (sum dz, sum dz xhat).
-template <class T, int V, bool UNI, class ACT>
-__global__ __launch_bounds__(kGradThreads, 4) void grad_stats_kernel(const T *dy, const T *x, Cut k, const float *mean,
+template <class T, int V, int S, class ACT>
+__global__ __launch_bounds__(kGradThreads, S > 1 ? 4 : 3) void grad_stats_kernel(const T *dy, const T *x, Cut k, const float *mean,
                                                                      const float *rstd, ct::Param<T> gamma,
                                                                      ct::Param<T> beta, ACT f, Dropout drop, float2 *part,
                                                                      float2 *sums)
@@ -178,7 +175,7 @@ __global__ __launch_bounds__(kGradThreads, 4) void grad_stats_kernel(const T *dy
     constexpr int K = kGradTiles;
     __shared__ float2 lds[kGradThreads * V];
     const Place<V> pl(k, blockIdx.x);
-    const Constants<T, V, UNI> ch(k, pl, mean, rstd, gamma, beta);
+    const Constants<T, V, S> ch(k, pl, mean, rstd, gamma, beta);
     const uint64_t counter = drop.threshold ? drop.counter() : 0;
     float s1[V] = {}, s2[V] = {};
     for (int first = 0; first < k.tiles; first += K) {
@@ -188,7 +185,7 @@ __global__ __launch_bounds__(kGradThreads, 4) void grad_stats_kernel(const T *dy
 #pragma unroll
         for (int i = 0; i < K; ++i) {
             float dz[V], d[V];
-            tile_dz<T, V, UNI>(dz, d, held<T, V>(xr[i]), held<T, V>(dr[i]), ch, f, drop, counter,
+            tile_dz<T, V, S>(dz, d, held<T, V>(xr[i]), held<T, V>(dr[i]), ch, f, drop, counter,
                                pl.tile(k, first + i) + pl.off);
 #pragma unroll
             for (int j = 0; j < V; ++j) {
@@ -201,7 +198,7 @@ __global__ __launch_bounds__(kGradThreads, 4) void grad_stats_kernel(const T *dy
 #pragma unroll
     for (int j = 0; j < V; ++j) {
         s1[j] *= drop.factor;
-        s2[j] *= drop.factor * ch.rs[UNI ? 0 : j];
+        s2[j] *= drop.factor * ch.rs[j / S];
     }
     join_sums<kGradThreads, T, V>(
         k, pl, s1, s2, lds, gamma,
@@ -281,8 +278,8 @@ __global__ __launch_bounds__(256) void param_kernel(const float2 *sums, int64_t 
 // The second pass.  The first `head` blocks make dgamma and dbeta; the others write dx.
 // finished: c1 and c2 are there; else every block joins the parts of its groups while its
 // values are on their way.
-template <class T, int V, bool UNI, class ACT>
-__global__ __launch_bounds__(kApplyThreads, 4) void grad_apply_kernel(const T *dy, const T *x, Cut k, Cut s, const float *mean,
+template <class T, int V, int S, class ACT>
+__global__ __launch_bounds__(kApplyThreads, S > 1 ? 4 : 3) void grad_apply_kernel(const T *dy, const T *x, Cut k, Cut s, const float *mean,
                                                                       const float *rstd, ct::Param<T> gamma,
                                                                       ct::Param<T> beta, ACT f, Dropout drop,
                                                                       const float2 *part, bool finished, const float2 *sums,
@@ -298,7 +295,7 @@ __global__ __launch_bounds__(kApplyThreads, 4) void grad_apply_kernel(const T *d
     Held<V> xr[K], dr[K];
     load_tiles<T, K, V>(xr, x, k, pl, 0);
     load_tiles<T, K, V>(dr, dy, k, pl, 0);
-    Constants<T, V, UNI> ch(k, pl, mean, rstd, gamma, beta);
+    Constants<T, V, S> ch(k, pl, mean, rstd, gamma, beta);
     if (finished) {
         for (int g = threadIdx.x; g < pl.groups; g += kApplyThreads) coef[g] = part[pl.n * k.G + pl.g0 + g];
     } else {
@@ -311,13 +308,9 @@ __global__ __launch_bounds__(kApplyThreads, 4) void grad_apply_kernel(const T *d
     __syncthreads();
     if (!pl.active) return;
     const uint64_t counter = drop.threshold ? drop.counter() : 0;
-    float k1[kOwn<UNI, V>], k2[kOwn<UNI, V>], a[V];
-#pragma unroll
-    for (int j = 0; j < V; ++j) a[j] = ch.a[j];
-    output_constants<T, V, UNI>(k1, k2, ch, k, pl, coef, drop);
+    float k1[kOwn<S, V>], k2[kOwn<S, V>];
+    output_constants<T, V, S>(k1, k2, ch, k, pl, coef, 1.0f);  // the factor goes to dz here
     const float factor = drop.factor;
-#pragma unroll
-    for (int j = 0; j < V; ++j) ch.a[j] = a[j];  // the factor goes to dz here
     for (int first = 0;;) {
 #pragma unroll
         for (int i = 0; i < K; ++i) {
@@ -325,11 +318,11 @@ __global__ __launch_bounds__(kApplyThreads, 4) void grad_apply_kernel(const T *d
             if (valid == 0) continue;
             const int64_t at = pl.tile(k, first + i) + pl.off;
             float dz[V], d[V];
-            tile_dz<T, V, UNI>(dz, d, held<T, V>(xr[i]), held<T, V>(dr[i]), ch, f, drop, counter, at);
+            tile_dz<T, V, S>(dz, d, held<T, V>(xr[i]), held<T, V>(dr[i]), ch, f, drop, counter, at);
             Raw<T, V> o;
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                const int q = UNI ? 0 : j;
+                const int q = j / S;
                 o[j] = T(__builtin_fmaf(dz[j] * factor, ch.a[j], __builtin_fmaf(-d[j], k2[q], -k1[q])));
             }
             store_first<T, V>(dx + at, o, valid);
@@ -358,36 +351,34 @@ void ct::norm::launch_gradient(const Call &c, const Plan &p, char *ws, hipStream
         T *const dx = static_cast<T *>(c.dx);
         const Param<T> gamma{c.gamma, c.params_f32}, beta{c.beta, c.params_f32};
         if (p.one) {
-            mark_before(st);
-            with_act(c.act, [&](auto f) {
-                auto go = [&](auto uni, auto tiles) {
-                    one_grad_kernel<T, kVec<T>, decltype(uni)::value, decltype(tiles)::value, decltype(f)>
-                        <<<unsigned(blocks), kOneGradThreads, 0, st>>>(dy, x, p.a, c.mean, c.rstd, gamma, beta, f, c.drop, sums,
-                                                                      dx);
-                };
-                constexpr std::true_type yes{};
-                constexpr std::false_type no{};
-                constexpr std::integral_constant<int, kOneShort> few{};
-                constexpr std::integral_constant<int, one_grad_tiles(kVec<T>)> many{};
-                if (p.uni && p.a.tiles <= kOneShort) go(yes, few);
-                else if (p.uni) go(yes, many);
-                else if (p.a.tiles <= kOneShort) go(no, few);
-                else go(no, many);
+            with_vector<T>(p, [&](auto v, auto run) {
+                constexpr int V = decltype(v)::value, S = decltype(run)::value;
+                if constexpr (V == kVec<T>)
+                    with_act(c.act, [&](auto f) {
+                        using F = decltype(f);
+                        mark_before(st);
+                        if (p.a.tiles <= kOneShort)
+                            one_grad_kernel<T, V, S, kOneShort, F><<<unsigned(blocks), kOneGradThreads, 0, st>>>(
+                                dy, x, p.a, c.mean, c.rstd, gamma, beta, f, c.drop, sums, dx);
+                        else
+                            one_grad_kernel<T, V, S, one_grad_tiles(V), F><<<unsigned(blocks), kOneGradThreads, 0, st>>>(
+                                dy, x, p.a, c.mean, c.rstd, gamma, beta, f, c.drop, sums, dx);
+                        mark_after(st);
+                    });
             });
-            mark_after(st);
             if (params) param_kernel<T><<<unsigned(head), 256, 0, st>>>(sums, c.N, p.a.C, c.params_f32, c.dgamma, c.dbeta);
             return;
         }
-        with_vector<T>(p, [&](auto v, auto uni) {
+        with_vector<T>(p, [&](auto v, auto run) {
             constexpr int V = decltype(v)::value;
-            constexpr bool UNI = decltype(uni)::value;
+            constexpr int S = decltype(run)::value;
             with_act(c.act, [&](auto f) {
                 using F = decltype(f);
-                grad_stats_kernel<T, V, UNI, F><<<unsigned(c.N * p.s.chunks * p.s.slabs), kGradThreads, 0, st>>>(
+                grad_stats_kernel<T, V, S, F><<<unsigned(c.N * p.s.chunks * p.s.slabs), kGradThreads, 0, st>>>(
                     dy, x, p.s, c.mean, c.rstd, gamma, beta, f, c.drop, part, sums);
                 if (p.finish) grad_finish_kernel<<<unsigned((groups + 3) / 4), 256, 0, st>>>(part, p.s, groups, coef);
                 mark_before(st);
-                grad_apply_kernel<T, V, UNI, F><<<unsigned(blocks + head), kApplyThreads, 0, st>>>(
+                grad_apply_kernel<T, V, S, F><<<unsigned(blocks + head), kApplyThreads, 0, st>>>(
                     dy, x, p.a, p.s, c.mean, c.rstd, gamma, beta, f, c.drop, p.finish ? coef : part, p.finish, sums,
                     c.N * p.s.chunks, head, c.dgamma, c.dbeta, dx);
                 mark_after(st);
