@@ -423,8 +423,7 @@ __global__ __launch_bounds__(kThreads) void rows_kernel(const T *dy, const uint3
 {
     constexpr int V = ct::kVec<T>;
     __shared__ float lds[kThreads * V];
-    __shared__ int many[kThreads][3];  // row of the block, first and last chunk; then whether slot 1 is the first's
-    __shared__ int head_of[kThreads], found;
+    __shared__ int many[kThreads][4], found;  // row of the block, first and last chunk, the first's slot
     const int lane = threadIdx.x & (rs.lanes - 1), group = threadIdx.x / rs.lanes;
     const int groups = kThreads / rs.lanes;
     for (int64_t v0 = int64_t(blockIdx.x) * groups; v0 < rows; v0 += int64_t(gridDim.x) * groups) {
@@ -447,7 +446,7 @@ __global__ __launch_bounds__(kThreads) void rows_kernel(const T *dy, const uint3
             many[at][0] = group;
             many[at][1] = c0;
             many[at][2] = c1;
-            head_of[at] = head;
+            many[at][3] = head;
         }
         if (v < rows && !shared) {
             G *const dst = dtable + v * rs.width;
@@ -466,7 +465,7 @@ __global__ __launch_bounds__(kThreads) void rows_kernel(const T *dy, const uint3
             for (int64_t s0 = 0; s0 < rs.slots; s0 += rs.lanes) {
                 const int64_t s = s0 + lane;
                 float acc[V] = {};
-                if (s < rs.slots) add_partials<V>(acc, partial, first + from, first + to, first, head_of[m], rs, s);
+                if (s < rs.slots) add_partials<V>(acc, partial, first + from, first + to, first, many[m][3], rs, s);
                 __syncthreads();
 #pragma unroll
                 for (int j = 0; j < V; ++j) lds[threadIdx.x * V + j] = acc[j];

@@ -45,6 +45,12 @@ struct Sizes {
 // Controls for tests and tuning (group_norm_set_control).
 std::atomic<int> g_one_block{-1}, g_finish{-1};
 
+void set_lanes(Cut *k, int threads)
+{
+    k->lanes = 1;
+    while (k->lanes < 64 && 2 * k->lanes * k->per <= threads) k->lanes *= 2;
+}
+
 // The slabs and the tile of blocks of `threads` threads; false when whole vectors of V
 // elements do not fit this channel count.
 bool cut_tiles(const Sizes &s, int V, int threads, int64_t most_groups, Cut *k)
@@ -83,8 +89,7 @@ bool cut_tiles(const Sizes &s, int V, int threads, int64_t most_groups, Cut *k)
     const int64_t fit = std::min<int64_t>(most / k->width, (int64_t(1) << 30) / s.C) / unit * unit;
     if (fit < 1) return false;
     k->rows = int(std::min(fit, (s.P + unit - 1) / unit * unit));
-    k->lanes = 1;
-    while (k->lanes < 64 && 2 * k->lanes * k->per <= threads) k->lanes *= 2;
+    set_lanes(k, threads);
     return true;
 }
 
@@ -96,6 +101,22 @@ void cut_chunks(Cut *k, int64_t tiles)
     const int64_t all = tiles_of(*k), chunks = (all + tiles - 1) / tiles;
     k->tiles = int((all + chunks - 1) / chunks);
     k->chunks = int((all + k->tiles - 1) / k->tiles);
+}
+
+// One block for a group's slab where a thread holds at most four vectors and the reads stay
+// small.  The slab of a block may be only 16 bytes wide, and each block reads the whole
+// 128-byte lines it touches: what counts is those.  Measured (float16, 256 channels in 32
+// groups, N images of P positions; one block / two passes, us): N 1, P 2048 9.0 / 12.6,
+// P 4096 (eight vectors) 15.2 / 12.6; N 8, P 1024 (32 MiB of lines) 13.8 / 16.4, P 2048
+// 25.0 / 17.1; N 32, P 256 (32 MiB) 12.8 / 14.2, P 1024 44.5 / 15.8.  Gradient: N 1, P 1024
+// 10.5 / 11.4, P 2048 (eight vectors) 15.3 / 12.6; N 8, P 256 (16 MiB) 10.2 / 10.9, P 1024
+// (64 MiB) 21.1 / 16.2; 64 channels in 16 groups, float32, N 8, P 1024 (32 MiB) 12.2 / 11.6.
+constexpr int64_t kOneBytes = 32 << 20, kOneGradBytes = 16 << 20;
+int64_t line_bytes(const Sizes &s, const Cut &k, bool backward)
+{
+    const int64_t run = int64_t(k.width) * int64_t(ct::float_size(s.dt));
+    const int64_t lines = s.N * s.P * ((s.C + k.width - 1) / k.width) * ((run + 127) / 128 * 128);
+    return backward ? 2 * lines : lines;
 }
 
 constexpr int64_t kPartBytes = 32 << 10;      // parts that every block of the second pass joins
@@ -120,10 +141,12 @@ Plan make_plan(const Sizes &s, bool backward)
     if (want_one != 0) {
         const int64_t step = V / std::gcd(Cg, int64_t(V));
         const int threads = backward ? kOneGradThreads : kOneThreads;
-        const int64_t held = backward ? one_grad_tiles(V) : one_tiles(p.run);
-        if (cut_tiles(s, V, threads, step, &p.a) && p.a.split == 1 && tiles_of(p.a) <= held) {
+        if (cut_tiles(s, V, threads, step, &p.a) && p.a.split == 1 && tiles_of(p.a) <= kOneTiles &&
+            line_bytes(s, p.a, backward) <= (backward ? kOneGradBytes : kOneBytes)) {
             p.one = true;
-            cut_chunks(&p.a, held);
+            cut_chunks(&p.a, kOneTiles);
+            p.threads = (int(int64_t(p.a.rows) * p.a.width / V) + 63) / 64 * 64;
+            set_lanes(&p.a, p.threads);
             p.s = p.a;
             if (backward) p.sums = place(size_t(s.N) * s.C * 8);
             p.bytes = at;

@@ -319,16 +319,14 @@ struct Call {
 // in which a block has all positions of its groups.
 constexpr int kStatThreads = 512, kStatTiles = 16, kStatShort = 4;
 constexpr int kApplyThreads = 256, kApplyTiles = 4;
-constexpr int kOneThreads = 512, kOneShort = 4;
-constexpr int one_tiles(int S) { return S > 1 ? 16 : 8; }
+constexpr int kOneThreads = 512, kOneGradThreads = 256, kOneTiles = 4;
 constexpr int kGradThreads = 256, kGradTiles = 4;
-constexpr int kOneGradThreads = 256;
-constexpr int one_grad_tiles(int V) { return V == 8 ? 12 : 16; }
 
 struct Plan {
     bool vec = true;   // 16-byte vectors, else single elements
     int run = 1;       // consecutive elements of a vector that share a group: all, 4 or 1
     bool one = false;  // a block has all positions of its groups: one kernel
+    int threads = 0;   // of its blocks: as many as a tile needs
     bool finish = false;  // many parts a group: a kernel joins them before the second pass
     Cut s, a;          // the pass for the statistics, the pass that writes (or the only one)
     // places in the workspace (bytes)

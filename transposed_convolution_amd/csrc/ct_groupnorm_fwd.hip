@@ -36,7 +36,7 @@ __device__ __forceinline__ void join_block(const Cut &k, const Place<V> &pl, con
     }
     __syncthreads();
     const int per = (k.split > 1 ? pl.width : k.Cg) / unit, row = pl.width / unit, lane = threadIdx.x & (k.lanes - 1);
-    for (int g = int(threadIdx.x) / k.lanes; g < pl.groups; g += THREADS / k.lanes) {
+    for (int g = int(threadIdx.x) / k.lanes; g < pl.groups; g += int(blockDim.x) / k.lanes) {
         Moments s;
         for (int i = lane; i < per * k.rows; i += k.lanes) {
             const int r = i / per, at = r * row + g * per + (i - r * per);
@@ -93,12 +93,12 @@ __device__ __forceinline__ void channel_constants(OwnFloats<S, V> &mu, float (&a
 }
 
 // One block has all positions of its groups: x is read once and held in registers.
-template <class T, int V, int S, int K, class ACT>
+template <class T, int V, int S, class ACT>
 __global__ __launch_bounds__(kOneThreads, 4) void one_kernel(const T *x, Cut k, float eps, ct::Param<T> gamma,
                                                              ct::Param<T> beta, ACT f, Dropout drop, T *y, float *mean,
                                                              float *rstd)
 {
-    constexpr int A = kOwn<S, V>;
+    constexpr int A = kOwn<S, V>, K = kOneTiles;
     __shared__ float lds[3][kOneThreads * A];
     __shared__ float2 stat[kMostGroups];
     const Place<V> pl(k, blockIdx.x);
@@ -275,12 +275,8 @@ void ct::norm::launch_forward(const Call &c, const Plan &p, char *ws, hipStream_
                     with_act(c.act, [&](auto f) {
                         using F = decltype(f);
                         mark_before(st);
-                        if (p.a.tiles <= kOneShort)
-                            one_kernel<T, V, S, kOneShort, F><<<unsigned(blocks), kOneThreads, 0, st>>>(
-                                x, p.a, c.eps, gamma, beta, f, c.drop, y, c.mean, c.rstd);
-                        else
-                            one_kernel<T, V, S, one_tiles(S), F><<<unsigned(blocks), kOneThreads, 0, st>>>(
-                                x, p.a, c.eps, gamma, beta, f, c.drop, y, c.mean, c.rstd);
+                        one_kernel<T, V, S, F><<<unsigned(blocks), p.threads, 0, st>>>(
+                            x, p.a, c.eps, gamma, beta, f, c.drop, y, c.mean, c.rstd);
                         mark_after(st);
                     });
             });

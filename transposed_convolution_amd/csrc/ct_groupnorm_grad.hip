@@ -61,9 +61,25 @@ __device__ __forceinline__ void join_sums(const Cut &k, const Place<V> &pl, cons
 #pragma unroll
         for (int j = 0; j < V; ++j) lds[pl.e + j] = make_float2(s1[j], s2[j]);
     __syncthreads();
-    for (int c = threadIdx.x; c < pl.width; c += THREADS) {
+    // a narrow slab has many rows and few columns: first up to 16 threads a column, rows apart
+    const int parts = min(min(16, k.rows), int(blockDim.x) / pl.width);
+    if (parts > 1) {
+        const int q = int(threadIdx.x) / pl.width, c = int(threadIdx.x) - q * pl.width;
+        float2 s = make_float2(0.0f, 0.0f);
+        if (q < parts)
+            for (int r = q; r < k.rows; r += parts) {
+                const float2 v = lds[r * pl.width + c];
+                s.x += v.x;
+                s.y += v.y;
+            }
+        __syncthreads();
+        if (q < parts) lds[q * pl.width + c] = s;
+        __syncthreads();
+    }
+    const int rows = parts > 1 ? parts : k.rows;
+    for (int c = threadIdx.x; c < pl.width; c += int(blockDim.x)) {
         float2 s = lds[c];
-        for (int r = 1; r < k.rows; ++r) {
+        for (int r = 1; r < rows; ++r) {
             const float2 v = lds[r * pl.width + c];
             s.x += v.x;
             s.y += v.y;
@@ -74,7 +90,7 @@ __device__ __forceinline__ void join_sums(const Cut &k, const Place<V> &pl, cons
     }
     __syncthreads();
     const int per = k.split > 1 ? pl.width : k.Cg, lane = threadIdx.x & (k.lanes - 1);
-    for (int g = int(threadIdx.x) / k.lanes; g < pl.groups; g += THREADS / k.lanes) {
+    for (int g = int(threadIdx.x) / k.lanes; g < pl.groups; g += int(blockDim.x) / k.lanes) {
         float a = 0.0f, b = 0.0f;
         for (int c = lane; c < per; c += k.lanes) {
             const float2 v = lds[g * per + c];
@@ -107,12 +123,13 @@ __device__ __forceinline__ void output_constants(OwnFloats<S, V> &k1, OwnFloats<
 
 // One block has all positions of its groups: x and dy are read once, x is held in registers
 // and so is dz, in float32.  sums[n][c] = (sum dz, sum dz xhat).
-template <class T, int V, int S, int K, class ACT>
+template <class T, int V, int S, class ACT>
 __global__ __launch_bounds__(kOneGradThreads, 2) void one_grad_kernel(const T *dy, const T *x, Cut k, const float *mean,
                                                                       const float *rstd, ct::Param<T> gamma,
                                                                       ct::Param<T> beta, ACT f, Dropout drop, float2 *sums,
                                                                       T *dx)
 {
+    constexpr int K = kOneTiles;
     __shared__ float2 lds[kOneGradThreads * V];
     __shared__ float2 coef[kMostGroups];
     const Place<V> pl(k, blockIdx.x);
@@ -357,12 +374,8 @@ void ct::norm::launch_gradient(const Call &c, const Plan &p, char *ws, hipStream
                     with_act(c.act, [&](auto f) {
                         using F = decltype(f);
                         mark_before(st);
-                        if (p.a.tiles <= kOneShort)
-                            one_grad_kernel<T, V, S, kOneShort, F><<<unsigned(blocks), kOneGradThreads, 0, st>>>(
-                                dy, x, p.a, c.mean, c.rstd, gamma, beta, f, c.drop, sums, dx);
-                        else
-                            one_grad_kernel<T, V, S, one_grad_tiles(V), F><<<unsigned(blocks), kOneGradThreads, 0, st>>>(
-                                dy, x, p.a, c.mean, c.rstd, gamma, beta, f, c.drop, sums, dx);
+                        one_grad_kernel<T, V, S, F><<<unsigned(blocks), p.threads, 0, st>>>(
+                            dy, x, p.a, c.mean, c.rstd, gamma, beta, f, c.drop, sums, dx);
                         mark_after(st);
                     });
             });
