@@ -165,7 +165,7 @@ __global__ __launch_bounds__(kStatThreads, 4) void stats_kernel(const T *x, Cut 
 // Joins the parts of one group, `lanes` threads together; the moments on every one of them.
 __device__ __forceinline__ Moments join_parts(const float2 *part, const Cut &s, int64_t group, int lane, int lanes)
 {
-    constexpr int kAtOnce = 4;
+    constexpr int kAtOnce = 8;  // on their way together
     const float2 *p = part + group * s.chunks * s.split;
     const int count = s.chunks * s.split;
     Moments m;
@@ -201,7 +201,8 @@ __global__ __launch_bounds__(256) void finish_kernel(const float2 *part, const f
 }
 
 // The second pass.  finished: mean and rstd are there; else every block joins the parts of its
-// groups while its values are on their way, and the first chunk's blocks write them down.
+// groups, before it asks for its values (behind those they would arrive late), and the first
+// chunk's blocks write mean and rstd down.
 template <class T, int V, int S, class ACT>
 __global__ __launch_bounds__(kApplyThreads, 4) void apply_kernel(const T *x, Cut k, Cut s, const float2 *part,
                                                                  const float *pivots, bool finished, float eps,
@@ -211,11 +212,6 @@ __global__ __launch_bounds__(kApplyThreads, 4) void apply_kernel(const T *x, Cut
     constexpr int A = kOwn<S, V>, K = kApplyTiles;
     __shared__ float2 stat[kMostGroups];
     const Place<V> pl(k, blockIdx.x);
-    Held<V> raw[K];
-    load_tiles<T, K, V>(raw, x, k, pl, 0);
-    float a[V], be[V];
-    pl.params(a, k, gamma, 1.0f);
-    pl.params(be, k, beta, 0.0f);
     if (finished) {
         for (int g = threadIdx.x; g < pl.groups; g += kApplyThreads) {
             const int64_t at = pl.n * k.G + pl.g0 + g;
@@ -236,6 +232,11 @@ __global__ __launch_bounds__(kApplyThreads, 4) void apply_kernel(const T *x, Cut
             }
         }
     }
+    Held<V> raw[K];
+    load_tiles<T, K, V>(raw, x, k, pl, 0);
+    float a[V], be[V];
+    pl.params(a, k, gamma, 1.0f);
+    pl.params(be, k, beta, 0.0f);
     __syncthreads();
     if (!pl.active) return;
     float mu[A];
