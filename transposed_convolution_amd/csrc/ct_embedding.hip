@@ -9,6 +9,7 @@
 #include <hip/hip_runtime.h>
 
 #include <string>
+#include <type_traits>
 
 #include "ct_vec.hpp"
 
@@ -275,18 +276,6 @@ __global__ __launch_bounds__(kSortThreads) void one_sort_kernel(Source<I> src, i
     }
 }
 
-// First position of the sorted keys that is not below `key`.
-__device__ __forceinline__ int64_t lower_bound(const uint32_t *keys, int64_t count, uint32_t key)
-{
-    int64_t lo = 0, hi = count;
-    while (lo < hi) {
-        const int64_t mid = (lo + hi) >> 1;
-        if (keys[mid] < key) lo = mid + 1;
-        else hi = mid;
-    }
-    return lo;
-}
-
 // Adds dy[toks[i]] for i in [begin, end) into acc, slot s of the row: kAtOnce tokens' loads at
 // a time, added in order.
 template <int kAtOnce, class T, int V>
@@ -350,54 +339,6 @@ __device__ __forceinline__ void add_partials(float (&acc)[V], const float *parti
     }
 }
 
-// The sorted tokens in chunks: a row inside one chunk is summed by the kernel that writes
-// the rows; of a row that crosses a chunk's border every chunk makes a partial sum here,
-// slot 0 for the row at its start and slot 1 for the one at its end.  The block's groups of
-// lanes take consecutive shares of the row's tokens, joined in their order.
-template <class T>
-__global__ __launch_bounds__(kThreads) void partial_kernel(const T *dy, const uint32_t *keys, const uint32_t *toks,
-                                                           int64_t count, int64_t rows, int chunk, RowSlots rs, Bounds bounds,
-                                                           float *partial)
-{
-    constexpr int V = ct::kVec<T>;
-    __shared__ float lds[kThreads * V];
-    const int64_t a = int64_t(blockIdx.x) * chunk, b = a + chunk < count ? a + chunk : count;
-    for (int64_t i = a + threadIdx.x; i < b; i += kThreads) bounds.mark(keys, i, count, rows);
-    const uint32_t first = keys[a], last = keys[b - 1];
-    const int groups = kThreads / rs.lanes, group = threadIdx.x / rs.lanes, lane = threadIdx.x & (rs.lanes - 1);
-    for (int slot = 0; slot < 2; ++slot) {  // everything that steers here is the same on all threads
-        const uint32_t key = slot ? last : first;
-        if (key >= uint32_t(rows) || (slot && first == last)) continue;
-        const bool crosses = slot || first == last ? (b < count && keys[b] == key) || (!slot && a > 0 && keys[a - 1] == key)
-                                                   : a > 0 && keys[a - 1] == key;
-        if (!crosses) continue;
-        const int64_t lo = slot ? a + lower_bound(keys + a, b - a, key) : a;
-        const int64_t hi = slot ? b : a + lower_bound(keys + a, b - a, key + 1);
-        const int64_t share = (hi - lo + groups - 1) / groups;
-        const int64_t from = lo + group * share < hi ? lo + group * share : hi, to = from + share < hi ? from + share : hi;
-        float *const out = partial + (int64_t(blockIdx.x) * 2 + slot) * rs.width;
-        for (int64_t s0 = 0; s0 < rs.slots; s0 += rs.lanes) {
-            const int64_t s = s0 + lane;
-            float acc[V] = {};
-            if (s < rs.slots && from < to) add_rows<8, T, V>(acc, dy, toks, from, to, rs, s);
-            __syncthreads();
-#pragma unroll
-            for (int j = 0; j < V; ++j) lds[threadIdx.x * V + j] = acc[j];
-            __syncthreads();
-            if (group == 0 && s < rs.slots) {
-                for (int g = 1; g < groups; ++g)
-#pragma unroll
-                    for (int j = 0; j < V; ++j) acc[j] += lds[(g * rs.lanes + lane) * V + j];
-                if (s < rs.full) {
-                    *reinterpret_cast<Raw<float, V> *>(out + s * V) = as_floats(acc);
-                } else {
-                    out[rs.full * V + (s - rs.full)] = acc[0];
-                }
-            }
-        }
-    }
-}
-
 // Stores slot s of a table row.
 template <class G, int V>
 __device__ __forceinline__ void store_slot(G *dst, const RowSlots &rs, int64_t s, const float (&acc)[V], float scale)
@@ -412,14 +353,113 @@ __device__ __forceinline__ void store_slot(G *dst, const RowSlots &rs, int64_t s
     }
 }
 
-// The table's rows, one by each `lanes` threads: the sum of its tokens, or of the chunks'
-// partial sums of it.  Many partial sums (a frequent row) are shared out over the block:
+// The sorted tokens in chunks.  The groups of lanes take consecutive shares of a chunk's tokens
+// and walk them, kAtOnce rows of dy on their way together: a sum that begins and ends inside a
+// share is stored at once, those at a share's borders are joined in their order over LDS, and
+// of a row that crosses a chunk's border every chunk leaves a partial sum, in slot 0 of the
+// chunk for a row that is there from its start and in slot 1 for one that begins later.
+constexpr int kMostChunk = 1024;
+template <class T, class G>
+__global__ __launch_bounds__(kThreads) void chunk_kernel(const T *dy, const uint32_t *keys, const uint32_t *toks,
+                                                         int64_t count, int64_t rows, int chunk, RowSlots rs, int64_t steps,
+                                                         int64_t work, Bounds bounds, float *partial, float scale, G *dtable)
+{
+    constexpr int V = ct::kVec<T>, kAtOnce = 8;
+    __shared__ uint32_t key[kMostChunk], tok[kMostChunk];
+    __shared__ float ends[2][kThreads * V];  // a share's first sum, and its last if that is another
+    __shared__ int valid;
+    const int groups = kThreads / rs.lanes, group = threadIdx.x / rs.lanes, lane = threadIdx.x & (rs.lanes - 1);
+    for (int64_t w = blockIdx.x; w < work; w += gridDim.x) {
+        const int64_t c = w / steps, s = (w - c * steps) * rs.lanes + lane, a = c * chunk;
+        const int n = int(count - a < chunk ? count - a : chunk);
+        const uint32_t left = a > 0 ? keys[a - 1] : uint32_t(rows), right = a + n < count ? keys[a + n] : uint32_t(rows);
+        __syncthreads();
+        if (threadIdx.x == 0) valid = 0;
+        for (int i = threadIdx.x; i < n; i += kThreads) {
+            key[i] = keys[a + i];
+            tok[i] = toks[a + i];
+        }
+        __syncthreads();
+        for (int i = threadIdx.x; i < n; i += kThreads) {
+            const uint32_t k = key[i];
+            if (k >= uint32_t(rows)) continue;
+            const uint32_t before = i > 0 ? key[i - 1] : left, after = i + 1 < n ? key[i + 1] : right;
+            if (i + 1 == n || after >= uint32_t(rows)) valid = i + 1;
+            if (s != lane) continue;  // one step a chunk marks
+            if (before != k) bounds.begin[k] = uint32_t(a + i);
+            if (after != k) bounds.end[k] = uint32_t(a + i + 1);
+        }
+        __syncthreads();
+        const int m = valid;
+        if (m == 0) continue;
+        const bool vec = s < rs.full, there = s < rs.slots;
+        const int64_t at = vec ? s * V : rs.full * V + (s - rs.full);  // the slot's first element
+        const int share = (m + groups - 1) / groups;
+        const int from = group * share < m ? group * share : m, to = from + share < m ? from + share : m;
+        float acc[V] = {};
+        int run = from;  // where the sum in acc began
+        auto keep = [&](int part) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) ends[part][threadIdx.x * V + j] = acc[j];
+        };
+        auto put = [&](uint32_t k) {
+            if (there) store_slot<G, V>(dtable + int64_t(k) * rs.width, rs, s, acc, scale);
+        };
+        for (int i = from; i < to; i += kAtOnce) {
+            Raw<T, V> v[kAtOnce];
+#pragma unroll
+            for (int q = 0; q < kAtOnce; ++q) {  // past the end the last token, not added
+                const T *const src = dy + int64_t(tok[i + q < to ? i + q : to - 1]) * rs.width + at;
+                v[q] = Raw<T, V>{};
+                if (vec) v[q] = *reinterpret_cast<const Raw<T, V> *>(src);
+                else if (there) v[q][0] = *src;
+            }
+#pragma unroll
+            for (int q = 0; q < kAtOnce; ++q) {
+                if (i + q >= to) break;
+                if (i + q > run && key[i + q] != key[i + q - 1]) {
+                    if (run == from) keep(0);
+                    else put(key[run]);
+                    run = i + q;
+#pragma unroll
+                    for (int j = 0; j < V; ++j) acc[j] = 0.0f;
+                }
+#pragma unroll
+                for (int j = 0; j < V; ++j) acc[j] += float(v[q][j]);
+            }
+        }
+        if (from < to) keep(run == from ? 0 : 1);
+        __syncthreads();
+        // each share's groups of lanes write the rows that begin in its first or last sum
+        for (int part = 0; part < 2 && from < to; ++part) {
+            const uint32_t k = part ? key[to - 1] : key[from];
+            if (part ? k == key[from] : from > 0 && key[from - 1] == k) continue;
+#pragma unroll
+            for (int j = 0; j < V; ++j) acc[j] = ends[part][threadIdx.x * V + j];
+            if (key[to - 1] == k)
+                for (int g = group + 1; g * share < m && key[g * share] == k; ++g)
+#pragma unroll
+                    for (int j = 0; j < V; ++j) acc[j] += ends[0][(g * rs.lanes + lane) * V + j];
+            if (!((k == key[0] && left == k) || (k == key[m - 1] && m == n && right == k))) {
+                put(k);
+            } else if (there) {
+                float *const out = partial + (c * 2 + (k == key[0] ? 0 : 1)) * rs.width + at;
+                if (vec) *reinterpret_cast<Raw<float, V> *>(out) = as_floats(acc);
+                else *out = acc[0];
+            }
+        }
+    }
+}
+
+// The table's rows, one by each `lanes` threads: zeros, or the sum of the chunks' partial sums
+// of it; the rows inside a chunk are written already.  With one chunk there is no kernel
+// before this one, and a row is the sum of its tokens.  Many partial sums (a frequent row) are shared out over the block:
 // consecutive ones to each group of lanes, joined in their order.
 constexpr int kFewPartials = 4;
 template <class T, class G>
 __global__ __launch_bounds__(kThreads) void rows_kernel(const T *dy, const uint32_t *keys, const uint32_t *toks,
                                                         int64_t count, int64_t rows, int chunk, RowSlots rs, Bounds bounds,
-                                                        const float *partial, float scale, G *dtable)
+                                                        const float *partial, bool inner, float scale, G *dtable)
 {
     constexpr int V = ct::kVec<T>;
     __shared__ float lds[kThreads * V];
@@ -448,7 +488,7 @@ __global__ __launch_bounds__(kThreads) void rows_kernel(const T *dy, const uint3
             many[at][2] = c1;
             many[at][3] = head;
         }
-        if (v < rows && !shared) {
+        if (v < rows && !shared && !(inner && hi > lo && c0 == c1)) {
             G *const dst = dtable + v * rs.width;
             for (int64_t s = lane; s < rs.slots; s += rs.lanes) {
                 float acc[V] = {};
@@ -510,7 +550,7 @@ GradPlan grad_plan(int64_t tokens, int64_t rows, int64_t width)
     // 132 / 114 / -).  Up to 512 tokens a row's sum is left to the threads of that row (257
     // tokens x 77: 11.8 against 14.6 with chunks of 64).
     g.chunk = 64;
-    while (int64_t(g.chunk) * g.chunk * 32 < tokens) g.chunk *= 2;
+    while (g.chunk < kMostChunk && int64_t(g.chunk) * g.chunk * 32 < tokens) g.chunk *= 2;
     if (tokens <= 512) g.chunk = 512;
     g.chunks = (tokens + g.chunk - 1) / g.chunk;
     size_t at = 0;
@@ -663,17 +703,20 @@ ct_status embedding_backward_nd(ct_dtype dtype, ct_dtype index_dtype, int64_t to
         const RowSlots rs = row_slots<ct::kVec<T>>(width);
         float *const partial = reinterpret_cast<float *>(words(g.partial));
         const T *const dyp = static_cast<const T *>(dy);
-        if (g.chunks > 1)
-            partial_kernel<T><<<unsigned(g.chunks), kThreads, 0, hs>>>(dyp, keys, toks, tokens, rows, g.chunk, rs, bounds, partial);
-        const unsigned blocks = blocks_for(rows, kThreads / rs.lanes);
-        ct::mark_before(hs);
-        if (gt == CT_FLOAT32)
-            rows_kernel<T, float><<<blocks, kThreads, 0, hs>>>(dyp, keys, toks, tokens, rows, g.chunk, rs, bounds, partial, scale,
-                                                              static_cast<float *>(dtable));
-        else
-            rows_kernel<T, T><<<blocks, kThreads, 0, hs>>>(dyp, keys, toks, tokens, rows, g.chunk, rs, bounds, partial, scale,
-                                                          static_cast<T *>(dtable));
-        ct::mark_after(hs);
+        const bool inner = g.chunks > 1;
+        const int64_t steps = (rs.slots + rs.lanes - 1) / rs.lanes, work = g.chunks * steps;
+        auto go = [&](auto *grad) {
+            using G = std::remove_reference_t<decltype(*grad)>;
+            ct::mark_before(hs);
+            if (inner)
+                chunk_kernel<T, G><<<blocks_for(work, 1), kThreads, 0, hs>>>(dyp, keys, toks, tokens, rows, g.chunk, rs, steps,
+                                                                            work, bounds, partial, scale, grad);
+            rows_kernel<T, G><<<blocks_for(rows, kThreads / rs.lanes), kThreads, 0, hs>>>(
+                dyp, keys, toks, tokens, rows, g.chunk, rs, bounds, partial, inner, scale, grad);
+            ct::mark_after(hs);
+        };
+        if (gt == CT_FLOAT32) go(static_cast<float *>(dtable));
+        else go(static_cast<T *>(dtable));
     });
     st = ct::launch_status("embedding gradient launch failed", &err);
     return st == CT_OK ? CT_OK : fail(st, err);
