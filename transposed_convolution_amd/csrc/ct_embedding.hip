@@ -8,6 +8,7 @@
 // and no gradient: nothing outside the table is read or written.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <string>
 #include <type_traits>
 
@@ -149,8 +150,22 @@ __global__ __launch_bounds__(kThreads) void scatter_kernel(Source<I> src, int64_
 {
     constexpr int kWaves = kThreads / kWave;
     __shared__ uint32_t off[kWaves][kDigits];
-    __shared__ uint32_t scan[kDigits];
+    __shared__ uint32_t wave_sum[kWaves];
     const int d = threadIdx.x, lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+    // a wave's tokens are consecutive, so the order within a digit is wave, round, lane
+    const int per_wave = per_block / kWaves;
+    const int64_t first = int64_t(blockIdx.x) * per_block + int64_t(wave) * per_wave;
+    constexpr int kEarly = 2;  // rounds whose tokens are asked for first: all of them but in very long sorts
+    uint32_t early_key[kEarly], early_tok[kEarly];
+#pragma unroll
+    for (int r = 0; r < kEarly; ++r) {
+        const int64_t i = first + r * kWave + lane;
+        const bool in = r * kWave < per_wave && i < count;
+        early_key[r] = in ? src.key(i) : 0u;
+        early_tok[r] = in ? src.tok(i) : 0u;
+    }
+    auto key_at = [&](int r, int64_t i) { return r == 0 ? early_key[0] : r == kWave ? early_key[1] : src.key(i); };
+    auto tok_at = [&](int r, int64_t i) { return r == 0 ? early_tok[0] : r == kWave ? early_tok[1] : src.tok(i); };
     // where this block's tokens of digit d start: all smaller digits, then d in earlier blocks
     uint32_t total = 0, before = 0;
 #pragma unroll 16
@@ -159,22 +174,19 @@ __global__ __launch_bounds__(kThreads) void scatter_kernel(Source<I> src, int64_
         before += b < int(blockIdx.x) ? v : 0u;
         total += v;
     }
-    scan[d] = total;
     for (int w = 0; w < kWaves; ++w) off[w][d] = 0;
-    __syncthreads();
-    for (int s = 1; s < kDigits; s *= 2) {
-        const uint32_t v = d >= s ? scan[d - s] : 0u;
-        __syncthreads();
-        scan[d] += v;
-        __syncthreads();
+    uint32_t upto = total;  // of this wave's digits up to d
+    for (int s = 1; s < kWave; s *= 2) {
+        const uint32_t v = __shfl_up(upto, s);
+        upto += lane >= s ? v : 0u;
     }
-    const uint32_t base = scan[d] - total + before;
-    // a wave's tokens are consecutive, so the order within a digit is wave, round, lane
-    const int per_wave = per_block / kWaves;
-    const int64_t first = int64_t(blockIdx.x) * per_block + int64_t(wave) * per_wave;
+    if (lane == kWave - 1) wave_sum[wave] = upto;
+    __syncthreads();
+    uint32_t base = upto - total + before;
+    for (int w = 0; w < wave; ++w) base += wave_sum[w];
     for (int r = 0; r < per_wave; r += kWave) {
         const int64_t i = first + r + lane;
-        if (i < count) atomicAdd(&off[wave][(src.key(i) >> shift) & (kDigits - 1)], 1u);
+        if (i < count) atomicAdd(&off[wave][(key_at(r, i) >> shift) & (kDigits - 1)], 1u);
     }
     __syncthreads();
     uint32_t sum = base;
@@ -187,11 +199,11 @@ __global__ __launch_bounds__(kThreads) void scatter_kernel(Source<I> src, int64_
     for (int r = 0; r < per_wave; r += kWave) {
         const int64_t i = first + r + lane;
         const bool in = i < count;
-        const uint32_t key = in ? src.key(i) : 0u;
+        const uint32_t key = in ? key_at(r, i) : 0u;
         const uint32_t at = place_in_order(off[wave], (key >> shift) & (kDigits - 1), in, lane);
         if (in) {
             keys_out[at] = key;
-            toks_out[at] = src.tok(i);
+            toks_out[at] = tok_at(r, i);
         }
     }
 }
@@ -323,19 +335,23 @@ template <int V>
 __device__ __forceinline__ void add_partials(float (&acc)[V], const float *partial, int from, int to, int first, int head,
                                              const RowSlots &rs, int64_t s)
 {
+    constexpr int kAtOnce = 8;  // on their way together; past the end the last one, not added
     const bool vec = s < rs.full;
     const float *const src = partial + (vec ? s * V : rs.full * V + (s - rs.full));
-    if (vec) {
-#pragma unroll 4
-        for (int c = from; c < to; ++c) {
-            const Raw<float, V> p =
-                *reinterpret_cast<const Raw<float, V> *>(src + (int64_t(c) * 2 + (c == first ? head : 0)) * rs.width);
+    for (int c = from; c < to; c += kAtOnce) {
+        Raw<float, V> p[kAtOnce];
 #pragma unroll
-            for (int j = 0; j < V; ++j) acc[j] += p[j];
+        for (int q = 0; q < kAtOnce; ++q) {
+            const int at = c + q < to ? c + q : to - 1;
+            const float *const one = src + (int64_t(at) * 2 + (at == first ? head : 0)) * rs.width;
+            p[q] = Raw<float, V>{};
+            if (vec) p[q] = *reinterpret_cast<const Raw<float, V> *>(one);
+            else p[q][0] = *one;
         }
-    } else {
-#pragma unroll 4
-        for (int c = from; c < to; ++c) acc[0] += src[(int64_t(c) * 2 + (c == first ? head : 0)) * rs.width];
+#pragma unroll
+        for (int q = 0; q < kAtOnce; ++q)
+#pragma unroll
+            for (int j = 0; j < V; ++j) acc[j] += c + q < to ? p[q][j] : 0.0f;
     }
 }
 
@@ -455,57 +471,63 @@ __global__ __launch_bounds__(kThreads) void chunk_kernel(const T *dy, const uint
 // of it; the rows inside a chunk are written already.  With one chunk there is no kernel
 // before this one, and a row is the sum of its tokens.  Many partial sums (a frequent row) are shared out over the block:
 // consecutive ones to each group of lanes, joined in their order.
-constexpr int kFewPartials = 4;
+constexpr int kFewPartials = 8, kBlockRows = 1024;
 template <class T, class G>
 __global__ __launch_bounds__(kThreads) void rows_kernel(const T *dy, const uint32_t *keys, const uint32_t *toks,
                                                         int64_t count, int64_t rows, int chunk, RowSlots rs, Bounds bounds,
-                                                        const float *partial, bool inner, float scale, G *dtable)
+                                                        const float *partial, bool inner, int ahead, float scale, G *dtable)
 {
     constexpr int V = ct::kVec<T>;
     __shared__ float lds[kThreads * V];
-    __shared__ int many[kThreads][4], found;  // row of the block, first and last chunk, the first's slot
+    __shared__ int low[kBlockRows], high[kBlockRows], many[kBlockRows], found;
     const int lane = threadIdx.x & (rs.lanes - 1), group = threadIdx.x / rs.lanes;
     const int groups = kThreads / rs.lanes;
-    for (int64_t v0 = int64_t(blockIdx.x) * groups; v0 < rows; v0 += int64_t(gridDim.x) * groups) {
-        const int64_t v = v0 + group;
-        int64_t lo = 0, hi = 0;
-        if (count > 0 && v < rows) {
-            const uint32_t begin = bounds.begin[v], end = bounds.end[v];
-            if (begin < uint32_t(count) && keys[begin] == uint32_t(v)) {
-                lo = begin;
-                hi = end;
+    const int64_t stride = int64_t(gridDim.x) * groups;  // from a group's row to its next
+    for (int64_t v0 = int64_t(blockIdx.x) * groups; v0 < rows; v0 += stride * ahead) {
+        __syncthreads();
+        for (int t = threadIdx.x; t < groups * ahead; t += kThreads) {
+            const int64_t v = v0 + t / groups * stride + t % groups;
+            int lo = 0, hi = 0;
+            if (count > 0 && v < rows) {
+                const uint32_t begin = bounds.begin[v], end = bounds.end[v];
+                if (begin < uint32_t(count) && keys[begin] == uint32_t(v)) {
+                    lo = int(begin);
+                    hi = int(end);
+                }
             }
+            low[t] = lo;
+            high[t] = hi;
         }
-        const int c0 = int(lo / chunk), c1 = hi > lo ? int((hi - 1) / chunk) : c0;
-        const int head = lo > int64_t(c0) * chunk ? 1 : 0;
-        const bool shared = c1 - c0 >= kFewPartials;
         if (threadIdx.x == 0) found = 0;
         __syncthreads();
-        if (shared && lane == 0) {
-            const int at = atomicAdd(&found, 1);  // any order: each row is summed by itself
-            many[at][0] = group;
-            many[at][1] = c0;
-            many[at][2] = c1;
-            many[at][3] = head;
-        }
-        if (v < rows && !shared && !(inner && hi > lo && c0 == c1)) {
+        for (int q = 0; q < ahead; ++q) {
+            const int t = q * groups + group;
+            const int64_t v = v0 + q * stride + group;
+            if (v >= rows) break;
+            const int lo = low[t], hi = high[t], c0 = lo / chunk, c1 = hi > lo ? (hi - 1) / chunk : c0;
+            if (inner && hi > lo && c0 == c1) continue;
+            if (c1 - c0 >= kFewPartials) {
+                if (lane == 0) many[atomicAdd(&found, 1)] = t;  // any order: each row is summed by itself
+                continue;
+            }
             G *const dst = dtable + v * rs.width;
             for (int64_t s = lane; s < rs.slots; s += rs.lanes) {
                 float acc[V] = {};
                 if (hi > lo && c0 == c1) add_rows<4, T, V>(acc, dy, toks, lo, hi, rs, s);
-                else if (hi > lo) add_partials<V>(acc, partial, c0, c1 + 1, c0, head, rs, s);
+                else if (hi > lo) add_partials<V>(acc, partial, c0, c1 + 1, c0, lo > c0 * chunk ? 1 : 0, rs, s);
                 store_slot<G, V>(dst, rs, s, acc, scale);
             }
         }
         __syncthreads();
         for (int m = 0; m < found; ++m) {
-            const int first = many[m][1], n = many[m][2] - first + 1, share = (n + groups - 1) / groups;
+            const int t = many[m], first = low[t] / chunk, n = (high[t] - 1) / chunk - first + 1;
+            const int share = (n + groups - 1) / groups, head = low[t] > first * chunk ? 1 : 0;
             const int from = group * share < n ? group * share : n, to = from + share < n ? from + share : n;
-            G *const dst = dtable + (v0 + many[m][0]) * rs.width;
+            G *const dst = dtable + (v0 + t / groups * stride + t % groups) * rs.width;
             for (int64_t s0 = 0; s0 < rs.slots; s0 += rs.lanes) {
                 const int64_t s = s0 + lane;
                 float acc[V] = {};
-                if (s < rs.slots) add_partials<V>(acc, partial, first + from, first + to, first, many[m][3], rs, s);
+                if (s < rs.slots) add_partials<V>(acc, partial, first + from, first + to, first, head, rs, s);
                 __syncthreads();
 #pragma unroll
                 for (int j = 0; j < V; ++j) lds[threadIdx.x * V + j] = acc[j];
@@ -518,7 +540,6 @@ __global__ __launch_bounds__(kThreads) void rows_kernel(const T *dy, const uint3
                 }
             }
         }
-        __syncthreads();
     }
 }
 
@@ -544,13 +565,13 @@ GradPlan grad_plan(int64_t tokens, int64_t rows, int64_t width)
     g.per_block = int(per);
     g.sort_blocks = int((tokens + per - 1) / per);
     g.one_sort = tokens <= kOneSort;
-    // Short chunks spread a frequent row over many blocks, long ones leave fewer partial sums of
-    // it to add (float16, ids by 1/rank, us at 32 / 64 / 128 / 256 tokens a chunk: 32768 tokens x
-    // 512 46.4 / 47.8 / 54.9 / 67.7, 60000 x 256 55.2 / 51.4 / 55.7 / 70.8, 400000 x 64 168 /
-    // 132 / 114 / -).  Up to 512 tokens a row's sum is left to the threads of that row (257
-    // tokens x 77: 11.8 against 14.6 with chunks of 64).
-    g.chunk = 64;
-    while (g.chunk < kMostChunk && int64_t(g.chunk) * g.chunk * 32 < tokens) g.chunk *= 2;
+    // Short chunks spread the sums over many blocks, long ones leave fewer partial sums of a
+    // frequent row to add (ids by 1/rank, us at 32 / 64 / 128 / 256 tokens a chunk: 2000 tokens x
+    // 1024 bfloat16 24.0 / 26.5 / 31.6 / 41.0; float16 32768 x 512 39.6 / 39.4 / 42.0 / 51.3,
+    // 60000 x 256 48.1 / 44.9 / 45.1 / 48.8, 400000 x 64 120 / 91 / 76 / 69).  Up to 512 tokens the
+    // rows' own threads add them and a launch is saved (500 tokens x 256 12.9 against 17.7).
+    g.chunk = 32;
+    while (g.chunk < kMostChunk && int64_t(g.chunk) * g.chunk * 16 < tokens) g.chunk *= 2;
     if (tokens <= 512) g.chunk = 512;
     g.chunks = (tokens + g.chunk - 1) / g.chunk;
     size_t at = 0;
@@ -711,8 +732,15 @@ ct_status embedding_backward_nd(ct_dtype dtype, ct_dtype index_dtype, int64_t to
             if (inner)
                 chunk_kernel<T, G><<<blocks_for(work, 1), kThreads, 0, hs>>>(dyp, keys, toks, tokens, rows, g.chunk, rs, steps,
                                                                             work, bounds, partial, scale, grad);
-            rows_kernel<T, G><<<blocks_for(rows, kThreads / rs.lanes), kThreads, 0, hs>>>(
-                dyp, keys, toks, tokens, rows, g.chunk, rs, bounds, partial, inner, scale, grad);
+            // Where the table is long a block takes several rows in turn, so that few rounds of
+            // blocks wait for begin and end (float16, us at 2 / 4 / 8 / 16 rows: 2000 tokens into
+            // 128000 x 512 69.9 / 65.2 / 58.7 / 55.3, 32768 into 16384 x 512 40.0 / 39.1 / 40.3 /
+            // 44.1; 400000 into 30000 x 64 at 1 / 2 / 4 71.2 / 71.8 / 74.2): as many as leave 1024
+            // blocks, at most 16.
+            const int64_t groups = kThreads / rs.lanes, turns = std::min({rows / (groups * 1024), kBlockRows / groups, int64_t(16)});
+            const int ahead = int(std::max(turns, int64_t(1)));
+            rows_kernel<T, G><<<blocks_for(rows, int(groups) * ahead), kThreads, 0, hs>>>(
+                dyp, keys, toks, tokens, rows, g.chunk, rs, bounds, partial, inner, ahead, scale, grad);
             ct::mark_after(hs);
         };
         if (gt == CT_FLOAT32) go(static_cast<float *>(dtable));
