@@ -393,6 +393,28 @@ def test_embedding_gradient_sums_in_token_order(T):
     assert np.array_equal(host(got), want)
 
 
+@pytest.mark.parametrize("tokens,rows,width,top", [
+    (513, 20000, 260, 3), (4096, 9000, 512, 9000), (5000, 50, 1030, 50), (9000, 40000, 8, 900), (2000, 30000, 300, 1),
+    (20000, 5, 100, 5),
+])
+def test_embedding_gradient_of_tokens_without_a_row(T, tokens, rows, width, top):
+    """Sums of small whole numbers are exact, and what padding or an id outside the table has for a
+    gradient (NaN here) goes nowhere; rows without tokens, the last ones too, are zeros."""
+    rng = np.random.default_rng(tokens)
+    ids = np.minimum((top + 1) ** rng.random(tokens) - 1, top - 1).astype(np.int64)
+    ids[rng.random(tokens) < 0.2] = -5
+    ids[rng.random(tokens) < 0.2] = rows
+    padding = top // 2
+    dy = rng.integers(-2, 3, size=(tokens, width)).astype(np.float64)
+    none = (ids < 0) | (ids >= rows) | (ids == padding)
+    want, _ = R.embedding_grad(np.where(none[:, None], 0.0, dy), ids, rows, 1.0, padding)
+    dy[none] = np.nan
+    for dtype in ("f32", "f16"):
+        d = torch.from_numpy(dy).to(DT[dtype]).cuda()
+        got = T.embedding_backward_nd(d, torch.from_numpy(ids).cuda(), rows, padding_idx=padding, grad_dtype=DT["f32"])
+        assert np.array_equal(host(got), want), dtype
+
+
 def test_embedding_gradient_against_differences(T):
     """The lookup is linear: sum(w y(table + h u)) changes by h <gradient, u> exactly."""
     gen = torch.Generator(device="cuda").manual_seed(4)
@@ -482,6 +504,25 @@ def test_prepared_and_captured_calls(T):
             assert torch.equal(got, w), k
         seen.append(outputs()[0].clone())
     assert not torch.equal(seen[0], seen[1])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("shape,groups", [((2, 16, 10, 9), 4), ((1, 24, 40000), 3), ((2, 9, 77), 3)])
+def test_dropped_gradients_may_be_anything(T, shape, groups, dtype):
+    """A value of dy that dropout hides adds nothing, infinite or NaN: the gradients are those of 0."""
+    gen = torch.Generator(device="cuda").manual_seed(6)
+    store = (shape[0],) + shape[2:] + (shape[1],)
+    x, dy = (torch.randn(store, generator=gen, device="cuda").to(DT[dtype]).movedim(-1, 1) for _ in range(2))
+    gamma = torch.rand(shape[1], generator=gen, device="cuda") + 0.5
+    kw = dict(activation="silu", dropout_p=0.3, seed=11, offset=5)
+    _, mean, rstd = T.group_norm_nd(x, groups, gamma, gamma, **kw)
+    keep = torch.from_numpy(R.keep_mask(x.numel(), 0.3, 11, 5)).cuda().reshape(store).movedim(-1, 1)
+    zero, bad = torch.where(keep, dy, 0), torch.where(keep, dy, float("nan"))
+    bad[0, 0] = torch.where(keep[0, 0], dy[0, 0], float("-inf"))
+    want = T.group_norm_backward_nd(zero, x, mean, rstd, groups, gamma, gamma, **kw)
+    got = T.group_norm_backward_nd(bad, x, mean, rstd, groups, gamma, gamma, **kw)
+    for w, g in zip(want, got):
+        assert torch.isfinite(w).all() and torch.equal(w, g)
 
 
 def test_offsets_beyond_32_bits(T):
