@@ -50,6 +50,10 @@ RowSlots row_slots(int64_t width)
     return r;
 }
 
+// The lookup: up to a wave's lanes share a row, 16 bytes each, and a block's rows are
+// consecutive tokens, so y is written in one stream.  Bound by memory: 32768 rows of 512
+// float16 (1 KB each) out of 16384 take 10.2 us, 42.7 MB, 4.2 TB/s; the id is one more read
+// in front of the row's, which the block's other waves hide.  One token is a launch, 4.4 us.
 template <class T, class I>
 __global__ __launch_bounds__(kThreads) void lookup_kernel(const I *ids, const T *table, T *y, int64_t tokens,
                                                           int64_t rows, RowSlots rs, float scale)
@@ -79,6 +83,13 @@ __global__ __launch_bounds__(kThreads) void lookup_kernel(const I *ids, const T 
 
 // ------------------------------------------------------------------------------------
 // The gradient: a stable radix sort of (id, token) by 8 bits a pass, then the rows' sums
+//
+// Sorted, a row's tokens stand together in ascending order: every row of dy is read once,
+// every row of the table is written once, and no sum depends on which block came first.
+// 32768 tokens of 512 float16 into 16384 rows (50.6 MB) take 38.2 us: two sorting passes
+// 17.7 (counts 2.7 and moves 6.2 each), the chunks 13.2, the rows 10.0.  The sort and the rows
+// are bound by chains of dependent reads (an id to a place, a row's begin to its key to its
+// partial sums) of about a microsecond a link, not by bytes; the chunks by memory.
 // ------------------------------------------------------------------------------------
 constexpr int kDigits = 256;
 constexpr int kMaxSortBlocks = 256;
@@ -102,6 +113,8 @@ struct Source {
     __device__ __forceinline__ uint32_t tok(int64_t i) const { return keys ? toks[i] : uint32_t(i); }
 };
 
+// One pass is two kernels: how many tokens of each digit a block has, then, with all blocks'
+// counts, where each of its tokens goes.
 template <class I>
 __global__ __launch_bounds__(kThreads) void histogram_kernel(Source<I> src, int64_t count, int per_block, int shift,
                                                              uint32_t *hist)
@@ -222,7 +235,10 @@ struct Bounds {
     }
 };
 
-// Up to kOneSort tokens: the whole sort in one block's LDS, one launch instead of two a pass.
+// Up to kOneSort tokens (their keys and places twice fill 64 KB of LDS): the whole sort in one
+// block, one launch instead of two a pass.  The whole gradient, one block / kernels a pass, us:
+// 600 tokens into 8000 rows 17.4 / 24.1, 2000 20.2 / 26.6, 4000 24.4 / 29.2, 4000 into 200 rows
+// (one pass) 19.0 / 19.7.
 constexpr int kOneSort = 4096, kSortThreads = 1024;
 template <class I>
 __global__ __launch_bounds__(kSortThreads) void one_sort_kernel(Source<I> src, int count, int passes, bool mark, Bounds bounds,
@@ -374,6 +390,9 @@ __device__ __forceinline__ void store_slot(G *dst, const RowSlots &rs, int64_t s
 // share is stored at once, those at a share's borders are joined in their order over LDS, and
 // of a row that crosses a chunk's border every chunk leaves a partial sum, in slot 0 of the
 // chunk for a row that is there from its start and in slot 1 for one that begins later.
+// The work is cut by tokens, so a frequent row and many rare ones take the same time; the
+// kernel reads all of dy: 33.5 MB and 9 MB of the table's rows in 13.2 us, 3.2 TB/s (16
+// rows on their way: 14.2).
 constexpr int kMostChunk = 1024;
 template <class T, class G>
 __global__ __launch_bounds__(kThreads) void chunk_kernel(const T *dy, const uint32_t *keys, const uint32_t *toks,
@@ -471,6 +490,7 @@ __global__ __launch_bounds__(kThreads) void chunk_kernel(const T *dy, const uint
 // of it; the rows inside a chunk are written already.  With one chunk there is no kernel
 // before this one, and a row is the sum of its tokens.  Many partial sums (a frequent row) are shared out over the block:
 // consecutive ones to each group of lanes, joined in their order.
+// kFewPartials: as many as are on their way together (4 / 16: 39.4 / 39.6 us for 32768 x 512).
 constexpr int kFewPartials = 8, kBlockRows = 1024;
 template <class T, class G>
 __global__ __launch_bounds__(kThreads) void rows_kernel(const T *dy, const uint32_t *keys, const uint32_t *toks,
