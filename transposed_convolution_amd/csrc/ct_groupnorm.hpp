@@ -317,6 +317,9 @@ struct Call {
 // Threads of a block and tiles held at once.  Statistics: 512 threads of 128 registers, 64 of
 // which hold 16 vectors, so a compute unit has 256 KB of x on its way.  `one`: the kernels
 // in which a block has all positions of its groups.
+// Chunks of up to kStatShort tiles take a kernel that holds as many (its load, of tiles that are
+// not there, and its arithmetic cost the longer one 19.2 against 15.5 us in an 8 x 256 x 2304
+// float16 call, 14.4 against 12.2 in a 4 x 36 x 1001 float32 one).
 constexpr int kStatThreads = 512, kStatTiles = 16, kStatShort = 4;
 constexpr int kApplyThreads = 256, kApplyTiles = 4;
 constexpr int kOneThreads = 512, kOneGradThreads = 256, kOneTiles = 4;

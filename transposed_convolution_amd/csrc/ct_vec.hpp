@@ -119,8 +119,9 @@ struct Param {
 //
 // 16 bits an element: one block serves a 16-byte vector of the 16-bit types.  A block takes
 // 274 cycles of a SIMD for a wave (20 wide integer multiplies are most of it), 353 with the
-// eight compares: for 33.5 M elements 13 and 17 us of the whole chip, under a pass of 36 us
-// that is bound by memory.  With 32 bits an element it would be as long as the memory's time.
+// eight compares: for 33.5 M elements 9 us of the whole chip, hidden under a pass that is bound
+// by memory.  With 32 bits an element it would be nearly twice that in both passes of the
+// norm's gradient, whose vector units are 70 % busy as it is.
 // ------------------------------------------------------------------------------------
 struct Dropout {
     uint32_t threshold = 0;          // 0: no dropout
