@@ -392,7 +392,7 @@ __device__ __forceinline__ void store_slot(G *dst, const RowSlots &rs, int64_t s
 // chunk for a row that is there from its start and in slot 1 for one that begins later.
 // The work is cut by tokens, so a frequent row and many rare ones take the same time; the
 // kernel reads all of dy: 33.5 MB and 9 MB of the table's rows in 13.2 us, 3.2 TB/s (16
-// rows on their way: 14.2).
+// rows on their way made the whole gradient 40.5 us instead of 39.4).
 constexpr int kMostChunk = 1024;
 template <class T, class G>
 __global__ __launch_bounds__(kThreads) void chunk_kernel(const T *dy, const uint32_t *keys, const uint32_t *toks,
