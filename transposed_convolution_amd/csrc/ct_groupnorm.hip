@@ -95,9 +95,11 @@ bool cut_tiles(const Sizes &s, int V, int threads, int64_t most_groups, Cut *k)
 
 int64_t tiles_of(const Cut &k) { return (k.P + k.rows - 1) / k.rows; }
 
-// Chunks of about `tiles` tiles.
+// Chunks of about `tiles` tiles, at most 2^30: tiles and chunks fit 32 bits for every size that is
+// let through (2^58 elements), as a query for a workspace may name sizes no memory holds.
 void cut_chunks(Cut *k, int64_t tiles)
 {
+    tiles = std::min(tiles, int64_t(1) << 30);
     const int64_t all = tiles_of(*k), chunks = (all + tiles - 1) / tiles;
     k->tiles = int((all + chunks - 1) / chunks);
     k->chunks = int((all + k->tiles - 1) / k->tiles);
@@ -115,6 +117,8 @@ constexpr int64_t kOneBytes = 32 << 20, kOneGradBytes = 16 << 20;
 int64_t line_bytes(const Sizes &s, const Cut &k, bool backward)
 {
     const int64_t run = int64_t(k.width) * int64_t(ct::float_size(s.dt));
+    const int64_t dense = s.N * s.P * s.C * int64_t(ct::float_size(s.dt));  // no line is read less than once
+    if (dense > kOneBytes) return dense;
     const int64_t lines = s.N * s.P * ((s.C + k.width - 1) / k.width) * ((run + 127) / 128 * 128);
     return backward ? 2 * lines : lines;
 }
