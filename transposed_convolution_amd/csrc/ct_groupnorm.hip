@@ -212,11 +212,7 @@ ct_status check_sizes(int dt, int nsp, const int64_t *shape, int64_t groups, Siz
     }
     for (int a = 0; a < nsp; ++a) s->P *= shape[2 + a];
     if (groups < 1 || s->C % groups != 0) return fail(CT_EINVAL, "groups must be at least 1 and divide the channels");
-    // a launch holds fewer than 2^32 threads; the smallest work item of a channel tile is a
-    // block of 1024 and that of a group a wave
-    const int64_t tiles = s->C / 64 + 1;
-    if (s->C > (1 << 30) || s->N > (int64_t(1) << 21) / tiles || (s->N > 0 && groups > (int64_t(1) << 25) / s->N))
-        return fail(CT_EUNSUPPORTED, "more than 2^21 images times tiles of 64 channels, or 2^25 images times groups");
+    if (s->C > (1 << 30)) return fail(CT_EUNSUPPORTED, "more than 2^30 channels");
     return CT_OK;
 }
 
@@ -247,13 +243,22 @@ ct_status check_params(int dt, int pt, const void *gamma, const void *beta)
     return CT_OK;
 }
 
-// A launch holds fewer than 2^32 threads.
-ct_status check_blocks(const Sizes &s, const Plan &p)
+// A launch holds fewer than 2^32 threads; here each of the call's launches at most 2^31: the two
+// passes (512 threads a block in the forward call's first one, else 256), the blocks for the
+// parameters' gradients that go before the second, and a wave a group where the parts are
+// joined between.
+ct_status check_launches(const Sizes &s, const Plan &p, bool backward)
 {
-    const int64_t most = int64_t(1) << 22;
-    const int64_t a = int64_t(p.a.chunks) * p.a.slabs, b = int64_t(p.s.chunks) * p.s.slabs;
-    if (a > most / s.N || b > most / s.N || s.G > (most * 4) / s.N)
-        return fail(CT_EUNSUPPORTED, "more than 2^22 blocks: too many images times groups");
+    constexpr int64_t most = int64_t(1) << 31;
+    const int64_t head = backward ? param_blocks(s.C) : 0;
+    int64_t first = 0, second = 0;
+    if (!s.empty()) {
+        first = s.N * p.s.chunks * p.s.slabs;
+        second = s.N * p.a.chunks * p.a.slabs;
+    }
+    if (first > most / (backward ? kGradThreads : kStatThreads) || second > most / kApplyThreads - head ||
+        (p.finish && s.N * s.G > most / 64))
+        return fail(CT_EUNSUPPORTED, "more than 2^31 threads in a launch: too many images, channels or groups");
     return CT_OK;
 }
 
@@ -280,8 +285,10 @@ ct_status group_norm_workspace_size(ct_dtype dtype, int nsp, const int64_t *x_sh
     Sizes s;
     const ct_status st = check_sizes(ct::enum_int(dtype), nsp, x_shape, groups, &s);
     if (st != CT_OK) return st;
-    *bytes_out = make_plan(s, backward != 0).bytes;
-    return CT_OK;
+    const Plan p = make_plan(s, backward != 0);
+    const ct_status ls = check_launches(s, p, backward != 0);
+    if (ls == CT_OK) *bytes_out = p.bytes;
+    return ls;
 }
 
 ct_status group_norm_nd(ct_dtype dtype, int nsp, const void *x, const int64_t *x_shape, int64_t groups,
@@ -310,7 +317,7 @@ ct_status group_norm_nd(ct_dtype dtype, int nsp, const void *x, const int64_t *x
     if (s.empty()) return CT_OK;
     if (!x || !y) return fail(CT_EINVAL, "x or y is NULL");
     const Plan p = make_plan(s, false);
-    st = check_blocks(s, p);
+    st = check_launches(s, p, false);
     if (st != CT_OK) return st;
     const hipStream_t hs = static_cast<hipStream_t>(stream);
     ct::Scratch ws;
@@ -362,14 +369,14 @@ ct_status group_norm_backward_nd(ct_dtype dtype, int nsp, const void *dy, const 
     const hipStream_t hs = static_cast<hipStream_t>(stream);
     if (s.C == 0) return CT_OK;
     if (!s.empty() && (!x || !dy || !dx || !mean || !rstd)) return fail(CT_EINVAL, "x, dy, dx, mean or rstd is NULL");
+    const Plan p = make_plan(s, true);
+    st = check_launches(s, p, true);
+    if (st != CT_OK) return st;
     if (s.empty()) {  // no element: the parameters' gradients are 0
         if (dgamma || dbeta) launch_no_gradient(dt, pt == CT_FLOAT32, int(s.C), dgamma, dbeta, hs);
         st = ct::launch_status("group norm gradient launch failed", &err);
         return st == CT_OK ? CT_OK : fail(st, err);
     }
-    const Plan p = make_plan(s, true);
-    st = check_blocks(s, p);
-    if (st != CT_OK) return st;
     ct::Scratch ws;
     st = ws.take(workspace, workspace_bytes, p.bytes, hs, &err);
     if (st != CT_OK) return fail(st, err);

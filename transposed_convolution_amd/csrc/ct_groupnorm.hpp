@@ -324,6 +324,8 @@ constexpr int kStatThreads = 512, kStatTiles = 16, kStatShort = 4;
 constexpr int kApplyThreads = 256, kApplyTiles = 4;
 constexpr int kOneThreads = 512, kOneGradThreads = 256, kOneTiles = 4;
 constexpr int kGradThreads = 256, kGradTiles = 4;
+// Blocks that make dgamma and dbeta, 16 channels each.
+inline int64_t param_blocks(int64_t C) { return (C + 15) / 16; }
 
 struct Plan {
     bool vec = true;   // 16-byte vectors, else single elements

@@ -375,7 +375,7 @@ void ct::norm::launch_gradient(const Call &c, const Plan &p, char *ws, hipStream
     float2 *const coef = reinterpret_cast<float2 *>(ws + p.stats);
     float2 *const sums = reinterpret_cast<float2 *>(ws + p.sums);
     const bool params = c.dgamma || c.dbeta;
-    const int head = params ? (p.a.C + 15) / 16 : 0;
+    const int head = params ? int(param_blocks(p.a.C)) : 0;
     const int64_t groups = c.N * p.a.G, blocks = c.N * p.a.chunks * p.a.slabs;
     with_type(c.dt, [&](auto t) {
         using T = decltype(t);
@@ -418,6 +418,6 @@ void ct::norm::launch_gradient(const Call &c, const Plan &p, char *ws, hipStream
 void ct::norm::launch_no_gradient(int dt, bool params_f32, int C, void *dgamma, void *dbeta, hipStream_t st)
 {
     with_type(dt, [&](auto t) {
-        param_kernel<decltype(t)><<<unsigned((C + 15) / 16), 256, 0, st>>>(nullptr, 0, C, params_f32, dgamma, dbeta);
+        param_kernel<decltype(t)><<<unsigned(param_blocks(C)), 256, 0, st>>>(nullptr, 0, C, params_f32, dgamma, dbeta);
     });
 }
