@@ -407,7 +407,9 @@ int convtranspose_igemm_tile(void);
  *   param_dtype    type of gamma and beta: dtype or CT_FLOAT32
  *   gamma, beta    device arrays of C values, or NULL (1 and 0)
  *   eps            finite, not negative
- *   activation     any ct_activation; act_p0 / act_p1 as for convtranspose_nd_fused
+ *   activation     any ct_activation; act_p0 / act_p1 as for convtranspose_nd_fused.  A NaN stays
+ *                  NaN, under ReLU too: a group with a value that is not finite has no
+ *                  statistics, and all its outputs that are not dropped are NaN
  *   dropout_p, seed, offset, step   dropout of the activation's output, as dropout_nd with
  *                  the elements numbered in y's storage order; 0 for none
  *   mean, rstd     device float32 arrays of N * groups values that receive the statistics
@@ -432,7 +434,7 @@ ct_status group_norm_nd(ct_dtype dtype, int nsp, const void *x, const int64_t *x
  *   dbeta[c] = sum of dz, dgamma[c] = sum of dz * xhat   over images and positions
  *   dx = rstd * (dz * gamma - average(dz * gamma) - xhat * average(dz * gamma * xhat)),
  * the averages over the group.  act' at a kink: ReLU 0 at 0, leaky ReLU 1 at 0, clip 1 at
- * both bounds.
+ * both bounds; NaN where z is, but for the identity.
  *   dy, x, dx      stored as for group_norm_nd; dx may be dy or x itself
  *   mean, rstd     what group_norm_nd wrote for this x
  *   dgamma, dbeta  device arrays of C values of param_dtype, or NULL; with an empty x they

@@ -38,15 +38,24 @@ struct Silu {
         return __builtin_fmaf(z * s, 1.0f - s, s);
     }
 };
+// A NaN stays NaN in both, ReLU's comparison included: a group with a value that is not finite
+// is not to leave as zeros.
 struct Piecewise {
     ct::Act a;
-    __device__ __forceinline__ float y(float z) const { return a(z); }
+    __device__ __forceinline__ float y(float z) const
+    {
+        const float relu = z <= 0.0f ? 0.0f : z;
+        const float leaky = z >= 0.0f ? z : a.p0 * z;
+        const float clip = z < a.p0 ? a.p0 : (z > a.p1 ? a.p1 : z);
+        return a.kind == CT_ACT_RELU ? relu : a.kind == CT_ACT_LEAKY_RELU ? leaky : a.kind == CT_ACT_CLIP ? clip : z;
+    }
     __device__ __forceinline__ float d(float z) const
     {
         const float relu = z > 0.0f ? 1.0f : 0.0f;
         const float leaky = z >= 0.0f ? 1.0f : a.p0;
         const float clip = z >= a.p0 && z <= a.p1 ? 1.0f : 0.0f;
-        return a.kind == CT_ACT_RELU ? relu : a.kind == CT_ACT_LEAKY_RELU ? leaky : a.kind == CT_ACT_CLIP ? clip : 1.0f;
+        const float d = a.kind == CT_ACT_RELU ? relu : a.kind == CT_ACT_LEAKY_RELU ? leaky : clip;
+        return a.identity() ? 1.0f : z == z ? d : z;
     }
 };
 template <class F>
