@@ -1,9 +1,11 @@
 """Group norm where float32 arithmetic can go wrong: values that are not finite, under every
-activation."""
+activation, and single values far from all others."""
+import numpy as np
 import pytest
 import torch
 
-from test_gpu_layers import ACTS, T, norm_inputs, path  # noqa: F401
+import layer_refs as R
+from test_gpu_layers import ACTS, T, host, norm_inputs, path, rows_of  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -32,3 +34,31 @@ def test_a_diverged_group_is_seen(T, path, kind, params, bad):
     for got, want in ((dgamma, grads[1]), (dbeta, grads[2])):
         for part in (slice(0, 8), slice(16, 32)):
             assert torch.equal(got[part], want[part])
+
+
+@pytest.mark.parametrize("far", [1e3, -1e5])
+@pytest.mark.parametrize("where", ["first", "last"])
+@pytest.mark.parametrize("shape", [(2, 32, (9, 7), 4), (1, 12, (3001,), 2), (1, 256, (64, 64), 32), (1, 24, (20011,), 3),
+                                   (2, 64, (4, 6, 5), 1), (1, 4104, (3, 3), 1), (2, 1001, (13,), 7), (5, 8, (129,), 2)])
+def test_group_norm_one_value_far_from_the_others(T, path, shape, where, far):
+    """Standard normals and one large value a group, the first or the last of it.
+
+    The large value A leaves the group of n values a spread s of A / sqrt(n).  What it costs are
+    roundings of A in the few values that are summed next to it, at most 2^-24 A a value, and
+    those are few of the n: together less than 2^-24 s.  The mean of the group comes to a few
+    2^-24 of itself and of s, and so does each x - mean."""
+    n, c, dims, groups = shape
+    rng = np.random.default_rng(17)
+    xv = rng.normal(size=(n,) + dims + (c,)).astype(np.float32)
+    by_group = xv.reshape(n, -1, groups, c // groups)
+    by_group[:, 0 if where == "first" else -1, :, 0 if where == "first" else -1] = far
+    x = torch.from_numpy(xv).cuda().movedim(-1, 1)
+    y, mean, rstd = T.group_norm_nd(x, groups, eps=0.0)
+    v = by_group.astype(np.float64)
+    m, s = v.mean((1, 3)), v.std((1, 3))
+    assert (np.abs(host(mean) - m) <= 4 * R.EPS * (np.abs(m) + s)).all(), np.abs(host(mean) - m).max()
+    assert (np.abs(host(rstd) * s - 1) <= R.FACTOR * R.EPS).all()
+    wide = lambda a: a[:, None, :, None]  # noqa: E731
+    z = (v - wide(m)) / wide(s)
+    bound = (8 * (1 + np.abs(wide(m)) / wide(s)) + R.FACTOR * np.abs(z)) * R.EPS
+    assert (np.abs(rows_of(y).reshape(v.shape) - z) <= bound).all()

@@ -12,9 +12,10 @@
 //
 // Statistics: a thread takes the mean and the sum of squared distances from it of the
 // values it holds, and such triples (count, mean, m2) are joined pairwise (Chan, Golub,
-// LeVeque 1983).  The values are first taken relative to the group's first one, so a mean
-// far from zero costs no digits of the spread around it.
-// Everything is float32 between the one load and the one store of an element.
+// LeVeque 1983).  A thread takes its values relative to its own first one, so a mean far from
+// zero costs no digits of the spread around it, and a value far from the others costs digits
+// of the few values only that share its thread; the joins hold means in 64 bits.
+// Everything else is float32 between the one load and the one store of an element.
 //
 // Both directions need every value of a group before the first output.  Small groups fit the
 // registers of one block, which reads them once; for the others a first pass over the
@@ -103,6 +104,8 @@ void cut_chunks(Cut *k, int64_t tiles)
     const int64_t all = tiles_of(*k), chunks = (all + tiles - 1) / tiles;
     k->tiles = int((all + chunks - 1) / chunks);
     k->chunks = int((all + k->tiles - 1) / k->tiles);
+    k->last_tiles = int(all - int64_t(k->chunks - 1) * k->tiles);
+    k->last_rows = int(k->P - (all - 1) * k->rows);
 }
 
 // One block for a group's slab where a thread holds at most four vectors and the reads stay
@@ -183,7 +186,6 @@ Plan make_plan(const Sizes &s, bool backward)
     p.part = place(size_t(s.N) * s.G * p.s.chunks * p.s.split * 8);
     p.stats = place(size_t(s.N) * s.G * 8);
     if (backward) p.sums = place(size_t(s.N) * p.s.chunks * s.C * 8);
-    else p.pivot = place(size_t(s.N) * s.G * 4);
     p.bytes = at;
     return p;
 }

@@ -12,16 +12,23 @@
 namespace ct {
 namespace norm {
 
-// (count, mean, sum of squared distances from the mean)
+// (count, mean, sum of squared distances from the mean).  A thread's own are in float32, its mean
+// relative to a value of its own (Moments<float>); where those of threads and blocks are
+// joined, means are absolute and 64 bits wide, so that neither a mean far from zero nor a
+// single value far from the others costs digits (Moments<double>).
+template <class M>
 struct Moments {
-    float n = 0.0f, mean = 0.0f, m2 = 0.0f;
-    __device__ __forceinline__ void join(float bn, float bmean, float bm2)
+    float n = 0.0f;
+    M mean = 0;
+    float m2 = 0.0f;
+    __device__ __forceinline__ void join(float bn, M bmean, float bm2)
     {
         const float total = n + bn;
         if (bn > 0.0f) {
-            const float d = bmean - mean, w = bn * __builtin_amdgcn_rcpf(total);  // counts: one rounding more is nothing
-            mean += d * w;
-            m2 += bm2 + d * d * n * w;
+            const float d = float(bmean - mean);
+            const float w = bn * __builtin_amdgcn_rcpf(total);  // counts: one rounding more is nothing
+            mean = n > 0.0f ? mean + M(d * w) : bmean;
+            m2 += n > 0.0f ? bm2 + d * d * n * w : bm2;
             n = total;
         }
     }
@@ -123,6 +130,7 @@ struct Cut {
     int per;           // groups of a slab
     int split;         // slabs of a group: 1, or more when a group is wider than a slab
     int rows, tiles, chunks;
+    int last_tiles, last_rows;  // tiles of the last chunk, positions of its last tile
     int lanes;  // threads that share a group when partials are joined: a power of two
 
     __host__ __device__ int64_t span() const { return int64_t(tiles) * rows; }  // positions of a chunk
@@ -220,7 +228,7 @@ struct Place {
 template <int S, int V>
 constexpr int kOwn = V / S;
 template <int S, int V>
-using OwnMoments = Moments[kOwn<S, V>];
+using OwnMoments = Moments<float>[kOwn<S, V>];
 template <int S, int V>
 using OwnFloats = float[kOwn<S, V>];
 template <int THREADS, int S, int V>
@@ -251,6 +259,17 @@ __device__ __forceinline__ Raw<T, V> held(Held<V> &b)
 // Keeps the compiler from working on several tiles at a time, whose temporaries would not
 // fit the registers; other waves fill the gaps.
 __device__ __forceinline__ void one_by_one() { __builtin_amdgcn_sched_barrier(0); }
+
+// What a thread's moments are relative to: the first value of each of its runs.  A first tile
+// in which a run does not exist has none of it anywhere.
+template <class T, int V, int S>
+__device__ __forceinline__ void first_values(OwnFloats<S, V> &pivot, const Held<V> &b)
+{
+    Raw<T, V> r;
+    __builtin_memcpy(&r, &b, sizeof(T) * V);
+#pragma unroll
+    for (int a = 0; a < V / S; ++a) pivot[a] = float(r[a * S]);
+}
 
 // The thread's moments over `tiles` tiles, updated tile by tile: get(i) is tile i's vector,
 // valid(i) how much of it exists.  An element that exists in a tile exists in all tiles
@@ -344,7 +363,7 @@ struct Plan {
     bool finish = false;  // many parts a group: a kernel joins them before the second pass
     Cut s, a;          // the pass for the statistics, the pass that writes (or the only one)
     // places in the workspace (bytes)
-    size_t part = 0, pivot = 0, stats = 0, sums = 0, bytes = 0;
+    size_t part = 0, stats = 0, sums = 0, bytes = 0;
 };
 
 void launch_forward(const Call &c, const Plan &p, char *ws, hipStream_t st);

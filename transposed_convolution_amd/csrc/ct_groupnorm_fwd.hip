@@ -12,47 +12,34 @@ using namespace ct::norm;
 using ct::Dropout;
 using ct::Raw;
 
-// What a group's moments are relative to: its first value.
-template <class T>
-__device__ __forceinline__ float pivot_of(const T *x, const Cut &k, int64_t n, int g)
-{
-    return float(x[n * k.P * k.C + int64_t(g) * k.Cg]);
-}
-
-// Joins the block's triples of each group of the slab and calls out(group of the slab,
-// moments), on one thread a group.
+// Joins the block's moments of each group of the slab and calls out(group of the slab,
+// moments), on one thread a group.  How many values a run has follows from its row.
 template <int THREADS, int V, int S, class Out>
-__device__ __forceinline__ void join_block(const Cut &k, const Place<V> &pl, const OwnMoments<S, V> &m,
-                                           JoinBuffer<THREADS, S, V> &lds, Out out)
+__device__ __forceinline__ void join_block(const Cut &k, const Place<V> &pl, const OwnFloats<S, V> &pivot,
+                                           const OwnMoments<S, V> &m, JoinBuffer<THREADS, S, V> &lds, Out out)
 {
-    constexpr int A = kOwn<S, V>, unit = S;  // elements a triple stands for
+    constexpr int A = kOwn<S, V>, unit = S;  // elements a run has in a tile
     if (pl.active) {
 #pragma unroll
         for (int a = 0; a < A; ++a) {
-            lds[0][threadIdx.x * A + a] = m[a].n;
+            lds[0][threadIdx.x * A + a] = pivot[a];
             lds[1][threadIdx.x * A + a] = m[a].mean;
             lds[2][threadIdx.x * A + a] = m[a].m2;
         }
     }
     __syncthreads();
     const int per = (k.split > 1 ? pl.width : k.Cg) / unit, row = pl.width / unit, lane = threadIdx.x & (k.lanes - 1);
+    const bool last = pl.chunk + 1 == k.chunks;  // a run past the image's end is in one tile less
+    const int tiles = last ? k.last_tiles : k.tiles, end = last ? k.last_rows : k.rows;
     for (int g = int(threadIdx.x) / k.lanes; g < pl.groups; g += int(blockDim.x) / k.lanes) {
-        Moments s;
+        Moments<double> s;
         for (int i = lane; i < per * k.rows; i += k.lanes) {
             const int r = i / per, at = r * row + g * per + (i - r * per);
-            s.join(lds[0][at], lds[1][at], lds[2][at]);
+            s.join(float(unit) * float(r < end ? tiles : tiles - 1), double(lds[0][at]) + double(lds[1][at]), lds[2][at]);
         }
         for (int o = 1; o < k.lanes; o *= 2) s.join(__shfl_xor(s.n, o), __shfl_xor(s.mean, o), __shfl_xor(s.m2, o));
         if (lane == 0) out(g, s);
     }
-}
-
-template <class T, int V, int S>
-__device__ __forceinline__ void load_pivots(OwnFloats<S, V> &pivot, const T *x, const Cut &k, const Place<V> &pl)
-{
-    pl.template each<S>(k, [&](int j, int, int g) {
-        pivot[j] = pivot_of(x, k, pl.n, pl.g0 + g);
-    });
 }
 
 // y of one tile from its x.
@@ -108,14 +95,14 @@ __global__ __launch_bounds__(kOneThreads, 4) void one_kernel(const T *x, Cut k, 
     load_tiles<T, K, V>(raw, x, k, pl, 0);
     const bool full = pl.full(k, 0, K);
     float pivot[A], a[V], be[V];
-    load_pivots<T, V, S>(pivot, x, k, pl);
     pl.params(a, k, gamma, 1.0f);
     pl.params(be, k, beta, 0.0f);
-    Moments m[A];
+    first_values<T, V, S>(pivot, raw[0]);
+    Moments<float> m[A];
     own_moments<T, V, S, K>(m, pivot, K, [&](int i) { return held<T, V>(raw[i]); },
                               [&](int i) { return full ? (pl.active ? V : 0) : pl.valid(k, i); });
-    join_block<kOneThreads, V, S>(k, pl, m, lds, [&](int g, const Moments &s) {
-        const float mu = pivot_of(x, k, pl.n, pl.g0 + g) + s.mean, r = 1.0f / sqrtf(s.m2 / s.n + eps);
+    join_block<kOneThreads, V, S>(k, pl, pivot, m, lds, [&](int g, const Moments<double> &s) {
+        const float mu = float(s.mean), r = 1.0f / sqrtf(s.m2 / s.n + eps);
         stat[g] = make_float2(mu, r);
         const int64_t at = pl.n * k.G + pl.g0 + g;
         if (mean) mean[at] = mu;
@@ -140,41 +127,40 @@ __global__ __launch_bounds__(kOneThreads, 4) void one_kernel(const T *x, Cut k, 
 // threads has 128 KB in flight), and leaves 8 bytes a group and chunk.  Bound by memory: 8 x 256 x
 // 16384 float16 (67 MB) 14.4 us, 4.7 TB/s.  A loop that starts the next tile's load when it
 // has used one was no faster.
-// part[n][g][chunk][slab of the group] = (mean relative to the pivot, m2); the counts follow
-// from the cut.  The pivots are written down too: a call in place overwrites the values.
+// part[n][g][chunk][slab of the group] = (mean, m2), the mean rounded to float32 (it is off by no
+// more than the call's own mean may be); the counts follow from the cut.
 template <class T, int V, int S, int K>
-__global__ __launch_bounds__(kStatThreads, 4) void stats_kernel(const T *x, Cut k, float2 *part, float *pivots)
+__global__ __launch_bounds__(kStatThreads, 4) void stats_kernel(const T *x, Cut k, float2 *part)
 {
     constexpr int A = kOwn<S, V>;
     __shared__ float lds[3][kStatThreads * A];
     const Place<V> pl(k, blockIdx.x);
     float pivot[A];
-    load_pivots<T, V, S>(pivot, x, k, pl);
-    Moments m[A];
+    Moments<float> m[A];
     for (int first = 0; first < k.tiles; first += K) {
         Held<V> raw[K];
         load_tiles<T, K, V>(raw, x, k, pl, first);
+        if (first == 0) first_values<T, V, S>(pivot, raw[0]);
         const bool full = pl.full(k, first, K);
-        Moments t[A];
+        Moments<float> t[A];
         own_moments<T, V, S, K>(t, pivot, K, [&](int i) { return held<T, V>(raw[i]); },
                                   [&](int i) { return full ? (pl.active ? V : 0) : pl.valid(k, first + i); });
 #pragma unroll
         for (int a = 0; a < A; ++a) m[a].join(t[a].n, t[a].mean, t[a].m2);
     }
-    join_block<kStatThreads, V, S>(k, pl, m, lds, [&](int g, const Moments &s) {
+    join_block<kStatThreads, V, S>(k, pl, pivot, m, lds, [&](int g, const Moments<double> &s) {
         const int64_t group = pl.n * k.G + pl.g0 + g;
-        part[(group * k.chunks + pl.chunk) * k.split + pl.sub] = make_float2(s.mean, s.m2);
-        if (pl.chunk == 0 && pl.sub == 0) pivots[group] = pivot_of(x, k, pl.n, pl.g0 + g);
+        part[(group * k.chunks + pl.chunk) * k.split + pl.sub] = make_float2(float(s.mean), s.m2);
     });
 }
 
 // Joins the parts of one group, `lanes` threads together; the moments on every one of them.
-__device__ __forceinline__ Moments join_parts(const float2 *part, const Cut &s, int64_t group, int lane, int lanes)
+__device__ __forceinline__ Moments<double> join_parts(const float2 *part, const Cut &s, int64_t group, int lane, int lanes)
 {
     constexpr int kAtOnce = 8;  // on their way together
     const float2 *p = part + group * s.chunks * s.split;
     const int count = s.chunks * s.split;
-    Moments m;
+    Moments<double> m;
     for (int q = lane; q < count; q += kAtOnce * lanes) {
         float2 v[kAtOnce];
 #pragma unroll
@@ -186,7 +172,7 @@ __device__ __forceinline__ Moments join_parts(const float2 *part, const Cut &s, 
             const int chunk = at / s.split, sub = at - chunk * s.split;
             const int64_t left = s.P - chunk * s.span();
             const int channels = s.split == 1 ? s.Cg : s.Cg - sub * s.width < s.width ? s.Cg - sub * s.width : s.width;
-            m.join(float(channels) * float(left < s.span() ? left : s.span()), v[j].x, v[j].y);
+            m.join(float(channels) * float(left < s.span() ? left : s.span()), double(v[j].x), v[j].y);
         }
     }
     for (int o = 1; o < lanes; o *= 2) m.join(__shfl_xor(m.n, o), __shfl_xor(m.mean, o), __shfl_xor(m.m2, o));
@@ -194,14 +180,14 @@ __device__ __forceinline__ Moments join_parts(const float2 *part, const Cut &s, 
 }
 
 // mean and rstd of every group, one wave a group.
-__global__ __launch_bounds__(256) void finish_kernel(const float2 *part, const float *pivots, Cut s, int64_t groups, float eps,
+__global__ __launch_bounds__(256) void finish_kernel(const float2 *part, Cut s, int64_t groups, float eps,
                                                      float *mean, float *rstd)
 {
     const int64_t g = (int64_t(blockIdx.x) * 256 + threadIdx.x) / 64;
     if (g >= groups) return;
-    const Moments m = join_parts(part, s, g, threadIdx.x & 63, 64);
+    const Moments<double> m = join_parts(part, s, g, threadIdx.x & 63, 64);
     if ((threadIdx.x & 63) == 0) {
-        mean[g] = pivots[g] + m.mean;
+        mean[g] = float(m.mean);
         rstd[g] = 1.0f / sqrtf(m.m2 / m.n + eps);
     }
 }
@@ -215,8 +201,8 @@ __global__ __launch_bounds__(256) void finish_kernel(const float2 *part, const f
 // chunk's blocks write mean and rstd down.
 template <class T, int V, int S, class ACT>
 __global__ __launch_bounds__(kApplyThreads, 4) void apply_kernel(const T *x, Cut k, Cut s, const float2 *part,
-                                                                 const float *pivots, bool finished, float eps,
-                                                                 ct::Param<T> gamma, ct::Param<T> beta, ACT f, Dropout drop,
+                                                                 bool finished, float eps, ct::Param<T> gamma,
+                                                                 ct::Param<T> beta, ACT f, Dropout drop,
                                                                  T *y, float *mean, float *rstd)
 {
     constexpr int A = kOwn<S, V>, K = kApplyTiles;
@@ -231,9 +217,9 @@ __global__ __launch_bounds__(kApplyThreads, 4) void apply_kernel(const T *x, Cut
         const int lane = threadIdx.x & (k.lanes - 1);
         for (int g = int(threadIdx.x) / k.lanes; g < pl.groups; g += kApplyThreads / k.lanes) {
             const int64_t group = pl.n * k.G + pl.g0 + g;
-            const Moments m = join_parts(part, s, group, lane, k.lanes);
+            const Moments<double> m = join_parts(part, s, group, lane, k.lanes);
             if (lane == 0) {
-                const float mu = pivots[group] + m.mean, r = 1.0f / sqrtf(m.m2 / m.n + eps);
+                const float mu = float(m.mean), r = 1.0f / sqrtf(m.m2 / m.n + eps);
                 stat[g] = make_float2(mu, r);
                 if (pl.chunk == 0 && pl.sub == 0) {
                     if (mean) mean[group] = mu;
@@ -271,7 +257,6 @@ __global__ __launch_bounds__(kApplyThreads, 4) void apply_kernel(const T *x, Cut
 void ct::norm::launch_forward(const Call &c, const Plan &p, char *ws, hipStream_t st)
 {
     float2 *const part = reinterpret_cast<float2 *>(ws + p.part);
-    float *const pivots = reinterpret_cast<float *>(ws + p.pivot);
     float *const stats = reinterpret_cast<float *>(ws + p.stats);
     const int64_t groups = c.N * p.a.G, blocks = c.N * p.a.chunks * p.a.slabs;
     with_type(c.dt, [&](auto t) {
@@ -298,19 +283,19 @@ void ct::norm::launch_forward(const Call &c, const Plan &p, char *ws, hipStream_
             constexpr int S = decltype(run)::value;
             const unsigned stat_blocks = unsigned(c.N * p.s.chunks * p.s.slabs);
             if (p.s.tiles <= kStatShort)
-                stats_kernel<T, V, S, kStatShort><<<stat_blocks, kStatThreads, 0, st>>>(x, p.s, part, pivots);
-            else stats_kernel<T, V, S, kStatTiles><<<stat_blocks, kStatThreads, 0, st>>>(x, p.s, part, pivots);
+                stats_kernel<T, V, S, kStatShort><<<stat_blocks, kStatThreads, 0, st>>>(x, p.s, part);
+            else stats_kernel<T, V, S, kStatTiles><<<stat_blocks, kStatThreads, 0, st>>>(x, p.s, part);
             float *mean = c.mean, *rstd = c.rstd;
             if (p.finish) {
                 if (!mean) mean = stats;
                 if (!rstd) rstd = stats + groups;
-                finish_kernel<<<unsigned((groups + 3) / 4), 256, 0, st>>>(part, pivots, p.s, groups, c.eps, mean, rstd);
+                finish_kernel<<<unsigned((groups + 3) / 4), 256, 0, st>>>(part, p.s, groups, c.eps, mean, rstd);
             }
             mark_before(st);
             with_act(c.act, [&](auto f) {
                 using F = decltype(f);
                 apply_kernel<T, V, S, F><<<unsigned(blocks), kApplyThreads, 0, st>>>(
-                    x, p.a, p.s, part, pivots, p.finish, c.eps, gamma, beta, f, c.drop, y, mean, rstd);
+                    x, p.a, p.s, part, p.finish, c.eps, gamma, beta, f, c.drop, y, mean, rstd);
             });
             mark_after(st);
         });
