@@ -51,9 +51,10 @@ struct Piecewise {
     ct::Act a;
     __device__ __forceinline__ float y(float z) const
     {
-        const float relu = z <= 0.0f ? 0.0f : z;
+        // one instruction for a maximum that keeps NaN, where a comparison and a select are two
+        const float relu = __builtin_elementwise_maximum(z, 0.0f);
         const float leaky = z >= 0.0f ? z : a.p0 * z;
-        const float clip = z < a.p0 ? a.p0 : (z > a.p1 ? a.p1 : z);
+        const float clip = __builtin_elementwise_minimum(__builtin_elementwise_maximum(z, a.p0), a.p1);
         return a.kind == CT_ACT_RELU ? relu : a.kind == CT_ACT_LEAKY_RELU ? leaky : a.kind == CT_ACT_CLIP ? clip : z;
     }
     __device__ __forceinline__ float d(float z) const
