@@ -1,5 +1,6 @@
 """Group norm where float32 arithmetic can go wrong: values that are not finite, under every
-activation, and single values far from all others."""
+activation, single values far from all others, and sums of many equal terms, whose roundings
+all go the same way."""
 import numpy as np
 import pytest
 import torch
@@ -62,3 +63,25 @@ def test_group_norm_one_value_far_from_the_others(T, path, shape, where, far):
     z = (v - wide(m)) / wide(s)
     bound = (8 * (1 + np.abs(wide(m)) / wide(s)) + R.FACTOR * np.abs(z)) * R.EPS
     assert (np.abs(rows_of(y).reshape(v.shape) - z) <= bound).all()
+
+
+@pytest.mark.parametrize("n,c,dims,groups", [((1 << 21) + 5, 2, (2,), 1), (300001, 16, (3,), 4), (1, 4, (1 << 28,), 2),
+                                             (600, 24, (60, 1000), 3)])
+def test_parameter_gradients_of_a_constant_gradient(T, n, c, dims, groups):
+    """dy = 0.1 everywhere and no activation: dbeta is 0.1 times the number of positions, to the
+    roundings of a sum in a tree.  One sum of 2^17 terms after another would be off by hundreds
+    of times that."""
+    print(f"[case] constant gradient {(n, c, dims)} f32", flush=True)
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    x = torch.randn((n,) + dims + (c,), generator=gen, device="cuda").movedim(-1, 1)
+    dy = torch.full_like(x, 0.1)
+    gamma = torch.ones(c, device="cuda")
+    _, mean, rstd = T.group_norm_nd(x, groups, gamma, gamma)
+    _, dgamma, dbeta = T.group_norm_backward_nd(dy, x, mean, rstd, groups, gamma, gamma, out=dy)
+    want = float(np.float32(0.1)) * n * int(np.prod(dims))
+    print(f"dbeta off by {np.abs(host(dbeta) / want - 1).max() / R.EPS:.1f} roundings", flush=True)
+    assert (np.abs(host(dbeta) - want) <= R.FACTOR * R.EPS * want).all()
+    # the sums of 0.1 xhat by group vanish, and those by channel are small beside the terms'
+    # magnitudes, 0.1 sqrt(2 / pi) on average
+    by_group = host(dgamma).reshape(groups, -1).sum(1)
+    assert (np.abs(by_group) <= R.FACTOR * R.EPS * want * (c // groups)).all()

@@ -187,8 +187,11 @@ __global__ __launch_bounds__(kOneGradThreads, 2) void one_grad_kernel(const T *d
 // with SiLU and dropout (134 MB): 36.4 us, 3.7 TB/s, the vector units 70 % busy (SiLU's
 // derivative takes an exponential and a reciprocal, the generator ten rounds for eight elements);
 // 2 x 64 x 131072 bfloat16 without dropout (67 MB): 16.9 us, 4.0 TB/s.
+// Sums of more than kSumTiles tiles are made in two levels, in float32: equal terms are all rounded
+// the same way, and n of them one after another may cost n / 4 roundings of their sum.
 // part[n][g][chunk][slab of the group] = (sum dz gamma, sum dz gamma xhat),
 // sums[n][chunk][c] = (sum dz, sum dz xhat).
+constexpr int kSumTiles = 64;
 template <class T, int V, int S, class ACT>
 __global__ __launch_bounds__(kGradThreads, S > 1 ? 4 : 3) void grad_stats_kernel(const T *dy, const T *x, Cut k, const float *mean,
                                                                      const float *rstd, ct::Param<T> gamma,
@@ -196,12 +199,22 @@ __global__ __launch_bounds__(kGradThreads, S > 1 ? 4 : 3) void grad_stats_kernel
                                                                      float2 *sums)
 {
     constexpr int K = kGradTiles;
+    static_assert(kSumTiles % K == 0, "a level ends between two rounds of loads");
     __shared__ float2 lds[kGradThreads * V];
     const Place<V> pl(k, blockIdx.x);
     const Constants<T, V, S> ch(k, pl, mean, rstd, gamma, beta);
     const uint64_t counter = drop.threshold ? drop.counter() : 0;
     float s1[V] = {}, s2[V] = {};
+    float2 *const own = lds + threadIdx.x * V;  // until the join, the thread's sums of the tiles before
     for (int first = 0; first < k.tiles; first += K) {
+        if (first > 0 && first % kSumTiles == 0) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const float2 before = first > kSumTiles ? own[j] : make_float2(0.0f, 0.0f);
+                own[j] = make_float2(before.x + s1[j], before.y + s2[j]);
+                s1[j] = s2[j] = 0.0f;
+            }
+        }
         Held<V> xr[K], dr[K];
         load_tiles<T, K, V>(xr, x, k, pl, first);
         load_tiles<T, K, V>(dr, dy, k, pl, first);
@@ -220,6 +233,10 @@ __global__ __launch_bounds__(kGradThreads, S > 1 ? 4 : 3) void grad_stats_kernel
     }
 #pragma unroll
     for (int j = 0; j < V; ++j) {
+        if (k.tiles > kSumTiles) {
+            s1[j] += own[j].x;
+            s2[j] += own[j].y;
+        }
         s1[j] *= drop.factor;
         s2[j] *= drop.factor * ch.rs[j / S];
     }
@@ -266,19 +283,21 @@ __global__ __launch_bounds__(256) void grad_finish_kernel(const float2 *part, Cu
 }
 
 // dgamma and dbeta of 16 channels from their `parts` sums, by one block: 16 threads a channel.
+// Added in 64 bits: a thread may have 2^17 parts (an image each), and equal ones would all be
+// rounded the same way.
 template <class T>
 __device__ __forceinline__ void param_gradients(const float2 *sums, int64_t parts, int C, int tile, bool f32, void *dgamma,
                                                 void *dbeta)
 {
-    __shared__ float2 lds[16][16];
+    __shared__ double2 lds[16][16];
     const int c = tile * 16 + int(threadIdx.x & 15), q = threadIdx.x / 16;
-    float2 s = make_float2(0.0f, 0.0f);
+    double2 s = make_double2(0.0, 0.0);
     if (c < C) {
 #pragma unroll 8
         for (int64_t i = q; i < parts; i += 16) {
             const float2 v = sums[i * C + c];
-            s.x += v.x;
-            s.y += v.y;
+            s.x += double(v.x);
+            s.y += double(v.y);
         }
     }
     lds[q][threadIdx.x & 15] = s;
@@ -289,12 +308,12 @@ __device__ __forceinline__ void param_gradients(const float2 *sums, int64_t part
         s.y += lds[i][threadIdx.x].y;
     }
     if (dgamma) {
-        if (f32) static_cast<float *>(dgamma)[c] = s.y;
-        else static_cast<T *>(dgamma)[c] = T(s.y);
+        if (f32) static_cast<float *>(dgamma)[c] = float(s.y);
+        else static_cast<T *>(dgamma)[c] = T(float(s.y));
     }
     if (dbeta) {
-        if (f32) static_cast<float *>(dbeta)[c] = s.x;
-        else static_cast<T *>(dbeta)[c] = T(s.x);
+        if (f32) static_cast<float *>(dbeta)[c] = float(s.x);
+        else static_cast<T *>(dbeta)[c] = T(float(s.x));
     }
 }
 
