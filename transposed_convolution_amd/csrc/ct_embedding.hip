@@ -86,8 +86,9 @@ __global__ __launch_bounds__(kThreads) void lookup_kernel(const I *ids, const T 
 //
 // Sorted, a row's tokens stand together in ascending order: every row of dy is read once,
 // every row of the table is written once, and no sum depends on which block came first.
-// 32768 tokens of 512 float16 into 16384 rows (50.6 MB) take 38.2 us: two sorting passes
-// 17.7 (counts 2.7 and moves 6.2 each), the chunks 13.2, the rows 10.0.  The sort and the rows
+// 32768 tokens of 512 float16 into 16384 rows (50.6 MB) take 37.8 us.  A trace, which keeps the
+// kernels further apart, has the counts at 3.9 and 2.6, the moves at 6.2 and 6.1, the chunks at
+// 13.1 and the rows at 9.7 (medians; more than the untraced call when added).  The sort and the rows
 // are bound by chains of dependent reads (an id to a place, a row's begin to its key to its
 // partial sums) of about a microsecond a link, not by bytes; the chunks by memory.
 // ------------------------------------------------------------------------------------
@@ -391,7 +392,7 @@ __device__ __forceinline__ void store_slot(G *dst, const RowSlots &rs, int64_t s
 // of a row that crosses a chunk's border every chunk leaves a partial sum, in slot 0 of the
 // chunk for a row that is there from its start and in slot 1 for one that begins later.
 // The work is cut by tokens, so a frequent row and many rare ones take the same time; the
-// kernel reads all of dy: 33.5 MB and 9 MB of the table's rows in 13.2 us, 3.2 TB/s (16
+// kernel reads all of dy: 33.5 MB and 9 MB of the table's rows in 13.1 us (traced), 3.2 TB/s (16
 // rows on their way made the whole gradient 40.5 us instead of 39.4).
 constexpr int kMostChunk = 1024;
 template <class T, class G>

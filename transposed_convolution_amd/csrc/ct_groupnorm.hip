@@ -14,15 +14,15 @@
 // values it holds, and such triples (count, mean, m2) are joined pairwise (Chan, Golub,
 // LeVeque 1983).  A thread takes its values relative to its own first one, so a mean far from
 // zero costs no digits of the spread around it, and a value far from the others costs digits
-// of the few values only that share its thread; the joins hold means in 64 bits.
+// of the few values only that share its thread; the joins hold means in 64 bits, and in 64
+// bits the parameters' gradients are added over images and chunks.
 // Everything else is float32 between the one load and the one store of an element.
 //
 // Both directions need every value of a group before the first output.  Small groups fit the
 // registers of one block, which reads them once; for the others a first pass over the
-// tensor makes partial sums and a second one reads it again, from the memory-side cache
-// where it fits that, joins the partial sums at the start of every block and writes.  Here
-// are the plan and the entry points, the kernels are in ct_groupnorm_fwd.hip and
-// ct_groupnorm_grad.hip.
+// tensor makes partial sums and a second one reads it again, joins the partial sums at the
+// start of every block and writes.  Here are the plan and the entry points, the kernels are
+// in ct_groupnorm_fwd.hip and ct_groupnorm_grad.hip.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -127,15 +127,18 @@ int64_t line_bytes(const Sizes &s, const Cut &k, bool backward)
 }
 
 // Parts that every block of the second pass joins by itself; more are joined by a kernel
-// between the passes.  Joined by every block / by a kernel, us: 36 x 1001 float32, 4 images (a few
-// parts) 12.4 / 13.9; float16, 8 x 256 x 16384 in 32 groups (16 KB a block) 40.8 / 40.7; gradient
-// 2 x 64 x 131072 in 16 groups (32 KB) 36.6 / 38.3; 64 x 1048576 in 16 groups (64 KB) 81.8 / 76.7,
-// gradient 111.1 / 110.3; 256 x 131072 in 32 groups (128 KB) 55.5 / 41.4, gradient 62.1 / 61.1;
-// 256 x 65536 in 256 groups (1 MB) 285 / 34, gradient 292 / 44.
+// between the passes.  Joined by every block / by a kernel, us, with SiLU: 36 x 1001 float32, 4
+// images (a few parts) 12.2 / 13.8, gradient 13.0 / 14.8; float16, 8 x 256 x 16384 in 32 groups
+// (16 KB a block) 40.5 / 40.7, gradient 65.9 / 67.7; bfloat16, 2 x 64 x 131072 in 16 groups (32 KB)
+// 31.9 / 28.4, gradient 36.0 / 37.3; float16, 64 x 1048576 in 16 groups (64 KB) 90.1 / 82.8,
+// gradient 119.6 / 119.0; 256 x 131072 in 32 groups (128 KB) 59.3 / 41.9, gradient 71.5 / 68.6;
+// 256 x 65536 in 256 groups (1 MB) 287 / 34, gradient 302 / 45.
 constexpr int64_t kPartBytes = 32 << 10;
-// Blocks of a first pass, at most about: 512 blocks of 512 threads are one round of the chip (us
-// at 256 / 512 / 768 / 1024, whole call: forward 8 x 256 x 16384 float16 43.5 / 41.2 / 47 / 48, its
-// gradient 83.4 / 76.9 / 81.7 / 75.9, gradient 2 x 64 x 131072 39.2 / 37.4 / 40.2 / 38.9).
+// Blocks of a first pass, at most about.  The forward call's have 512 threads, and 512 of them are one
+// round of the chip; the gradient's have 256, so 512 are half a round of what its registers
+// allow, and a whole one gained as much in one call as it lost in the other (us at 256 / 512 /
+// 768 / 1024, whole call: forward 8 x 256 x 16384 float16 43.5 / 41.2 / 47 / 48, its gradient
+// 83.4 / 76.9 / 81.7 / 75.9, gradient 2 x 64 x 131072 39.2 / 37.4 / 40.2 / 38.9).
 constexpr int64_t kStatBlocks = 512;
 // and of a second one, 1024 blocks of 256 threads (us at 512 / 768 / 1024 / 1536 / 2048, the same
 // calls: 41.0 / 40.2 / 40.8 / 40.2 / 41.1, 78.9 / 75.7 / 75.8 / 74.7 / 74.2, 39.5 / 38.6 / 36.6 /

@@ -37,6 +37,12 @@ struct Moments {
 // Activation and its derivative.  Kernels are compiled for SiLU and for the piecewise linear
 // kinds (none among them), which are told apart by selects: a switch inside a kernel made
 // the compiler hoist the unpacking of every held value above it, into spilled registers.
+//
+// SiLU by the hardware's 2^x and reciprocal: z log2(e) is rounded before 2^x, so y is off by up to
+// (|z| + 5) 2^-24 of itself for negative z (30 at z = -30, where y is 3e-12) and 2.5 * 2^-24
+// for others, measured; beside z, about 2^-24.  exp and a division (2.6 * 2^-24
+// everywhere) took 50.7 us for 40.2 in an 8 x 256 x 16384 float16 call and 88.6 for 67.5 in
+// its gradient.
 struct Silu {
     __device__ __forceinline__ float y(float z) const { return z * __builtin_amdgcn_rcpf(1.0f + __expf(-z)); }
     __device__ __forceinline__ float d(float z) const

@@ -125,7 +125,7 @@ __global__ __launch_bounds__(kOneThreads, 4) void one_kernel(const T *x, Cut k, 
 
 // The first pass: x is read once, 16 vectors of a thread on their way at a time (a block of 512
 // threads has 128 KB in flight), and leaves 8 bytes a group and chunk.  Bound by memory: 8 x 256 x
-// 16384 float16 (67 MB) 14.4 us, 4.7 TB/s.  A loop that starts the next tile's load when it
+// 16384 float16 (67 MB) 14.6 us in a trace, 4.6 TB/s.  A loop that starts the next tile's load when it
 // has used one was no faster.
 // part[n][g][chunk][slab of the group] = (mean, m2), the mean rounded to float32 (it is off by no
 // more than the call's own mean may be); the counts follow from the cut.
@@ -193,7 +193,7 @@ __global__ __launch_bounds__(256) void finish_kernel(const float2 *part, Cut s, 
 }
 
 // The second pass: x is read again and y written, bound by memory: 8 x 256 x 16384 float16
-// (134 MB) 26.1 us, 5.1 TB/s, a copy's rate.  With the first pass 40.0 us; one pass that keeps x
+// (134 MB) 26.3 us in a trace, 5.1 TB/s, a copy's rate.  The whole call takes 40.2 us; one pass that keeps x
 // in registers while the blocks exchange their parts would read x once, but the exchange
 // (6 to 13 us an image, while its blocks wait) cost more than the second read.
 // finished: mean and rstd are there; else every block joins the parts of its

@@ -123,7 +123,7 @@ __device__ __forceinline__ void output_constants(OwnFloats<S, V> &k1, OwnFloats<
 
 // One block has all positions of its groups: x and dy are read once, x is held in registers
 // and so is dz, in float32.  sums[n][c] = (sum dz, sum dz xhat).  Bound by its chain of load,
-// join and store, and the launch for the parameters: 1 x 256 x 1024 float16 10.5 us.
+// join and store, and the launch for the parameters: 1 x 256 x 1024 float16 10.9 us.
 template <class T, int V, int S, class ACT>
 __global__ __launch_bounds__(kOneGradThreads, 2) void one_grad_kernel(const T *dy, const T *x, Cut k, const float *mean,
                                                                       const float *rstd, ct::Param<T> gamma,
@@ -183,10 +183,10 @@ __global__ __launch_bounds__(kOneGradThreads, 2) void one_grad_kernel(const T *d
 }
 
 // The first pass.  A thread owns the same channels in all its tiles, so sums by channel stay in
-// registers and the groups' follow from them at the end, with gamma.  8 x 256 x 16384 float16
-// with SiLU and dropout (134 MB): 36.4 us, 3.7 TB/s, the vector units 70 % busy (SiLU's
+// registers and the groups' follow from them at the end, with gamma.  In a trace, 8 x 256 x 16384
+// float16 with SiLU and dropout (134 MB): 38.3 us, 3.5 TB/s, the vector units 69 % busy (SiLU's
 // derivative takes an exponential and a reciprocal, the generator ten rounds for eight elements);
-// 2 x 64 x 131072 bfloat16 without dropout (67 MB): 16.9 us, 4.0 TB/s.
+// 2 x 64 x 131072 bfloat16 without dropout (67 MB): 16.8 us, 4.0 TB/s.
 // Sums of more than kSumTiles tiles are made in two levels, in float32: equal terms are all rounded
 // the same way, and n of them one after another may cost n / 4 roundings of their sum.
 // part[n][g][chunk][slab of the group] = (sum dz gamma, sum dz gamma xhat),
@@ -325,8 +325,9 @@ __global__ __launch_bounds__(256) void param_kernel(const float2 *sums, int64_t 
 }
 
 // The second pass makes dz again (stored, it would be two more passes over memory) and dx from
-// it: 8 x 256 x 16384 float16 with SiLU and dropout (201 MB) 39.8 us, 5.1 TB/s, a copy's rate;
-// 2 x 64 x 131072 bfloat16 (101 MB) 20.7 us, 4.9 TB/s.  The first `head` blocks make dgamma and dbeta; the others write dx.
+// it.  In a trace, 8 x 256 x 16384 float16 with SiLU and dropout (201 MB): 42.2 us, 4.8 TB/s, the
+// vector units 71 % busy; 2 x 64 x 131072 bfloat16 (101 MB): 20.4 us, 4.9 TB/s, a copy's rate.  The
+// first `head` blocks make dgamma and dbeta; the others write dx.
 // finished: c1 and c2 are there; else every block joins the parts of its groups, before it asks for
 // its values: behind those the parts took 8 us of a block's 20 to arrive.
 template <class T, int V, int S, class ACT>
