@@ -1,6 +1,6 @@
 """Group norm where float32 arithmetic can go wrong: values that are not finite, under every
 activation, single values far from all others, and sums of many equal terms, whose roundings
-all go the same way."""
+all go the same way; and the embedding's gradient of narrow rows with very many tokens."""
 import numpy as np
 import pytest
 import torch
@@ -85,3 +85,18 @@ def test_parameter_gradients_of_a_constant_gradient(T, n, c, dims, groups):
     # magnitudes, 0.1 sqrt(2 / pi) on average
     by_group = host(dgamma).reshape(groups, -1).sum(1)
     assert (np.abs(by_group) <= R.FACTOR * R.EPS * want * (c // groups)).all()
+
+
+@pytest.mark.parametrize("tokens,rows,width", [(6225, 90, 1), (3003, 6, 1), (22634, 19, 2), (29915, 63, 18), (70001, 2, 3),
+                                               (40000, 1, 9), (5000, 300, 130)])
+def test_embedding_gradient_of_frequent_narrow_rows(T, tokens, rows, width):
+    """A row's partial sums are shared out over up to 256 groups of lanes, some without a share: whole
+    numbers, so every partial sum is counted exactly once."""
+    rng = np.random.default_rng(tokens)
+    ids = np.minimum((rows + 1) ** rng.random(tokens) - 1, rows - 1).astype(np.int64)
+    dy = rng.integers(-2, 3, size=(tokens, width)).astype(np.float64)
+    want, _ = R.embedding_grad(dy, ids, rows, 1.0)
+    for dtype in (torch.float32, torch.bfloat16):
+        d = torch.from_numpy(dy).to(dtype).cuda()
+        got = T.embedding_backward_nd(d, torch.from_numpy(ids).cuda(), rows, grad_dtype=torch.float32)
+        assert np.array_equal(host(got), want), dtype
