@@ -41,7 +41,9 @@
  * Next to the convolution the library holds the other operators of a decoder layer:
  * channels-last group norm with an activation (group_norm_nd and its gradient), dropout
  * from a counter-based generator (dropout_nd, its own gradient) and the embedding lookup
- * (embedding_nd and its gradient).  They also serve bfloat16.
+ * (embedding_nd and its gradient); attention over tokens (attention_nd and its gradient) with
+ * rotary positions (rotary_nd, its own gradient); and the step that trains them (adamw_nd).
+ * They also serve bfloat16.
  *
  * Thread safety: every call is re-entrant; the error text is per host thread.
  */
@@ -517,6 +519,120 @@ ct_status embedding_backward_nd(ct_dtype dtype, ct_dtype index_dtype, int64_t to
 
 /* Workspace bytes of embedding_backward_nd.  Host only. */
 ct_status embedding_workspace_size(int64_t tokens, int64_t rows, int64_t width, size_t *bytes_out);
+
+/*
+ * Attention over tokens, enqueued on a HIP stream.  Query token i of image n and head h sees
+ * keys j of head h / (H / kv_heads):
+ *   s_ij = scale * q[n,i,h,:] . k[n,j,:],   lse[n,h,i] = log(sum over its keys of exp(s_ij)),
+ *   out[n,i,h,:] = sum over its keys of exp(s_ij - lse) * v[n,j,:]
+ * A token sees key j when j < lengths[n], and in a causal call j <= starts[n] + i.  A token that
+ * sees nothing gives out = 0 and lse = -infinity.  Keys and values at or behind lengths[n] are never
+ * looked at; there may be anything.  A value that is not finite in a key or value that one token
+ * of a causal call sees may make the outputs of others of that image and key head NaN.
+ *   dtype          CT_FLOAT32, CT_FLOAT16 or CT_BFLOAT16: the type of q, k, v and out; sums,
+ *                  scores and statistics are float32, the weights are rounded to dtype once
+ *   q_shape        {N, Tq, H, D}; 1 <= D <= 256
+ *   kv_tokens, kv_heads   k and v are (N, kv_tokens, kv_heads, D); kv_heads divides H
+ *   *_strides      strides in elements of a tensor's image, token and head axes, in that order;
+ *                  a head's D elements are dense.  So q, k and v may be parts of one
+ *                  projection, a cache of more tokens than are seen, or repeated (stride 0)
+ *   scale          positive and finite
+ *   causal         0 or 1
+ *   lengths        device array of N int32, or NULL (kv_tokens); taken as 0 below 0 and as
+ *                  kv_tokens above it
+ *   starts         device array of N int32: the place of the first query among the keys; NULL:
+ *                  kv_tokens - Tq.  For causal calls only.  A serving step gives lengths (with the
+ *                  new tokens) and starts = lengths - Tq
+ *   out, lse       dense (N, Tq, H, D) of dtype and (N, H, Tq) of float32
+ *   workspace      as for group_norm_nd (attention_workspace_size bytes)
+ * Validation comes first: on any error nothing is launched and the outputs are untouched.  With
+ * no tokens at all nothing is written.  The same inputs give the same bits.
+ */
+ct_status attention_nd(ct_dtype dtype, const int64_t *q_shape, int64_t kv_tokens, int64_t kv_heads, const void *q,
+                       const int64_t *q_strides, const void *k, const int64_t *k_strides, const void *v,
+                       const int64_t *v_strides, float scale, int causal, const int32_t *lengths, const int32_t *starts,
+                       void *out, float *lse, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Its gradient.  With P = exp(s - lse), dP_ij = dout_i . v_j, delta_i = dout_i . out_i and
+ * dS = scale * P * (dP - delta):
+ *   dv_j = sum of P_ij dout_i,  dk_j = sum of dS_ij q_i,  dq_i = sum of dS_ij k_j,
+ * the sums for keys over the tokens and heads that see them.  P is computed again, nothing of
+ * size Tq * kv_tokens is stored.  Keys at or behind lengths[n] get zeros, so do tokens that see
+ * nothing (whatever dout and q hold there).
+ *   dout, out      (N, Tq, H, D) with strides like q's; out and lse are what attention_nd wrote
+ *   dq, dk, dv     dense (N, Tq, H, D), (N, kv_tokens, kv_heads, D) twice, of dtype, not
+ *                  overlapping anything else
+ * The other arguments and the errors as for attention_nd.  No atomics: the same inputs give the
+ * same bits.
+ */
+ct_status attention_backward_nd(ct_dtype dtype, const int64_t *q_shape, int64_t kv_tokens, int64_t kv_heads,
+                                const void *dout, const int64_t *dout_strides, const void *q, const int64_t *q_strides,
+                                const void *k, const int64_t *k_strides, const void *v, const int64_t *v_strides,
+                                const void *out, const int64_t *out_strides, const float *lse, float scale, int causal,
+                                const int32_t *lengths, const int32_t *starts, void *dq, void *dk, void *dv,
+                                void *workspace, size_t workspace_bytes, void *stream);
+
+/* Workspace bytes of attention_nd (backward 0) or attention_backward_nd (1).  Host only. */
+ct_status attention_workspace_size(ct_dtype dtype, const int64_t *q_shape, int64_t kv_tokens, int64_t kv_heads, int backward,
+                                   size_t *bytes_out);
+
+/*
+ * Rotary positions with several axes, enqueued on a HIP stream.  The first 2 R elements of every
+ * head, R = sections[0] + .. + sections[axes - 1], are R pairs; the first sections[0] go by axis
+ * 0, the next by axis 1 and so on.  Pair p of axis a, the j-th of its section, becomes
+ *   (x0 cos A - x1 sin A, x0 sin A + x1 cos A),  A = positions[n, t, a] * base^(-e),
+ * e = j / sections[a], or p / R with whole_ladder (one ladder of frequencies through all axes).
+ * The elements behind the pairs are copied.  inverse turns by -A: the gradient of x is this call
+ * with inverse on the gradient of y.
+ *   dtype          CT_FLOAT32, CT_FLOAT16 or CT_BFLOAT16; one rounding
+ *   shape          {N, T, H, D}, strides of x and y as for attention_nd; y may be x itself (with
+ *                  x's strides) and must not overlap it otherwise
+ *   position_dtype CT_INT32 or CT_INT64; positions is (N, T, axes), its axes dense,
+ *                  position_strides those of N and T (0: the same for all images or tokens)
+ *   axes           1..4; R <= 256, 2 R <= D
+ *   base           positive and finite
+ *   interleaved    0: pair p is (p, p + R); 1: (2 p, 2 p + 1)
+ * Angles are exact to 2^-32 of a turn at positions up to 2^31 in magnitude.
+ */
+ct_status rotary_nd(ct_dtype dtype, const int64_t *shape, const void *x, const int64_t *x_strides, ct_dtype position_dtype,
+                    int axes, const void *positions, const int64_t *position_strides, const int64_t *sections, double base,
+                    int whole_ladder, int interleaved, int inverse, void *y, const int64_t *y_strides, void *stream);
+
+/*
+ * One AdamW step over many tensors, enqueued on a HIP stream, in place:
+ *   g = grad_scale * grad,  m = beta1 m + (1 - beta1) g,  v = beta2 v + (1 - beta2) g^2,
+ *   param = param (1 - lr weight_decay) - lr / (1 - beta1^step) m / (sqrt(v) / sqrt(1 - beta2^step) + eps)
+ * in float32, each output rounded once.
+ *   dtype, grad_dtype   types of param and grad: CT_FLOAT32, CT_FLOAT16 or CT_BFLOAT16
+ *   state_bits     32: m and v are float32.  8: m and v hold e4m3 values, and m_scale and v_scale a
+ *                  float32 for each 256 consecutive elements (the last may be fewer):
+ *                  m = code * m_scale, sqrt(v) = code * v_scale.  A scale is the largest
+ *                  magnitude / 448, at least 2^-126; a code is the quotient rounded to nearest, but
+ *                  a positive sqrt(v) has at least the smallest code, 2^-9.  Zeros everywhere
+ *                  (scales too) are the states before the first step.  One value that is not
+ *                  finite makes its block's states NaN.  The step itself uses m and v unrounded
+ *   copy_dtype     type of the copies: CT_FLOAT16 or CT_BFLOAT16 (any value without copies)
+ *   lr, grad_scale, step   host values; lr_device, grad_scale_device (one float32) and step_device (one int64)
+ *                  are read when the kernels run and take their place, or NULL.  step counts from 1
+ *   beta1, beta2   in [0, 1); eps finite, not negative
+ * Tensors are dense and must not overlap; one of count 0 is passed over.  The list may be freed
+ * after the call: a captured graph keeps its own copy.
+ */
+typedef struct {
+    void *param;
+    const void *grad;
+    void *m, *v;              /* float32, or e4m3 bytes                                   */
+    float *m_scale, *v_scale; /* state_bits 8: (count + 255) / 256 values each            */
+    void *copy;               /* also receives param, in copy_dtype; NULL: none           */
+    int64_t count;
+    float weight_decay;
+} ct_adamw_tensor;
+
+ct_status adamw_nd(ct_dtype dtype, ct_dtype grad_dtype, int state_bits, ct_dtype copy_dtype, int64_t tensors,
+                   const ct_adamw_tensor *list, double lr, const float *lr_device, double beta1, double beta2, double eps,
+                   int64_t step, const int64_t *step_device, double grad_scale, const float *grad_scale_device,
+                   void *stream);
 
 /* Text of the last error on the calling host thread ("" after a successful call).
  * The pointer stays valid until the next library call on that thread. */

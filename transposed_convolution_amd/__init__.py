@@ -27,7 +27,7 @@ __all__ = [
     "to_channels_last", "KERNELS", "ACTIVATIONS", "convolution_nd", "convolution_output_shape",
     "IGEMM_TILES", "set_igemm_tile", "igemm_tile", "qlinear_convtranspose_nd", "PreparedCall",
     "NORM_ACTIVATIONS", "group_norm_nd", "group_norm_backward_nd", "dropout_nd", "embedding_nd",
-    "embedding_backward_nd", "set_group_norm_control",
+    "embedding_backward_nd", "set_group_norm_control", "attention_nd", "attention_backward_nd", "rotary_nd", "adamw_nd",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -42,7 +42,7 @@ ACTIVATIONS = {"identity": (0, 0), "relu": (1, 0), "leaky_relu": (2, 1), "clip":
 # group norm's activations: the same and SiLU
 NORM_ACTIVATIONS = {**ACTIVATIONS, "silu": (4, 0)}
 _DTYPES = {torch.float32: 0, torch.float16: 1}
-# group norm, dropout and the embedding
+# group norm, dropout, the embedding, attention, rotary positions and AdamW
 _LAYER_DTYPES = {**_DTYPES, torch.bfloat16: 4}
 _INDEX_DTYPES = {torch.int32: 5, torch.int64: 6}
 _STATUS = {0: "CT_OK", 1: "CT_EINVAL", 2: "CT_ESHAPE", 3: "CT_EUNSUPPORTED", 4: "CT_EDEVICE"}
@@ -124,8 +124,17 @@ def load_library():
     lib.embedding_backward_nd.argtypes = [c_int, c_int, c_i64, vp, c_i64, c_i64, vp, c_f32, c_i64, c_int, vp, vp, c_size,
                                           vp]
     lib.embedding_workspace_size.argtypes = [c_i64, c_i64, c_i64, ctypes.POINTER(c_size)]
+    c_f64 = ctypes.c_double
+    mask = [c_f32, c_int, vp, vp]  # scale, causal, lengths, starts
+    lib.attention_nd.argtypes = [c_int, i64p, c_i64, c_i64] + [vp, i64p] * 3 + mask + [vp, vp, vp, c_size, vp]
+    lib.attention_backward_nd.argtypes = [c_int, i64p, c_i64, c_i64] + [vp, i64p] * 5 + [vp] + mask + [
+        vp, vp, vp, vp, c_size, vp]
+    lib.attention_workspace_size.argtypes = [c_int, i64p, c_i64, c_i64, c_int, ctypes.POINTER(c_size)]
+    lib.rotary_nd.argtypes = [c_int, i64p, vp, i64p, c_int, c_int, vp, i64p, i64p, c_f64, c_int, c_int, c_int, vp, i64p, vp]
+    lib.adamw_nd.argtypes = [c_int, c_int, c_int, c_int, c_i64, vp, c_f64, vp, c_f64, c_f64, c_f64, c_i64, vp, c_f64, vp, vp]
     for fn in ("group_norm_nd", "group_norm_backward_nd", "group_norm_workspace_size", "dropout_nd", "embedding_nd",
-               "embedding_backward_nd", "embedding_workspace_size"):
+               "embedding_backward_nd", "embedding_workspace_size", "attention_nd", "attention_backward_nd",
+               "attention_workspace_size", "rotary_nd", "adamw_nd"):
         getattr(lib, fn).restype = ctypes.c_int
     lib.convtranspose_set_igemm_tile.argtypes = [ctypes.c_int]
     lib.convtranspose_set_igemm_tile.restype = ctypes.c_int
@@ -872,10 +881,246 @@ def embedding_backward_nd(dy: torch.Tensor, ids: torch.Tensor, rows: int, *, sca
     return _call(lib.embedding_backward_nd, args, out, ws, _prepare_only)
 
 
+# ------------------------------------------------------------------------------------
+# Attention over tokens, rotary positions, and the step that trains a model
+# ------------------------------------------------------------------------------------
+def _token_strides(name, t):
+    """Strides of the image, token and head axes of an (N, T, H, D) tensor with dense heads."""
+    if t.dim() != 4:
+        raise ConvTransposeError(1, f"{name} must be (N, T, H, D)")
+    if t.shape[3] > 1 and t.stride(3) != 1 and t.numel():
+        raise ConvTransposeError(1, f"the elements of a head must be dense in {name}")
+    return _i64(t.stride()[:3])
+
+
+def _attention_args(q, k, v, scale, causal, lengths, starts):
+    """Checks both directions of attention share; (sizes, operands, mask) arguments."""
+    if q.dtype not in _LAYER_DTYPES:
+        raise ConvTransposeError(3, f"dtype {q.dtype} is not served (float32, float16, bfloat16)")
+    operands = []
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        _check_tensor(name, t, q.device, q.dtype)
+        operands += [_ptr(t), _token_strides(name, t)]
+    if k.shape != v.shape or k.shape[0] != q.shape[0] or k.shape[3] != q.shape[3]:
+        raise ConvTransposeError(1, "k and v must have one shape, and q's images and head size")
+    if k.shape[2] < 1 or q.shape[2] < 1 or q.shape[2] % k.shape[2]:
+        raise ConvTransposeError(1, "q's heads must be a multiple of k's")
+    scale = q.shape[3] ** -0.5 if scale is None and q.shape[3] else scale
+    if scale is None or not 0.0 < float(scale) < 3e38:
+        raise ConvTransposeError(1, "scale must be positive and finite")
+    if starts is not None and not causal:
+        raise ConvTransposeError(1, "starts are for causal calls")
+    for name, t in (("lengths", lengths), ("starts", starts)):
+        if t is not None:
+            _check_tensor(name, t, q.device, torch.int32)
+            if tuple(t.shape) != (q.shape[0],) or not t.is_contiguous():
+                raise ConvTransposeError(1, f"{name} must be a dense int32 tensor with one value an image")
+    return ([_LAYER_DTYPES[q.dtype], _i64(q.shape), k.shape[1], k.shape[2]], operands,
+            [float(scale), int(bool(causal)), _ptr(lengths), _ptr(starts)])
+
+
+def _attention_workspace(sizes, backward):
+    nbytes = ctypes.c_size_t(0)
+    st = load_library().attention_workspace_size(*sizes, int(backward), ctypes.byref(nbytes))
+    if st:
+        _raise(st)
+    return nbytes.value
+
+
+def _dense_like(name, t, like):
+    """A caller's output (None: a new one) of `like`'s shape and type, dense."""
+    if t is None:
+        return torch.empty(like.shape, dtype=like.dtype, device=like.device)
+    _check_tensor(name, t, like.device, like.dtype)
+    if t.shape != like.shape or not t.is_contiguous():
+        raise ConvTransposeError(2, f"{name} must be dense with shape {tuple(like.shape)}")
+    return t
+
+
+def attention_nd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, scale: Optional[float] = None,
+                 causal: bool = False, lengths: Optional[torch.Tensor] = None, starts: Optional[torch.Tensor] = None,
+                 out: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None,
+                 _prepare_only: bool = False) -> Tuple[torch.Tensor, torch.Tensor]:
+    """(out, lse): softmax(scale q k^T) v over tokens, and the logarithm of its denominators.
+
+    q: (N, Tq, H, D) float32/float16/bfloat16; k, v: (N, Tk, Hkv, D), Hkv dividing H (head h reads key
+    head h / (H / Hkv)); D up to 256, dense, the other axes with any strides: q, k and v may be
+    parts of one projection, or a cache.  A channels-last (N, C, D1..Dn) tensor is
+    ``x.movedim(1, -1).reshape(N, -1, H, C // H)``.  ``scale``: 1 / sqrt(D).  ``lengths``: (N,) int32,
+    keys of each image (what stands behind them is never looked at).  ``causal``: query i sees
+    the keys up to ``starts[n] + i``; ``starts``: (N,) int32, by default Tk - Tq.  A single token over a
+    cache gives ``lengths`` with it and ``starts = lengths - 1``.  A query that sees nothing
+    gives zeros and lse = -inf.  out is dense (N, Tq, H, D), lse (N, H, Tq) float32, for
+    ``attention_backward_nd``."""
+    lib = load_library()
+    sizes, operands, mask = _attention_args(q, k, v, scale, causal, lengths, starts)
+    nbytes = _attention_workspace(sizes, False) if _prepare_only else 0
+    with _on(stream):
+        out = _dense_like("out", out, q)
+        lse = torch.empty((q.shape[0], q.shape[2], q.shape[1]), dtype=torch.float32, device=q.device)
+        ws, wsb = _scratch(nbytes, q.device, _prepare_only)
+    args = (*sizes, *operands, *mask, _ptr(out), _ptr(lse), _ptr(ws), wsb, _stream_ptr(stream, q.device))
+    return _call(lib.attention_nd, args, (out, lse), ws, _prepare_only)
+
+
+def attention_backward_nd(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor,
+                          lse: torch.Tensor, *, scale: Optional[float] = None, causal: bool = False,
+                          lengths: Optional[torch.Tensor] = None, starts: Optional[torch.Tensor] = None,
+                          stream: Optional[torch.cuda.Stream] = None, _prepare_only: bool = False
+                          ) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """(dq, dk, dv): the gradient of ``attention_nd`` from out's gradient dout, its inputs, and the out and
+    lse it returned, with the same mask and scale.  dk and dv have k's shape: the query heads
+    that share a key head are summed.  Dense results; the probabilities are computed again, and the
+    sums have a fixed order."""
+    lib = load_library()
+    sizes, operands, mask = _attention_args(q, k, v, scale, causal, lengths, starts)
+    for name, t in (("dout", dout), ("out", out)):
+        _check_tensor(name, t, q.device, q.dtype)
+        if t.shape != q.shape:
+            raise ConvTransposeError(2, f"{name} has shape {tuple(t.shape)}, expected {tuple(q.shape)}")
+    _check_tensor("lse", lse, q.device, torch.float32)
+    if tuple(lse.shape) != (q.shape[0], q.shape[2], q.shape[1]) or not lse.is_contiguous():
+        raise ConvTransposeError(1, "lse must be a dense (N, H, Tq) tensor")
+    nbytes = _attention_workspace(sizes, True) if _prepare_only else 0
+    with _on(stream):
+        dq, dk, dv = (_dense_like(None, None, t) for t in (q, k, v))
+        ws, wsb = _scratch(nbytes, q.device, _prepare_only)
+    args = (*sizes, _ptr(dout), _token_strides("dout", dout), *operands, _ptr(out), _token_strides("out", out), _ptr(lse),
+            *mask, _ptr(dq), _ptr(dk), _ptr(dv), _ptr(ws), wsb, _stream_ptr(stream, q.device))
+    return _call(lib.attention_backward_nd, args, (dq, dk, dv), ws, _prepare_only)
+
+
+def rotary_nd(x: torch.Tensor, positions: torch.Tensor, sections: Sequence[int], *, base: float = 10000.0,
+              whole_ladder: bool = False, interleaved: bool = False, inverse: bool = False,
+              out: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None,
+              _prepare_only: bool = False) -> torch.Tensor:
+    """Rotary positions with several axes: the first ``2 * sum(sections)`` elements of each head are pairs that
+    turn by the token's positions, the rest is copied.
+
+    x: (N, T, H, D) float32/float16/bfloat16, heads dense, the other axes with any strides, so the
+    query and key heads of one projection turn in one call.  positions: (N, T, axes) int32/int64 (N and
+    T may be expanded), for instance a token's time, height and width.  ``sections``: pairs of
+    each axis; the j-th of a section of s turns ``base ** (-j / s)`` a position, or with
+    ``whole_ladder`` the p-th of all R pairs ``base ** (-p / R)``.  A pair is (p, p + R), or (2 p, 2 p + 1)
+    if ``interleaved``.  ``inverse`` turns back: the gradient of x is
+    ``rotary_nd(dy, ..., inverse=True)``.  ``out``: the caller's y, which may be x."""
+    lib = load_library()
+    if x.dtype not in _LAYER_DTYPES:
+        raise ConvTransposeError(3, f"dtype {x.dtype} is not served (float32, float16, bfloat16)")
+    _check_tensor("x", x, x.device, x.dtype)
+    strides = _token_strides("x", x)
+    if not isinstance(positions, torch.Tensor):
+        raise TypeError("positions must be a torch.Tensor")
+    if positions.dtype not in _INDEX_DTYPES:
+        raise ConvTransposeError(3, f"positions must be int32 or int64 (got {positions.dtype})")
+    _check_tensor("positions", positions, x.device, positions.dtype)
+    axes = len(sections)
+    if tuple(positions.shape) != (x.shape[0], x.shape[1], axes) or (axes > 1 and positions.stride(2) != 1):
+        raise ConvTransposeError(1, "positions must be (N, T, axes) with one section an axis, its axes dense")
+    if out is None:
+        with _on(stream):
+            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    else:
+        _check_tensor("out", out, x.device, x.dtype)
+        if out.shape != x.shape:
+            raise ConvTransposeError(2, f"out has shape {tuple(out.shape)}, expected {tuple(x.shape)}")
+        if out.data_ptr() == x.data_ptr() and out.stride() != x.stride():
+            raise ConvTransposeError(1, "out must have x's strides where it is x")
+        if any(size > 1 and st == 0 for size, st in zip(out.shape, out.stride())):
+            raise ConvTransposeError(1, "out must not be expanded")
+    args = (_LAYER_DTYPES[x.dtype], _i64(x.shape), _ptr(x), strides, _INDEX_DTYPES[positions.dtype], axes, _ptr(positions),
+            _i64(positions.stride()[:2]), _i64(sections), float(base), int(bool(whole_ladder)), int(bool(interleaved)),
+            int(bool(inverse)), _ptr(out), _token_strides("out", out), _stream_ptr(stream, x.device))
+    return _call(lib.rotary_nd, args, out, None, _prepare_only)
+
+
+class _AdamWTensor(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("param", "grad", "m", "v", "m_scale", "v_scale", "copy")] + [
+        ("count", ctypes.c_int64), ("weight_decay", ctypes.c_float)]
+
+
+def _device_scalar(name, value, dtype, device):
+    """(host value, pointer) of a number or of a one-element device tensor."""
+    if not isinstance(value, torch.Tensor):
+        return value, None
+    _check_tensor(name, value, device, dtype)
+    if value.numel() != 1:
+        raise ConvTransposeError(1, f"{name} must hold one value")
+    return 1, _ptr(value)
+
+
+def adamw_nd(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], ms: Sequence[torch.Tensor],
+             vs: Sequence[torch.Tensor], *, lr, step, betas: Tuple[float, float] = (0.9, 0.999), eps: float = 1e-8,
+             weight_decay=0.01, grad_scale=1.0, m_scales: Optional[Sequence[torch.Tensor]] = None,
+             v_scales: Optional[Sequence[torch.Tensor]] = None, copies: Optional[Sequence[Optional[torch.Tensor]]] = None,
+             stream: Optional[torch.cuda.Stream] = None, _prepare_only: bool = False) -> Tuple[torch.Tensor, ...]:
+    """One AdamW step over all ``params``, in place; returns them.
+
+    params: float32/float16/bfloat16, grads: any of these, all dense and of one type each.  ms, vs: the
+    moments, float32; or float8_e4m3fn with ``m_scales`` and ``v_scales``, a float32 for each 256
+    consecutive elements (m = value * scale, sqrt(v) = value * scale), all zeros at the start.
+    ``step``: the number of the step, from 1.  ``weight_decay``: one number, or one a tensor.
+    ``grad_scale``: multiplies the gradients (one over a loss scale).  ``copies``: float16 or bfloat16
+    tensors (or None) that receive the updated parameters too.  ``lr``, ``step`` and ``grad_scale`` may be
+    one-element device tensors (float32, int64, float32), read when the kernel runs, so a captured or
+    prepared call follows them."""
+    lib = load_library()
+    params, count = tuple(params), len(params)
+    lists = [("grads", grads), ("ms", ms), ("vs", vs)]
+    lists += [(n, t) for n, t in (("m_scales", m_scales), ("v_scales", v_scales), ("copies", copies)) if t is not None]
+    for name, t in lists:
+        if len(t) != count:
+            raise ConvTransposeError(1, f"{name} must hold one tensor a parameter")
+    decay = [float(weight_decay)] * count if not hasattr(weight_decay, "__len__") else [float(w) for w in weight_decay]
+    if len(decay) != count:
+        raise ConvTransposeError(1, "weight_decay must be one number, or one a parameter")
+    if not count:
+        if _prepare_only:
+            raise ConvTransposeError(1, "there are no parameters")
+        return params
+    dev, dtype, gtype, stype = params[0].device, params[0].dtype, grads[0].dtype, ms[0].dtype
+    if dtype not in _LAYER_DTYPES or gtype not in _LAYER_DTYPES:
+        raise ConvTransposeError(3, "params and grads must be float32, float16 or bfloat16")
+    if stype not in (torch.float32, torch.float8_e4m3fn):
+        raise ConvTransposeError(3, f"the moments must be float32 or float8_e4m3fn (got {stype})")
+    bits = 32 if stype == torch.float32 else 8
+    if (bits == 8) != (m_scales is not None) or (bits == 8) != (v_scales is not None):
+        raise ConvTransposeError(1, "m_scales and v_scales belong to moments in float8_e4m3fn")
+    written = [c for c in copies or () if c is not None]
+    ctype = written[0].dtype if written else torch.float16
+    if ctype not in (torch.float16, torch.bfloat16):
+        raise ConvTransposeError(3, f"copies must be float16 or bfloat16 (got {ctype})")
+    table, seen = (_AdamWTensor * count)(), set()
+    for i in range(count):
+        n = params[i].numel()
+        parts = [("params", params[i], dtype, n), ("grads", grads[i], gtype, n), ("ms", ms[i], stype, n), ("vs", vs[i], stype, n)]
+        for name, scales in (("m_scales", m_scales), ("v_scales", v_scales)):
+            parts.append((name, None if scales is None else scales[i], torch.float32, (n + 255) // 256))
+        parts.append(("copies", copies[i] if copies is not None else None, ctype, n))
+        for name, t, kind, size in parts:
+            if t is None:
+                continue
+            _check_tensor(name, t, dev, kind)
+            if t.numel() != size or not t.is_contiguous():
+                raise ConvTransposeError(1, f"{name}[{i}] must be dense with {size} elements")
+            if name != "grads" and size:
+                if t.data_ptr() in seen:
+                    raise ConvTransposeError(1, f"{name}[{i}] is there twice")
+                seen.add(t.data_ptr())
+        table[i] = _AdamWTensor(*(None if t is None else t.data_ptr() for _, t, _, _ in parts), n, decay[i])
+    lr, lr_at = _device_scalar("lr", lr, torch.float32, dev)
+    step, step_at = _device_scalar("step", step, torch.int64, dev)
+    grad_scale, scale_at = _device_scalar("grad_scale", grad_scale, torch.float32, dev)
+    args = (_LAYER_DTYPES[dtype], _LAYER_DTYPES[gtype], bits, _LAYER_DTYPES[ctype], count, table, float(lr), lr_at,
+            float(betas[0]), float(betas[1]), float(eps), int(step), step_at, float(grad_scale), scale_at,
+            _stream_ptr(stream, dev))
+    return _call(lib.adamw_nd, args, params, None, _prepare_only)
+
+
 class PreparedCall:
     """One call of ``convolution_nd``, ``qlinear_convtranspose_nd``, ``group_norm_nd``,
-    ``group_norm_backward_nd``, ``dropout_nd``, ``embedding_nd`` or
-    ``embedding_backward_nd`` with its arguments validated and marshalled once (and its
+    ``group_norm_backward_nd``, ``dropout_nd``, ``embedding_nd``, ``embedding_backward_nd``,
+    ``attention_nd``, ``attention_backward_nd``, ``rotary_nd`` or ``adamw_nd`` with its arguments validated and marshalled once (and its
     workspace, where it takes one, allocated): ``PreparedCall(convolution_nd, x, w, ...)``
     takes the function's own arguments; each call then enqueues the operation with a single
     C call, writing the same output tensors (``.out``).  Repeated calls must be ordered on
@@ -883,7 +1128,7 @@ class PreparedCall:
 
     def __init__(self, fn, *args, **kwargs):
         if fn not in (convolution_nd, qlinear_convtranspose_nd, group_norm_nd, group_norm_backward_nd, dropout_nd,
-                      embedding_nd, embedding_backward_nd):
+                      embedding_nd, embedding_backward_nd, attention_nd, attention_backward_nd, rotary_nd, adamw_nd):
             raise TypeError("PreparedCall serves the package's functions that take tensors and return new ones, "
                             "except convtranspose_nd (ConvTransposePlan)")
         self._fn, self._args, self.out, *keep = fn(*args, _prepare_only=True, **kwargs)

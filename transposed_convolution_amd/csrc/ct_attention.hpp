@@ -1,0 +1,299 @@
+// ct_attention.hpp -- what the attention kernels share: tiles in LDS that are read by rows and by
+// columns, fragments of the matrix instructions, and the launchers' declarations.
+//
+// The mathematics of all three kernels is laid out so that no value changes its lane.  A 32 x 32
+// product leaves lane l with column l % 32 and, in register r, row 8 (r / 4) + 4 (l / 32) + r % 4.
+// Its next use is as the right operand of a product whose sum runs over those rows: there lane l
+// has to bring 8 values of column l % 32 a step, and any 8 rows will do if the left operand brings
+// the same ones.  So registers 8 s .. 8 s + 7 go in as they are, and the left operand is read from
+// LDS by columns at the rows 16 s + 4 (l / 32) + {0..3, 8..11}: for 16-bit types two transposing
+// reads (ds_read_b64_tr_b16) an operand, for float32 eight words.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <type_traits>
+
+#include "ct_vec.hpp"
+
+namespace ct {
+
+constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
+constexpr int kMaxHead = 256;  // elements of a head that the kernels' registers hold
+
+// Token and head strides (elements) of a (N, T, H, D) tensor whose D is dense.
+struct Strided {
+    const void *p = nullptr;
+    int64_t n = 0, t = 0, h = 0;
+};
+
+// One call, either direction.  The G = H / Hkv query heads of a key head and the Tq tokens are
+// one axis of R = Tq * G rows, row = token * G + head: a tile of keys serves all of them, and a
+// single token still has G rows for the matrix instructions.
+struct Attention {
+    Strided q, k, v, o, d_o;   // o, d_o: the gradient's inputs
+    int64_t N = 0, Tq = 0, Tk = 0, H = 0, Hkv = 0;
+    int G = 1, D = 0;
+    int64_t R = 0;
+    float scale = 1.0f;
+    int causal = 0;
+    const int *lengths = nullptr, *starts = nullptr;
+    void *out = nullptr;       // forward: (N, Tq, H, D) dense
+    float *lse = nullptr;      // (N, H, Tq): written by the forward call, read by the gradient
+    void *dq = nullptr, *dk = nullptr, *dv = nullptr;
+    // partial results of calls whose work is split (see the launchers)
+    float *part = nullptr;
+    int splits = 1;
+
+    __device__ __forceinline__ int64_t length(int64_t n) const
+    {
+        if (!lengths) return Tk;
+        const int64_t l = lengths[n];
+        return l < 0 ? 0 : l < Tk ? l : Tk;
+    }
+    // Keys that token t of an image sees: the first seen(...) ones.
+    __device__ __forceinline__ int64_t seen(int64_t len, int64_t start, int64_t t) const
+    {
+        if (!causal) return len;
+        const int64_t e = start + t + 1;
+        return e < 0 ? 0 : e < len ? e : len;
+    }
+    __device__ __forceinline__ int64_t start(int64_t n) const { return starts ? int64_t(starts[n]) : Tk - Tq; }
+};
+
+using f32x16 = float __attribute__((ext_vector_type(16)));
+using f32x4 = float __attribute__((ext_vector_type(4)));
+
+template <class T>
+using Frag = T __attribute__((ext_vector_type(8)));  // 8 values of one row or column for a step of 16
+
+// A 32 x 32 product over 16, in float32 (float32 operands: 8 instructions over 2 each; the sum
+// runs over the same 16 whatever place a value has in it, as long as both operands agree).
+__device__ __forceinline__ f32x16 mma(Frag<_Float16> a, Frag<_Float16> b, f32x16 c)
+{
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x16 mma(Frag<__bf16> a, Frag<__bf16> b, f32x16 c)
+{
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x16 mma(Frag<float> a, Frag<float> b, f32x16 c)
+{
+#pragma unroll
+    for (int j = 0; j < 8; ++j) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a[j], b[j], c, 0, 0, 0);
+    return c;
+}
+
+// Registers 8 s .. 8 s + 7 of a product as an operand, one rounding to T.
+template <class T>
+__device__ __forceinline__ Frag<T> operand(const f32x16 &c, int s)
+{
+    Frag<float> v;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = c[8 * s + j];
+    return __builtin_convertvector(v, Frag<T>);
+}
+
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// Row of register r of a product.
+__device__ __forceinline__ constexpr int c_row(int r, int half) { return 8 * (r / 4) + 4 * half + r % 4; }
+
+// The values of lane l % 32 and of the lane 32 above it, in both.  (The elements go through
+// variables: a bit cast of a vector's element takes its first one.)
+__device__ __forceinline__ void both_halves(float x, float &low, float &high)
+{
+    const unsigned u = __builtin_bit_cast(unsigned, x);
+    const auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    const unsigned a = r[0], b = r[1];
+    low = __builtin_bit_cast(float, a);
+    high = __builtin_bit_cast(float, b);
+}
+__device__ __forceinline__ float half_max(float x)
+{
+    float a, b;
+    both_halves(x, a, b);
+    return fmaxf(a, b);
+}
+__device__ __forceinline__ float half_sum(float x)
+{
+    float a, b;
+    both_halves(x, a, b);
+    return a + b;
+}
+
+// 16 bytes of a row, of which the first `valid` elements exist; the others are 0.
+template <class T>
+__device__ __forceinline__ Raw<T, kVec<T>> load_chunk(const T *p, int valid)
+{
+    constexpr int V = kVec<T>;
+    if (valid >= V) return *reinterpret_cast<const Raw<T, V> *>(p);
+    Raw<T, V> r = {};
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+        if (j < valid) r[j] = p[j];
+    return r;
+}
+
+// 8 elements d .. d + 7 of a row of D, 0 behind it.
+template <class T>
+__device__ __forceinline__ Frag<T> load_frag(const T *row, int d, int D)
+{
+    constexpr int V = kVec<T>;
+    Frag<T> f;
+#pragma unroll
+    for (int c = 0; c < 8 / V; ++c) {
+        const Raw<T, V> r = load_chunk<T>(row + d + c * V, D - d - c * V);
+#pragma unroll
+        for (int j = 0; j < V; ++j) f[c * V + j] = r[j];
+    }
+    return f;
+}
+
+// A tile of rows of DP elements in LDS, in 16-byte chunks.  Chunk c of row r lies at c ^ turn(r),
+// which keeps both kinds of read free of bank conflicts: by rows, 16 lanes read one chunk of 16
+// consecutive rows; by columns, 32 lanes read 4 chunks of 4 consecutive rows.  A row has 4 g
+// chunks; g odd: 4 rows cover the 64 banks 4 chunks each and 2 bits are turned; g = 2 (mod 4):
+// 2 rows cover them, 3 bits; g = 0 (mod 4): 4 bits.
+template <class T, int DP>
+struct Tile {
+    static constexpr int kChunk = int(16 / sizeof(T)), kChunks = DP / kChunk, kG = kChunks / 4;
+    static_assert(DP % 32 == 0, "whole products over columns");
+    __device__ static __forceinline__ int turn(int row)
+    {
+        const int low = row >> 2 & 3;
+        return kG % 2 ? low : kG % 4 == 2 ? low | (row & 2) << 1 : low | (row & 3) << 2;
+    }
+    __device__ static __forceinline__ int at(int row, int chunk) { return row * DP + (chunk ^ turn(row)) * kChunk; }
+    // the 8 values of `row` for step ks: the elements 16 ks + 8 half ..
+    __device__ static __forceinline__ Frag<T> by_rows(const T *tile, int row, int ks, int half)
+    {
+        Frag<T> f;
+        if constexpr (sizeof(T) == 2) {
+            f = *reinterpret_cast<const Frag<T> *>(tile + at(row, ks * 2 + half));
+        } else {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const Raw<T, 4> r = *reinterpret_cast<const __attribute__((aligned(16))) Raw<T, 4> *>(tile + at(row, ks * 4 + half * 2 + c));
+#pragma unroll
+                for (int j = 0; j < 4; ++j) f[c * 4 + j] = r[j];
+            }
+        }
+        return f;
+    }
+    // the 8 values of column 32 db + lane % 32 at the rows row0 + 4 (lane / 32) + {0..3, 8..11};
+    // row0 a multiple of 16
+    __device__ static __forceinline__ Frag<T> by_columns(const T *tile, int row0, int db, int lane)
+    {
+        const int half = lane >> 5;
+        Frag<T> f;
+        if constexpr (sizeof(T) == 2) {
+            // 16 lanes read 4 rows of 16 elements; lane i gets column i of them
+            using V4 = short __attribute__((ext_vector_type(4)));
+            const int in = lane & 15, col = db * 32 + (lane & 16) + (in & 3) * 4;
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const int row = row0 + 8 * c + 4 * half + (in >> 2);
+                const T *p = tile + at(row, col / 8) + (col & 7);
+                const V4 r = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                    (__attribute__((address_space(3))) V4 *)(const_cast<T *>(p)));
+                const Raw<T, 4> v = __builtin_bit_cast(Raw<T, 4>, r);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) f[c * 4 + j] = v[j];
+            }
+        } else {
+            const int col = db * 32 + (lane & 31);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int row = row0 + 4 * half + (j & 3) + (j & 4) * 2;
+                f[j] = tile[at(row, col / 4) + (col & 3)];
+            }
+        }
+        return f;
+    }
+};
+
+// ROWS rows on their way from memory to a tile, 16 bytes a thread and piece.
+template <class T, int DP, int ROWS, int THREADS>
+struct Mover {
+    using L = Tile<T, DP>;
+    static constexpr int kPieces = ROWS * L::kChunks / THREADS;
+    static_assert(ROWS * L::kChunks % THREADS == 0, "every thread has as many pieces");
+    Raw<T, L::kChunk> r[kPieces];
+    // row(i): pointer to row i of the tile, or null for zeros
+    template <class F>
+    __device__ __forceinline__ void load(int tid, int D, F &&row)
+    {
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+            const int e = tid + i * THREADS, at = e / L::kChunks, c = e % L::kChunks;
+            const T *p = row(at);
+            r[i] = load_chunk<T>(p + c * L::kChunk, p ? D - c * L::kChunk : 0);
+        }
+    }
+    __device__ __forceinline__ void store(T *tile, int tid) const
+    {
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+            const int e = tid + i * THREADS;
+            *reinterpret_cast<__attribute__((aligned(16))) Raw<T, L::kChunk> *>(tile + L::at(e / L::kChunks, e % L::kChunks)) = r[i];
+        }
+    }
+};
+
+// Column `lane % 32` of a (DP x 32) product as a row of D elements of T.
+template <class T, int DB>
+__device__ __forceinline__ void store_columns(T *row, const f32x16 (&c)[DB], float factor, int D, int half)
+{
+#pragma unroll
+    for (int db = 0; db < DB; ++db)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int d = db * 32 + 8 * k + 4 * half;
+            Raw<T, 4> v;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] = T(c[db][4 * k + j] * factor);
+            if (d + 4 <= D) {
+                *reinterpret_cast<Raw<T, 4> *>(row + d) = v;
+            } else {
+#pragma unroll
+                for (int j = 0; j < 3; ++j)
+                    if (d + j < D) row[d + j] = v[j];
+            }
+        }
+}
+
+inline int padded_head(int64_t D) { return D <= 32 ? 32 : D <= 64 ? 64 : D <= 96 ? 96 : D <= 128 ? 128 : 256; }
+
+// Calls f with the padded head size as a constant.
+template <class F>
+inline void with_head(int64_t D, F &&f)
+{
+    switch (padded_head(D)) {
+    case 32: f(std::integral_constant<int, 32>{}); break;
+    case 64: f(std::integral_constant<int, 64>{}); break;
+    case 96: f(std::integral_constant<int, 96>{}); break;
+    case 128: f(std::integral_constant<int, 128>{}); break;
+    default: f(std::integral_constant<int, 256>{}); break;
+    }
+}
+
+// One instance a type, each in a file of its own.
+struct AttendPlan {
+    int waves = 4, row_tile = 128, splits = 1;
+    int64_t tiles = 0;
+    size_t bytes = 0;
+};
+AttendPlan attend_plan(const Attention &a, int dtype);
+template <class T>
+void launch_attend(Attention a, const AttendPlan &p, hipStream_t st);
+
+struct AttendGradPlan {
+    int key_splits = 1, row_splits = 1;      // of the query gradient, of the key and value gradient
+    size_t stat = 0, top = 0, part = 0, bytes = 0;  // offsets in the workspace, and its size
+};
+AttendGradPlan attend_grad_plan(const Attention &a, int dtype);
+template <class T>
+void launch_attend_grad(Attention a, const AttendGradPlan &p, char *ws, hipStream_t st);
+
+}  // namespace ct
