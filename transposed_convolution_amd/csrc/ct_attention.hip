@@ -11,42 +11,53 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 size_t align16(size_t n) { return (n + 15) & ~size_t(15); }
 }  // namespace
 
-// Blocks wanted before a call's work is split over its keys (and joined by a second kernel).
-constexpr int64_t kWantBlocks = 512;
+// Blocks wanted before a call's work is split over its keys (and joined by a second kernel), and the
+// keys a split should have.
+constexpr int64_t kWantBlocks = 512, kWantFewBlocks = 512, kLeastKeys = 256, kLeastFewKeys = 128;
+constexpr int kMostSplits = 64;
 
 AttendPlan attend_plan(const Attention &a, int dtype)
 {
     AttendPlan p;
-    (void)dtype;
-    p.waves = a.R <= 32 ? 1 : 4;
-    p.row_tile = p.waves * 32;
-    p.tiles = ceil_div(a.R, p.row_tile);
-    const int64_t base = a.N * a.Hkv * p.tiles, least = 256;  // keys a split should have
-    if (base > 0 && base < kWantBlocks)
-        p.splits = int(std::max<int64_t>(1, std::min({ceil_div(kWantBlocks, base), ceil_div(a.Tk, least), int64_t(64)})));
-    if (p.splits > 1) p.bytes = size_t(p.splits) * size_t(a.N * a.Hkv * a.R) * size_t(a.D + 2) * 4;
+    const int64_t heads = int64_t(a.N) * a.Hkv;
+    p.few = a.R <= 32;
+    p.tiles = p.few ? 1 : int(ceil_div(a.R, 128));
+    const int64_t base = heads * p.tiles, wanted = p.few ? kWantFewBlocks : kWantBlocks, least = p.few ? kLeastFewKeys : kLeastKeys;
+    if (base > 0 && base < wanted)
+        p.splits = int(std::max<int64_t>(1, std::min({ceil_div(wanted, base), ceil_div(a.Tk, least), int64_t(kMostSplits)})));
+    if (p.splits > 1) p.bytes = size_t(p.splits) * size_t(heads * a.R) * size_t(a.D + 2) * 4;
     return p;
 }
 
 AttendGradPlan attend_grad_plan(const Attention &a, int dtype)
 {
     AttendGradPlan p;
-    const int64_t heads = a.N * a.Hkv, key_blocks = heads * ceil_div(a.Tk, 128), row_blocks = heads * ceil_div(a.R, 128);
-    auto split = [](int64_t blocks, int64_t length) {
-        if (blocks == 0 || blocks >= kWantBlocks / 2) return 1;
-        return int(std::max<int64_t>(1, std::min({ceil_div(kWantBlocks, blocks), ceil_div(length, 512), int64_t(64)})));
+    const int64_t heads = int64_t(a.N) * a.Hkv;
+    // Blocks of 4 waves share what they read, blocks of one wave make more of a small call: those
+    // are taken where 4-wave blocks, split as far as is sensible, would not fill the chip.
+    auto chunk = [&](int waves, int64_t blocks, int64_t length) {
+        const int64_t wanted = waves == 1 ? 2048 : 512, least = waves == 1 ? 64 : 512, step = 64;
+        if (blocks == 0 || length == 0 || blocks >= wanted) return std::max<int64_t>(1, length);
+        const int64_t splits = std::max<int64_t>(1, std::min({wanted * 2 / blocks, ceil_div(length, least), int64_t(kMostSplits)}));
+        return ceil_div(ceil_div(length, splits), step) * step;
     };
-    p.row_splits = split(key_blocks, a.R);
-    p.key_splits = split(row_blocks, a.Tk);
+    const int64_t most = std::max(a.Tk, a.R);
+    p.waves = heads * ceil_div(most, 128) * std::max<int64_t>(1, std::min<int64_t>(a.Tk, a.R) / 512) >= 256 ? 4 : 1;
+    const int64_t span = 32 * p.waves;
+    p.row_chunk = int(chunk(p.waves, heads * ceil_div(a.Tk, span), a.R));
+    p.key_chunk = int(chunk(p.waves, heads * ceil_div(a.R, span), a.Tk));
+    p.row_splits = int(std::max<int64_t>(1, ceil_div(a.R, p.row_chunk)));
+    p.key_splits = int(std::max<int64_t>(1, ceil_div(a.Tk, p.key_chunk)));
     size_t at = 0;
     p.stat = at;
     at = align16(at + size_t(heads * a.R) * 8);
     p.top = at;
     if (dtype == CT_FLOAT16) at = align16(at + size_t(heads * (ceil_div(a.R, 64) + ceil_div(a.Tk, 64))) * 4);
-    p.part = at;
-    const size_t keys = p.row_splits > 1 ? size_t(p.row_splits) * size_t(2 * a.Tk * heads * a.D) * 4 : 0;
-    const size_t rows = p.key_splits > 1 ? size_t(p.key_splits) * size_t(a.R * heads * a.D) * 4 : 0;
-    p.bytes = at + std::max(keys, rows);
+    p.key_part = at;
+    if (p.row_splits > 1) at = align16(at + size_t(p.row_splits) * size_t(2 * a.Tk * heads * a.D) * 4);
+    p.row_part = at;
+    if (p.key_splits > 1) at = align16(at + size_t(p.key_splits) * size_t(a.R * heads * a.D) * 4);
+    p.bytes = at;
     return p;
 }
 
@@ -62,7 +73,7 @@ ct_status fail(ct_status st, const std::string &msg)
     return st;
 }
 
-// Sizes of a call, checked; *launch is false where there is nothing to compute.
+// Sizes of a call, checked.
 ct_status sizes(int dt, const int64_t *q_shape, int64_t tk, int64_t kv_heads, Attention *a, std::string *err)
 {
     auto bad = [&](ct_status st, const char *msg) {
@@ -84,17 +95,19 @@ ct_status sizes(int dt, const int64_t *q_shape, int64_t tk, int64_t kv_heads, At
         if (x == 0 || y == 0 || z == 0) return int64_t(0);
         return x > most || y > most || z > most || x > most / y || x * y > most / z ? most + 1 : x * y * z;
     };
-    if (q_shape[1] > most || tk > most || q_shape[0] > most || product(q_shape[0], q_shape[1], q_shape[2]) > most ||
-        product(q_shape[0], tk, kv_heads) > most || product(q_shape[0], kv_heads, 1) > (1 << 22))
+    if (q_shape[0] > most || q_shape[1] > most || q_shape[2] > most || tk > most || product(q_shape[0], q_shape[1], q_shape[2]) > most ||
+        product(q_shape[0], tk, kv_heads) > most || product(q_shape[0], kv_heads, 1) > (1 << 22) ||
+        product(q_shape[1], q_shape[2], 1) > most)
         return bad(CT_EUNSUPPORTED, "more than 2^30 rows of queries or keys, or 2^22 images times key heads");
-    a->N = q_shape[0];
-    a->Tq = q_shape[1];
-    a->H = q_shape[2];
+    a->N = int(q_shape[0]);
+    a->Tq = int(q_shape[1]);
+    a->H = int(q_shape[2]);
     a->D = int(q_shape[3]);
-    a->Tk = tk;
-    a->Hkv = kv_heads;
-    a->G = int(a->H / kv_heads);
+    a->Tk = int(tk);
+    a->Hkv = int(kv_heads);
+    a->G = a->H / a->Hkv;
     a->R = a->Tq * a->G;
+    a->by_g = ct::Div31(a->G);
     return CT_OK;
 }
 
@@ -140,6 +153,10 @@ ct_status operand(const char *name, const void *p, const int64_t *strides, bool 
             *err = std::string("the strides of ") + name + " must lie in 0 .. 2^40";
             return CT_EINVAL;
         }
+    if (strides[1] > ct::kMaxTokenStride) {
+        *err = std::string("more than 2^24 elements from token to token of ") + name + " are not served";
+        return CT_EUNSUPPORTED;
+    }
     *s = {p, strides[0], strides[1], strides[2]};
     return CT_OK;
 }
@@ -176,9 +193,8 @@ extern "C" ct_status attention_nd(ct_dtype dtype, const int64_t *q_shape, int64_
     ct::Scratch ws;
     st = ws.take(workspace, workspace_bytes, p.bytes, hs, &err);
     if (st != CT_OK) return fail(st, err);
-    a.part = static_cast<float *>(ws.p);
     ct::mark_before(hs);
-    ct::with_type(dt, [&](auto t) { ct::launch_attend<decltype(t)>(a, p, hs); });
+    ct::with_type(dt, [&](auto t) { ct::launch_attend<decltype(t)>(a, p, static_cast<float *>(ws.p), hs); });
     ct::mark_after(hs);
     st = ct::launch_status("attention launch failed", &err);
     return st == CT_OK ? CT_OK : fail(st, err);

@@ -21,44 +21,55 @@ namespace ct {
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
 constexpr int kMaxHead = 256;  // elements of a head that the kernels' registers hold
 
-// Token and head strides (elements) of a (N, T, H, D) tensor whose D is dense.
+// Strides (elements) of the image, token and head axes of an (N, T, H, D) tensor whose D is dense.  A
+// token's is at most 2^24, so that the 64 rows of a tile are 32-bit byte offsets from its start.
 struct Strided {
     const void *p = nullptr;
     int64_t n = 0, t = 0, h = 0;
 };
+constexpr int64_t kMaxTokenStride = int64_t(1) << 24;
+
+// Division of u < 2^31 by d >= 1: with s = ceil(log2 d) and m = ceil(2^(31 + s) / d) the error of m is
+// below 2^s / d, that of 2 u m / 2^(32 + s) below 1 / d.
+struct Div31 {
+    unsigned m = 0x80000000u;
+    int s = 0, d = 1;
+    Div31() = default;
+    explicit Div31(int dv) : d(dv)
+    {
+        while ((int64_t(1) << s) < d) ++s;
+        m = unsigned(((uint64_t(1) << (31 + s)) + d - 1) / d);
+    }
+    __device__ __forceinline__ int div(int u) const { return int(__umulhi(unsigned(u) << 1, m) >> s); }
+};
 
 // One call, either direction.  The G = H / Hkv query heads of a key head and the Tq tokens are
 // one axis of R = Tq * G rows, row = token * G + head: a tile of keys serves all of them, and a
-// single token still has G rows for the matrix instructions.
+// single token still has G rows for the matrix instructions.  Tokens, rows and keys are below 2^30.
 struct Attention {
     Strided q, k, v, o, d_o;   // o, d_o: the gradient's inputs
-    int64_t N = 0, Tq = 0, Tk = 0, H = 0, Hkv = 0;
-    int G = 1, D = 0;
-    int64_t R = 0;
+    int N = 0, Tq = 0, Tk = 0, H = 0, Hkv = 0, G = 1, D = 0, R = 0;
+    Div31 by_g;
     float scale = 1.0f;
     int causal = 0;
     const int *lengths = nullptr, *starts = nullptr;
     void *out = nullptr;       // forward: (N, Tq, H, D) dense
     float *lse = nullptr;      // (N, H, Tq): written by the forward call, read by the gradient
     void *dq = nullptr, *dk = nullptr, *dv = nullptr;
-    // partial results of calls whose work is split (see the launchers)
-    float *part = nullptr;
-    int splits = 1;
 
-    __device__ __forceinline__ int64_t length(int64_t n) const
-    {
-        if (!lengths) return Tk;
-        const int64_t l = lengths[n];
-        return l < 0 ? 0 : l < Tk ? l : Tk;
-    }
+    __device__ __forceinline__ int length(int n) const { return lengths ? max(0, min(lengths[n], Tk)) : Tk; }
+    // The place of an image's first query among the keys, within what makes a difference.
+    __device__ __forceinline__ int start(int n) const { return starts ? max(-Tq, min(starts[n], Tk)) : Tk - Tq; }
     // Keys that token t of an image sees: the first seen(...) ones.
-    __device__ __forceinline__ int64_t seen(int64_t len, int64_t start, int64_t t) const
+    __device__ __forceinline__ int seen(int len, int start, int t) const
     {
-        if (!causal) return len;
-        const int64_t e = start + t + 1;
-        return e < 0 ? 0 : e < len ? e : len;
+        return causal ? max(0, min(start + t + 1, len)) : len;
     }
-    __device__ __forceinline__ int64_t start(int64_t n) const { return starts ? int64_t(starts[n]) : Tk - Tq; }
+    // The first token that sees a key at all.
+    __device__ __forceinline__ int first_token(int len, int start) const
+    {
+        return len == 0 ? Tq : causal ? max(0, -start) : 0;
+    }
 };
 
 using f32x16 = float __attribute__((ext_vector_type(16)));
@@ -122,16 +133,38 @@ __device__ __forceinline__ float half_sum(float x)
     return a + b;
 }
 
-// 16 bytes of a row, of which the first `valid` elements exist; the others are 0.
+// 16 bytes of a row, of which the first `valid` elements exist; the others are 0.  Where a row does not end
+// with a whole chunk its last one has `tail` elements, the same number everywhere: loads of 4, 2 and
+// 1 of them as it takes, not one an element.
 template <class T>
-__device__ __forceinline__ Raw<T, kVec<T>> load_chunk(const T *p, int valid)
+__device__ __forceinline__ Raw<T, kVec<T>> load_chunk(const T *p, int valid, int tail)
 {
     constexpr int V = kVec<T>;
-    if (valid >= V) return *reinterpret_cast<const Raw<T, V> *>(p);
     Raw<T, V> r = {};
+    if (valid >= V) r = *reinterpret_cast<const Raw<T, V> *>(p);
+    if (tail && valid > 0 && valid < V) {
+        using U1 = std::conditional_t<sizeof(T) == 2, unsigned short, unsigned>;
+        using U2 = U1 __attribute__((ext_vector_type(2), aligned(sizeof(T))));
+        using U4 = U1 __attribute__((ext_vector_type(4), aligned(sizeof(T))));
+        const U1 *q = reinterpret_cast<const U1 *>(p);
+        U4 four = {};
+        U2 two = {};
+        U1 one = 0;
+        if (V == 8 && tail & 4) four = *reinterpret_cast<const U4 *>(q);
+        if (tail & 2) two = *reinterpret_cast<const U2 *>(q + (tail & 4));
+        if (tail & 1) one = q[tail & 6];
+        U1 u[V];
 #pragma unroll
-    for (int j = 0; j < V; ++j)
-        if (j < valid) r[j] = p[j];
+        for (int j = 0; j < V; ++j) {
+            const int in2 = j - (tail & 4), in1 = j - (tail & 6);
+            U1 v = in1 == 0 && tail & 1 ? one : U1(0);
+            if (tail & 2) v = in2 == 0 ? two[0] : in2 == 1 ? two[1] : v;
+            if (V == 8 && j < 4 && tail & 4) v = four[j & 3];
+            u[j] = v;
+        }
+#pragma unroll
+        for (int j = 0; j < V; ++j) r[j] = __builtin_bit_cast(T, u[j]);
+    }
     return r;
 }
 
@@ -143,7 +176,7 @@ __device__ __forceinline__ Frag<T> load_frag(const T *row, int d, int D)
     Frag<T> f;
 #pragma unroll
     for (int c = 0; c < 8 / V; ++c) {
-        const Raw<T, V> r = load_chunk<T>(row + d + c * V, D - d - c * V);
+        const Raw<T, V> r = load_chunk<T>(row + d + c * V, D - d - c * V, D % V);
 #pragma unroll
         for (int j = 0; j < V; ++j) f[c * V + j] = r[j];
     }
@@ -181,6 +214,17 @@ struct Tile {
         }
         return f;
     }
+    // their place in the tile
+    __device__ static __forceinline__ void put(T *tile, int row, int ks, int half, const Frag<T> &f)
+    {
+#pragma unroll
+        for (int c = 0; c < 8 / kChunk; ++c) {
+            Raw<T, kChunk> r;
+#pragma unroll
+            for (int j = 0; j < kChunk; ++j) r[j] = f[c * kChunk + j];
+            *reinterpret_cast<__attribute__((aligned(16))) Raw<T, kChunk> *>(tile + at(row, (ks * 2 + half) * (8 / kChunk) + c)) = r;
+        }
+    }
     // the 8 values of column 32 db + lane % 32 at the rows row0 + 4 (lane / 32) + {0..3, 8..11};
     // row0 a multiple of 16
     __device__ static __forceinline__ Frag<T> by_columns(const T *tile, int row0, int db, int lane)
@@ -213,30 +257,56 @@ struct Tile {
     }
 };
 
-// ROWS rows on their way from memory to a tile, 16 bytes a thread and piece.
+// ROWS rows on their way from memory to a tile, 16 bytes a thread and piece; the threads of a row are a
+// power of two, so that a thread keeps its column.
 template <class T, int DP, int ROWS, int THREADS>
 struct Mover {
     using L = Tile<T, DP>;
-    static constexpr int kPieces = ROWS * L::kChunks / THREADS;
-    static_assert(ROWS * L::kChunks % THREADS == 0, "every thread has as many pieces");
-    Raw<T, L::kChunk> r[kPieces];
-    // row(i): pointer to row i of the tile, or null for zeros
-    template <class F>
-    __device__ __forceinline__ void load(int tid, int D, F &&row)
+    using Chunk = Raw<T, L::kChunk>;
+    static constexpr int kLanes = L::kChunks <= 4 ? 4 : L::kChunks <= 8 ? 8 : L::kChunks <= 16 ? 16 : L::kChunks <= 32 ? 32 : 64;
+    static constexpr int kStep = THREADS / kLanes, kPieces = ROWS / kStep;
+    static_assert(ROWS % kStep == 0 && THREADS % kLanes == 0, "every thread has as many pieces");
+    Chunk r[kPieces];
+    int row0, column;  // of the thread: first row, first element
+    __device__ __forceinline__ explicit Mover(int tid) : row0(tid / kLanes), column(tid % kLanes * L::kChunk)
     {
 #pragma unroll
-        for (int i = 0; i < kPieces; ++i) {
-            const int e = tid + i * THREADS, at = e / L::kChunks, c = e % L::kChunks;
-            const T *p = row(at);
-            r[i] = load_chunk<T>(p + c * L::kChunk, p ? D - c * L::kChunk : 0);
+        for (int i = 0; i < kPieces; ++i) r[i] = Chunk{};
+    }
+    // Rows base + row * stride, of which the first `valid` exist; the others become zeros.
+    __device__ __forceinline__ void load(const T *base, int64_t stride, int valid, int D)
+    {
+        const unsigned at = unsigned(row0 * int(stride) + column) * unsigned(sizeof(T));
+        const char *p = reinterpret_cast<const char *>(base);
+        const int64_t step = kStep * stride * int64_t(sizeof(T));
+        if (valid >= ROWS && D % L::kChunk == 0) {
+            // threads behind the row's end keep the zeros they began with
+            if (column < D) {
+#pragma unroll
+                for (int i = 0; i < kPieces; ++i) r[i] = *reinterpret_cast<const Chunk *>(p + i * step + at);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i)
+                r[i] = load_chunk<T>(reinterpret_cast<const T *>(p + i * step + at), row0 + i * kStep < valid ? D - column : 0, D % L::kChunk);
         }
     }
-    __device__ __forceinline__ void store(T *tile, int tid) const
+    // Rows row(i), null for zeros.
+    template <class F>
+    __device__ __forceinline__ void load(int D, F &&row)
     {
 #pragma unroll
         for (int i = 0; i < kPieces; ++i) {
-            const int e = tid + i * THREADS;
-            *reinterpret_cast<__attribute__((aligned(16))) Raw<T, L::kChunk> *>(tile + L::at(e / L::kChunks, e % L::kChunks)) = r[i];
+            const T *p = row(row0 + i * kStep);
+            r[i] = load_chunk<T>(p + column, p ? D - column : 0, D % L::kChunk);
+        }
+    }
+    __device__ __forceinline__ void store(T *tile) const
+    {
+        if (L::kChunks == kLanes || column < DP) {
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i)
+                *reinterpret_cast<__attribute__((aligned(16))) Chunk *>(tile + L::at(row0 + i * kStep, column / L::kChunk)) = r[i];
         }
     }
 };
@@ -278,22 +348,27 @@ inline void with_head(int64_t D, F &&f)
     }
 }
 
-// One instance a type, each in a file of its own.
+// How a call's work is cut.  Forward: calls of up to 32 rows a key head (a few tokens) have a kernel
+// whose waves take keys each; others give a wave 32 rows.  `splits` parts of the keys (or
+// rows) go to different blocks and are joined by a second kernel.
 struct AttendPlan {
-    int waves = 4, row_tile = 128, splits = 1;
-    int64_t tiles = 0;
-    size_t bytes = 0;
+    bool few = false;
+    int tiles = 0, splits = 1;
+    size_t bytes = 0;    // workspace: the parts of splits
 };
 AttendPlan attend_plan(const Attention &a, int dtype);
 template <class T>
-void launch_attend(Attention a, const AttendPlan &p, hipStream_t st);
+void launch_attend(const Attention &a, const AttendPlan &p, float *part, hipStream_t st);
 
+// The gradient: key blocks take the rows in chunks, row blocks the keys; more than one chunk leaves
+// parts that are joined.
 struct AttendGradPlan {
-    int key_splits = 1, row_splits = 1;      // of the query gradient, of the key and value gradient
-    size_t stat = 0, top = 0, part = 0, bytes = 0;  // offsets in the workspace, and its size
+    int waves = 4, row_chunk = 1, key_chunk = 1;
+    int key_splits = 1, row_splits = 1;             // of the query gradient, of the key and value gradient
+    size_t stat = 0, top = 0, key_part = 0, row_part = 0, bytes = 0;  // offsets in the workspace, and its size
 };
 AttendGradPlan attend_grad_plan(const Attention &a, int dtype);
 template <class T>
-void launch_attend_grad(Attention a, const AttendGradPlan &p, char *ws, hipStream_t st);
+void launch_attend_grad(const Attention &a, const AttendGradPlan &p, char *ws, hipStream_t st);
 
 }  // namespace ct

@@ -2,7 +2,7 @@
 //
 //   s_ij = scale q_i . k_j,  lse_i = log sum_j exp s_ij,  o_i = sum_j exp(s_ij - lse_i) v_j
 //
-// over the keys j that row i sees.  Tiles of keys and values go through LDS; a running reference m
+// over the keys j that row i sees.  Keys and values go through LDS; a running reference m
 // (near the largest score so far) keeps the exponentials in range, and the sum l and the output o
 // are scaled when it moves.  Scores, sums and outputs stay in float32 registers; the weights are
 // rounded once to the values' type for the second product.
@@ -19,214 +19,350 @@ constexpr float kSlack = 8.0f;
 template <class T>
 constexpr float kWeightBias = std::is_same_v<T, _Float16> ? 7.0f : 0.0f;
 
-template <class T, int DP, int QB, int WAVES, int KT>
-__global__ __launch_bounds__(WAVES * 64) void attend_kernel(Attention a, int64_t tiles)
+// The softmax of a row so far: reference m (in powers of two), sum l of 2^(s c - m + bias), this lane's
+// half of it.
+struct Running {
+    float m = -INFINITY, l = 0.0f;
+    // Moves the reference for a tile's scores, and scales the output where it does.
+    template <int KB, int DB>
+    __device__ __forceinline__ void look(const f32x16 (&s)[KB], f32x16 (&o)[DB], float c)
+    {
+        float top = s[0][0];
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) top = fmaxf(top, s[kb][r]);
+        top = half_max(top) * c;
+        const bool moves = top > m + kSlack || (m == -INFINITY && top > -INFINITY);
+        if (__any(moves)) {
+            const float to = moves ? top : m;
+            const float f = moves ? exp2_fast(m - to) : 1.0f;
+            m = to;
+            l *= f;
+#pragma unroll
+            for (int db = 0; db < DB; ++db)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) o[db][r] *= f;
+        }
+    }
+    // Scores become weights.
+    template <class T, int KB>
+    __device__ __forceinline__ void weigh(f32x16 (&s)[KB], float c)
+    {
+        const float base = m == -INFINITY ? 0.0f : m - kWeightBias<T>;
+        float sum[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                const float e = exp2_fast(fmaf(s[kb][r], c, -base));
+                s[kb][r] = e;
+                sum[r & 1] += e;
+            }
+        l += sum[0] + sum[1];
+    }
+};
+
+// Scores of keys at or behind `end` (of the tile's) become -inf.
+template <int KB>
+__device__ __forceinline__ void hide(f32x16 (&s)[KB], int end, int half)
+{
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) s[kb][r] = kb * 32 + c_row(r, half) < end ? s[kb][r] : -INFINITY;
+}
+
+// Where a row's parts lie in the workspace: (m, l) of every split and row, then the outputs.
+struct Parts {
+    float *stat, *out;
+    int64_t rows;
+    int D;
+    __device__ __forceinline__ Parts(float *p, const Attention &a, int splits)
+        : stat(p), out(p + 2 * int64_t(splits) * a.N * a.Hkv * a.R), rows(int64_t(a.N) * a.Hkv * a.R), D(a.D)
+    {
+    }
+};
+
+// The result of a row: stored, or left as a part.
+template <class T, int DB>
+__device__ __forceinline__ void finish(const Attention &a, float *part, int splits, int split, int nh, int n, int hk, int row,
+                                       int half, float m, float l, const f32x16 (&o)[DB])
+{
+    const int t = a.by_g.div(row), h = hk * a.G + row - t * a.G;
+    const float to = m - kWeightBias<T>;
+    if (splits == 1) {
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        store_columns<T, DB>(static_cast<T *>(a.out) + ((int64_t(n) * a.Tq + t) * a.H + h) * a.D, o, inv, a.D, half);
+        if (half == 0) a.lse[(int64_t(n) * a.H + h) * a.Tq + t] = l == 0.0f ? -INFINITY : (to + __log2f(l)) * kLn2;
+    } else {
+        const Parts ps(part, a, splits);
+        const int64_t at = split * ps.rows + int64_t(nh) * a.R + row;
+        if (half == 0) {
+            ps.stat[2 * at] = l == 0.0f ? -INFINITY : to;
+            ps.stat[2 * at + 1] = l;
+        }
+        store_columns<float, DB>(ps.out + at * a.D, o, 1.0f, a.D, half);
+    }
+}
+
+// A wave holds 32 rows, a block goes through the keys KT at a time; the next tile is on its way while one
+// is worked on.
+template <class T, int DP, int WAVES, int KT>
+__global__ __launch_bounds__(WAVES * 64, DP * sizeof(T) <= 256 ? 2 : 1) void attend_kernel(Attention a, float *part, int tiles, int splits)
 {
     using L = Tile<T, DP>;
-    constexpr int KS = DP / 16, DB = DP / 32, KB = KT / 32, THREADS = WAVES * 64;
+    constexpr int KS = DP / 16, DB = DP / 32, KB = KT / 32, THREADS = WAVES * 64, ROWS = WAVES * 32;
     __shared__ __attribute__((aligned(16))) T lds[2][2][KT * DP];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, half = lane >> 5;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), half = lane >> 5;
 
     // an XCD takes a contiguous run of blocks: those of one image and key head share its L2; a
     // causal call's long tiles go first
-    int64_t w = xcd_remap(blockIdx.x, gridDim.x);
-    const int split = int(w % a.splits);
-    w /= a.splits;
-    const int64_t tile = tiles - 1 - w % tiles, nh = w / tiles;
-    const int64_t n = nh / a.Hkv, hk = nh % a.Hkv;
-    const int64_t len = a.length(n), start = a.start(n);
-    const int64_t row0 = tile * (WAVES * QB * 32) + wave * (QB * 32);
+    int w = xcd_remap(blockIdx.x, gridDim.x);
+    const int split = w % splits;
+    w /= splits;
+    const int tile = tiles - 1 - w % tiles, nh = w / tiles, n = nh / a.Hkv, hk = nh % a.Hkv;
+    const int len = a.length(n), start = a.start(n);
+    const int block_row = tile * ROWS, row0 = block_row + wave * 32;
 
-    Frag<T> q[QB][KS];
-    int64_t seen[QB];
+    const int row = row0 + (lane & 31), t = a.by_g.div(row);
+    const bool there = row < a.R;
+    const int seen = there ? a.seen(len, start, t) : 0;
+    Frag<T> q[KS];
+    const T *qp = static_cast<const T *>(a.q.p) + n * a.q.n + t * a.q.t + (hk * a.G + row - t * a.G) * a.q.h;
 #pragma unroll
-    for (int qb = 0; qb < QB; ++qb) {
-        const int64_t row = row0 + qb * 32 + (lane & 31), t = row / a.G, g = row % a.G;
-        const bool there = row < a.R;
-        seen[qb] = there ? a.seen(len, start, t) : 0;
-        const T *p = static_cast<const T *>(a.q.p) + n * a.q.n + t * a.q.t + (hk * a.G + g) * a.q.h;
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks) q[qb][ks] = load_frag<T>(p, ks * 16 + half * 8, there ? a.D : 0);
-    }
+    for (int ks = 0; ks < KS; ++ks) q[ks] = load_frag<T>(qp, ks * 16 + half * 8, there ? a.D : 0);
     // keys the block looks at, and this split's share of them in whole tiles
-    const int64_t last = min(tile * (WAVES * QB * 32) + WAVES * QB * 32, a.R) - 1;
-    const int64_t want = (a.seen(len, start, last / a.G) + KT - 1) / KT, each = (want + a.splits - 1) / a.splits;
-    const int64_t kt0 = split * each, kt1 = min(want, kt0 + each);
+    const int want = (a.seen(len, start, a.by_g.div(min(block_row + ROWS, a.R) - 1)) + KT - 1) / KT;
+    const int each = (want + splits - 1) / splits, kt0 = split * each, kt1 = min(want, kt0 + each);
     // of this wave's rows: tiles before `whole` are seen by every row, tiles from `none` on by none
-    const int64_t first_seen = row0 < a.R ? a.seen(len, start, row0 / a.G) : 0;
-    const int64_t last_seen = row0 < a.R ? a.seen(len, start, (min(row0 + QB * 32, a.R) - 1) / a.G) : 0;
-    const int64_t whole = first_seen / KT, none = (last_seen + KT - 1) / KT;
+    const bool rows = row0 < a.R;
+    const int whole = rows ? a.seen(len, start, a.by_g.div(row0)) / KT : 0;
+    const int none = rows ? (a.seen(len, start, a.by_g.div(min(row0 + 32, a.R) - 1)) + KT - 1) / KT : 0;
 
     const T *kp = static_cast<const T *>(a.k.p) + n * a.k.n + hk * a.k.h;
     const T *vp = static_cast<const T *>(a.v.p) + n * a.v.n + hk * a.v.h;
-    Mover<T, DP, KT, THREADS> km, vm;
-    auto load = [&](int64_t kt) {
-        // rows behind the length are zeros: what stands there takes no part
-        km.load(tid, a.D, [&](int r) { return kt * KT + r < len ? kp + (kt * KT + r) * a.k.t : nullptr; });
-        vm.load(tid, a.D, [&](int r) { return kt * KT + r < len ? vp + (kt * KT + r) * a.v.t : nullptr; });
+    Mover<T, DP, KT, THREADS> km(tid), vm(tid);
+    // keys behind the length are zeros: what stands there takes no part
+    auto load = [&](int kt) {
+        km.load(kp + int64_t(kt) * KT * a.k.t, a.k.t, len - kt * KT, a.D);
+        vm.load(vp + int64_t(kt) * KT * a.v.t, a.v.t, len - kt * KT, a.D);
+    };
+    auto store = [&](int buf) {
+        km.store(lds[buf][0]);
+        vm.store(lds[buf][1]);
     };
 
-    f32x16 o[QB][DB];
-    float m[QB], l[QB];
+    f32x16 o[DB];
+    Running run;
 #pragma unroll
-    for (int qb = 0; qb < QB; ++qb) {
-        m[qb] = -INFINITY;
-        l[qb] = 0.0f;
-#pragma unroll
-        for (int db = 0; db < DB; ++db) o[qb][db] = f32x16{};
-    }
+    for (int db = 0; db < DB; ++db) o[db] = f32x16{};
     const float c = a.scale * kLog2e;
-
     if (kt0 < kt1) {
         load(kt0);
-        km.store(lds[0][0], tid);
-        vm.store(lds[0][1], tid);
+        store(0);
     }
-    for (int64_t kt = kt0; kt < kt1; ++kt) {
+    for (int kt = kt0; kt < kt1; ++kt) {
         __syncthreads();
-        const int buf = int(kt - kt0) & 1;
+        const int buf = (kt - kt0) & 1;
         if (kt + 1 < kt1) load(kt + 1);
         if (kt < none) {
             const T *kl = lds[buf][0], *vl = lds[buf][1];
-            f32x16 s[QB][KB];
+            f32x16 s[KB];
 #pragma unroll
             for (int kb = 0; kb < KB; ++kb) {
+                s[kb] = f32x16{};
 #pragma unroll
-                for (int qb = 0; qb < QB; ++qb) s[qb][kb] = f32x16{};
-#pragma unroll
-                for (int ks = 0; ks < KS; ++ks) {
-                    const Frag<T> kf = L::by_rows(kl, kb * 32 + (lane & 31), ks, half);
-#pragma unroll
-                    for (int qb = 0; qb < QB; ++qb) s[qb][kb] = mma(kf, q[qb][ks], s[qb][kb]);
-                }
+                for (int ks = 0; ks < KS; ++ks) s[kb] = mma(L::by_rows(kl, kb * 32 + (lane & 31), ks, half), q[ks], s[kb]);
             }
-            if (kt >= whole) {
-#pragma unroll
-                for (int qb = 0; qb < QB; ++qb) {
-                    const int end = int(max(int64_t(0), min(seen[qb] - kt * KT, int64_t(KT))));
-#pragma unroll
-                    for (int kb = 0; kb < KB; ++kb)
-#pragma unroll
-                        for (int r = 0; r < 16; ++r) s[qb][kb][r] = kb * 32 + c_row(r, half) < end ? s[qb][kb][r] : -INFINITY;
-                }
-            }
-#pragma unroll
-            for (int qb = 0; qb < QB; ++qb) {
-                float top = s[qb][0][0];
-#pragma unroll
-                for (int kb = 0; kb < KB; ++kb)
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) top = fmaxf(top, s[qb][kb][r]);
-                top = half_max(top) * c;
-                const bool moves = top > m[qb] + kSlack || (m[qb] == -INFINITY && top > -INFINITY);
-                if (__any(moves)) {
-                    const float to = moves ? top : m[qb];
-                    const float f = moves ? exp2_fast(m[qb] - to) : 1.0f;
-                    m[qb] = to;
-                    l[qb] *= f;
-#pragma unroll
-                    for (int db = 0; db < DB; ++db)
-#pragma unroll
-                        for (int r = 0; r < 16; ++r) o[qb][db][r] *= f;
-                }
-                const float base = m[qb] == -INFINITY ? 0.0f : m[qb] - kWeightBias<T>;
-                float sum = 0.0f;
-#pragma unroll
-                for (int kb = 0; kb < KB; ++kb)
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) {
-                        const float e = exp2_fast(fmaf(s[qb][kb][r], c, -base));
-                        s[qb][kb][r] = e;
-                        sum += e;
-                    }
-                l[qb] += sum;
-            }
+            if (kt >= whole) hide(s, seen - kt * KT, half);
+            run.look(s, o, c);
+            run.template weigh<T>(s, c);
 #pragma unroll
             for (int st = 0; st < KT / 16; ++st) {
-                Frag<T> p[QB];
+                const Frag<T> p = operand<T>(s[st / 2], st % 2);
 #pragma unroll
-                for (int qb = 0; qb < QB; ++qb) p[qb] = operand<T>(s[qb][st / 2], st % 2);
-#pragma unroll
-                for (int db = 0; db < DB; ++db) {
-                    const Frag<T> vf = L::by_columns(vl, st * 16, db, lane);
-#pragma unroll
-                    for (int qb = 0; qb < QB; ++qb) o[qb][db] = mma(vf, p[qb], o[qb][db]);
-                }
+                for (int db = 0; db < DB; ++db) o[db] = mma(L::by_columns(vl, st * 16, db, lane), p, o[db]);
             }
         }
-        if (kt + 1 < kt1) {
-            km.store(lds[buf ^ 1][0], tid);
-            vm.store(lds[buf ^ 1][1], tid);
-        }
+        if (kt + 1 < kt1) store(buf ^ 1);
     }
-
-#pragma unroll
-    for (int qb = 0; qb < QB; ++qb) {
-        const int64_t row = row0 + qb * 32 + (lane & 31), t = row / a.G, g = row % a.G;
-        if (row >= a.R) continue;
-        const float sum = half_sum(l[qb]), to = m[qb] - kWeightBias<T>;
-        if (a.splits == 1) {
-            const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-            const int64_t h = hk * a.G + g;
-            store_columns<T, DB>(static_cast<T *>(a.out) + ((n * a.Tq + t) * a.H + h) * a.D, o[qb], inv, a.D, half);
-            if (half == 0) a.lse[(n * a.H + h) * a.Tq + t] = sum == 0.0f ? -INFINITY : (to + __log2f(sum)) * kLn2;
-        } else {
-            // (o, m, l) of this split: the join takes them
-            const int64_t place = (int64_t(split) * a.N * a.Hkv + nh) * a.R + row;
-            float *stat = a.part + 2 * place, *part = a.part + 2 * a.splits * a.N * a.Hkv * a.R + place * a.D;
-            if (half == 0) {
-                stat[0] = sum == 0.0f ? -INFINITY : to;
-                stat[1] = sum;
-            }
-            store_columns<float, DB>(part, o[qb], 1.0f, a.D, half);
-        }
-    }
+    const float l = half_sum(run.l);
+    if (there) finish<T, DB>(a, part, splits, split, nh, n, hk, row, half, run.m, l, o);
 }
 
-// The splits of a row, one wave a row: weights 2^(m - largest m).
-template <class T>
-__global__ __launch_bounds__(256) void attend_join_kernel(Attention a)
+// Up to 32 rows a key head (a token or a few over a cache): every wave takes 32 keys of its own at a
+// time, keys straight into registers, values through LDS of its own; the block's waves are joined
+// at the end.  Bound by memory and its latency: nothing waits for another wave on the way.
+template <class T, int DP, int WAVES>
+__global__ __launch_bounds__(WAVES * 64, DP * sizeof(T) <= 256 ? 2 : 1) void attend_few_kernel(Attention a, float *part, int splits)
 {
-    const int64_t rows = a.N * a.Hkv * a.R;
-    const int lane = threadIdx.x & 63;
-    const int64_t id = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6);
-    if (id >= rows) return;
-    const int64_t nh = id / a.R, row = id % a.R, n = nh / a.Hkv, h = nh % a.Hkv * a.G + row % a.G, t = row / a.G;
-    const float *stat = a.part, *part = a.part + 2 * a.splits * rows;
-    float top = -INFINITY;
-    for (int s = 0; s < a.splits; ++s) top = fmaxf(top, stat[2 * (s * rows + id)]);
-    float acc[kMaxHead / 64] = {}, sum = 0.0f;
-    for (int s = 0; s < a.splits; ++s) {
-        const float m = stat[2 * (s * rows + id)], l = stat[2 * (s * rows + id) + 1];
-        if (l == 0.0f) continue;  // nothing seen there
-        const float f = exp2_fast(m - top);
-        sum = fmaf(l, f, sum);
+    using L = Tile<T, DP>;
+    constexpr int KS = DP / 16, DB = DP / 32;
+    // the tiles of the waves, and then their outputs: 32 rows of DP float32
+    __shared__ __attribute__((aligned(16))) char lds[WAVES * 32 * DP * 4];
+    __shared__ float ms[WAVES][32], ls[WAVES][32];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), half = lane >> 5;
+    T *vl = reinterpret_cast<T *>(lds) + wave * 32 * DP;
+
+    int w = xcd_remap(blockIdx.x, gridDim.x);
+    const int split = w % splits, nh = w / splits, n = nh / a.Hkv, hk = nh % a.Hkv;
+    const int len = a.length(n), start = a.start(n);
+    const int row = lane & 31, t = a.by_g.div(row), g = row - t * a.G;
+    const bool there = row < a.R;
+    const int seen = there ? a.seen(len, start, t) : 0;
+
+    // tiles of 32 keys, dealt to the splits in runs and to a block's waves in turn
+    const int want = (a.seen(len, start, a.Tq - 1) + 31) / 32, each = (want + splits - 1) / splits;
+    const int kt0 = split * each + wave, kt1 = min(want, split * each + each);
+    const int whole = a.seen(len, start, 0) / 32;
+    const T *kp = static_cast<const T *>(a.k.p) + n * a.k.n + hk * a.k.h;
+    const T *vp = static_cast<const T *>(a.v.p) + n * a.v.n + hk * a.v.h;
+
+    Frag<T> kf[KS], q[KS];
+    Mover<T, DP, 32, 64> vm(lane);
+    auto load = [&](int kt) {
+        const int key = kt * 32 + (lane & 31);
+        const T *p = kp + key * a.k.t;
 #pragma unroll
-        for (int i = 0; i < kMaxHead / 64; ++i)
-            if (i * 64 + lane < a.D) acc[i] = fmaf(part[(s * rows + id) * a.D + i * 64 + lane], f, acc[i]);
+        for (int ks = 0; ks < KS; ++ks) kf[ks] = load_frag<T>(p, ks * 16 + half * 8, key < len ? a.D : 0);
+        vm.load(vp + int64_t(kt) * 32 * a.v.t, a.v.t, len - kt * 32, a.D);
+    };
+    if (kt0 < kt1) load(kt0);
+    const T *qp = static_cast<const T *>(a.q.p) + n * a.q.n + t * a.q.t + (hk * a.G + g) * a.q.h;
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) q[ks] = load_frag<T>(qp, ks * 16 + half * 8, there ? a.D : 0);
+
+    f32x16 o[DB];
+#pragma unroll
+    for (int db = 0; db < DB; ++db) o[db] = f32x16{};
+    Running run;
+    const float c = a.scale * kLog2e;
+    for (int kt = kt0; kt < kt1; kt += WAVES) {
+        f32x16 s[1] = {f32x16{}};
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) s[0] = mma(kf[ks], q[ks], s[0]);
+        vm.store(vl);
+        if (kt + WAVES < kt1) load(kt + WAVES);
+        if (kt >= whole) hide(s, seen - kt * 32, half);
+        run.look(s, o, c);
+        run.weigh<T>(s, c);
+        // the wave's own tile: its stores are seen by its later reads in order
+#pragma unroll
+        for (int st = 0; st < 2; ++st) {
+            const Frag<T> p = operand<T>(s[0], st);
+#pragma unroll
+            for (int db = 0; db < DB; ++db) o[db] = mma(L::by_columns(vl, st * 16, db, lane), p, o[db]);
+        }
+    }
+    float l = half_sum(run.l), m = run.m;
+    if constexpr (WAVES > 1) {
+        if (half == 0) {
+            ms[wave][row] = m;
+            ls[wave][row] = l;
+        }
+        __syncthreads();  // the tiles are done with
+        float *ol = reinterpret_cast<float *>(lds) + wave * 32 * DP;
+        if (wave > 0 && there)
+#pragma unroll
+            for (int db = 0; db < DB; ++db)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const f32x4 v = {o[db][4 * k], o[db][4 * k + 1], o[db][4 * k + 2], o[db][4 * k + 3]};
+                    // chunks turned by the row, so that rows do not meet in the banks
+                    *reinterpret_cast<f32x4 *>(ol + row * DP + (((db * 8 + 2 * k + half) ^ (row & 7)) * 4)) = v;
+                }
+        __syncthreads();
+        if (wave > 0) return;
+        float top = m;
+#pragma unroll
+        for (int i = 1; i < WAVES; ++i) top = fmaxf(top, ms[i][row]);
+        const float f0 = m == -INFINITY ? 0.0f : exp2_fast(m - top);
+        l *= f0;
+#pragma unroll
+        for (int db = 0; db < DB; ++db)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) o[db][r] *= f0;
+        if (there)
+#pragma unroll
+            for (int i = 1; i < WAVES; ++i) {
+                const float mi = ms[i][row], f = mi == -INFINITY ? 0.0f : exp2_fast(mi - top);
+                l = fmaf(ls[i][row], f, l);
+                const float *oi = reinterpret_cast<const float *>(lds) + i * 32 * DP;
+#pragma unroll
+                for (int db = 0; db < DB; ++db)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const f32x4 v = *reinterpret_cast<const f32x4 *>(oi + row * DP + (((db * 8 + 2 * k + half) ^ (row & 7)) * 4));
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) o[db][4 * k + j] = fmaf(v[j], f, o[db][4 * k + j]);
+                    }
+            }
+        m = top;
+    }
+    if (there) finish<T, DB>(a, part, splits, split, nh, n, hk, row, half, m, l, o);
+}
+
+// The splits of a row, one wave a row: weights 2^(m - largest m).  A lane reads the statistics of one
+// split; C elements a lane, the parts of 8 splits asked for at a time.
+template <class T, int C>
+__global__ __launch_bounds__(64) void attend_join_kernel(Attention a, float *part, int splits)
+{
+    const Parts ps(part, a, splits);
+    const int lane = threadIdx.x;
+    const int64_t id = blockIdx.x;
+    const int nh = int(id / a.R), row = int(id - int64_t(nh) * a.R), n = nh / a.Hkv, t = a.by_g.div(row);
+    const int h = (nh - n * a.Hkv) * a.G + row - t * a.G;
+    constexpr int AT_ONCE = 8;
+    float v[AT_ONCE][C];
+    auto load = [&](int s0) {
+#pragma unroll
+        for (int k = 0; k < AT_ONCE; ++k)
+#pragma unroll
+            for (int i = 0; i < C; ++i) {
+                const int d = i * 64 + lane;
+                v[k][i] = s0 + k < splits && d < a.D ? ps.out[((s0 + k) * ps.rows + id) * a.D + d] : 0.0f;
+            }
+    };
+    load(0);
+    // a plan has at most 64 splits: one a lane
+    const bool mine = lane < splits;
+    const float m = mine ? ps.stat[2 * (lane * ps.rows + id)] : -INFINITY, l = mine ? ps.stat[2 * (lane * ps.rows + id) + 1] : 0.0f;
+    float top = m;
+#pragma unroll
+    for (int s = 32; s; s >>= 1) top = fmaxf(top, __shfl_xor(top, s));
+    const float f = l == 0.0f ? 0.0f : exp2_fast(m - top);  // nothing seen there: nothing to add
+    float sum = l * f;
+#pragma unroll
+    for (int s = 32; s; s >>= 1) sum += __shfl_xor(sum, s);
+    float acc[C] = {};
+    for (int s0 = 0; s0 < splits; s0 += AT_ONCE) {
+        if (s0) load(s0);
+#pragma unroll
+        for (int k = 0; k < AT_ONCE; ++k) {
+            const float wt = __shfl(f, (s0 + k) & 63);
+#pragma unroll
+            for (int i = 0; i < C; ++i) acc[i] = fmaf(v[k][i], wt, acc[i]);
+        }
     }
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-    T *out = static_cast<T *>(a.out) + ((n * a.Tq + t) * a.H + h) * a.D;
+    T *out = static_cast<T *>(a.out) + ((int64_t(n) * a.Tq + t) * a.H + h) * a.D;
 #pragma unroll
-    for (int i = 0; i < kMaxHead / 64; ++i)
+    for (int i = 0; i < C; ++i)
         if (i * 64 + lane < a.D) out[i * 64 + lane] = T(acc[i] * inv);
-    if (lane == 0) a.lse[(n * a.H + h) * a.Tq + t] = sum == 0.0f ? -INFINITY : (top + __log2f(sum)) * kLn2;
+    if (lane == 0) a.lse[(int64_t(n) * a.H + h) * a.Tq + t] = sum == 0.0f ? -INFINITY : (top + __log2f(sum)) * kLn2;
 }
 
 template <class T>
-void launch_attend(Attention a, const AttendPlan &p, hipStream_t st)
+void launch_attend(const Attention &a, const AttendPlan &p, float *part, hipStream_t st)
 {
-    a.splits = p.splits;
-    const unsigned blocks = unsigned(a.N * a.Hkv * p.tiles * p.splits);
+    const int heads = a.N * a.Hkv;
     with_head(a.D, [&](auto head) {
-        constexpr int DP = decltype(head)::value, KT = DP * sizeof(T) > 512 ? 32 : 64;
-        if (p.waves == 1) attend_kernel<T, DP, 1, 1, KT><<<blocks, 64, 0, st>>>(a, p.tiles);
-        else attend_kernel<T, DP, 1, 4, KT><<<blocks, 256, 0, st>>>(a, p.tiles);
+        constexpr int DP = decltype(head)::value, KT = DP * sizeof(T) > 256 ? 32 : 64, C = (DP + 63) / 64;
+        if (p.few) attend_few_kernel<T, DP, 4><<<unsigned(heads * p.splits), 256, 0, st>>>(a, part, p.splits);
+        else attend_kernel<T, DP, 4, KT><<<unsigned(heads * p.tiles * p.splits), 256, 0, st>>>(a, part, p.tiles, p.splits);
+        if (p.splits > 1) attend_join_kernel<T, C><<<unsigned(heads * a.R), 64, 0, st>>>(a, part, p.splits);
     });
-    if (p.splits > 1) {
-        const int64_t rows = a.N * a.Hkv * a.R;
-        attend_join_kernel<T><<<unsigned((rows + 3) / 4), 256, 0, st>>>(a);
-    }
 }
 
 }  // namespace ct

@@ -31,73 +31,81 @@ struct RowStat {
 
 constexpr int kStatRows = 64;  // rows or keys a block of stat_kernel looks at
 
-// A wave a row: RowStat of the rows, and for float16 the largest norm of 64 rows' do, or of 64 keys'
-// values, for each image and key head.
-template <class T>
-__global__ __launch_bounds__(256) void stat_kernel(Attention a, RowStat *stat, float *top, int64_t row_blocks, int64_t blocks)
+// RowStat of the rows, and for float16 the largest norm of 64 rows' do, or of 64 keys' values, for each
+// image and key head.  LANES lanes a row, 16 bytes a lane.
+template <class T, int LANES>
+__global__ __launch_bounds__(256) void stat_kernel(Attention a, RowStat *stat, float *top, int row_blocks, int blocks)
 {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t nh = blockIdx.x / blocks, b = blockIdx.x % blocks, n = nh / a.Hkv, hk = nh % a.Hkv;
-    const int64_t len = a.length(n), start = a.start(n);
+    constexpr int V = kVec<T>;
+    const int in = threadIdx.x & (LANES - 1), first = threadIdx.x / LANES;
+    const int nh = blockIdx.x / blocks, b = blockIdx.x - nh * blocks, n = nh / a.Hkv, hk = nh - n * a.Hkv;
+    const int len = a.length(n), start = a.start(n), from = a.first_token(len, start);
     float most = 0.0f;
-    __shared__ float shared[4];
-    if (b < row_blocks) {
-        for (int i = wave; i < kStatRows; i += 4) {
-            const int64_t row = b * kStatRows + i;
-            if (row >= a.R) break;
-            const int64_t t = row / a.G, h = hk * a.G + row % a.G;
-            const bool sees = a.seen(len, start, t) > 0;
-            float sum = 0.0f, sq = 0.0f;
+    const bool rows = b < row_blocks;
+    const int base = (rows ? b : b - row_blocks) * kStatRows;
+#pragma unroll
+    for (int i = 0; i < kStatRows * LANES / 256; ++i) {
+        const int at = base + first + i * (256 / LANES);
+        float sum = 0.0f, sq = 0.0f;
+        if (rows) {
+            const int t = a.by_g.div(at), h = hk * a.G + at - t * a.G;
+            const bool sees = at < a.R && t >= from;
             if (sees) {
                 const T *po = static_cast<const T *>(a.o.p) + n * a.o.n + t * a.o.t + h * a.o.h;
                 const T *pd = static_cast<const T *>(a.d_o.p) + n * a.d_o.n + t * a.d_o.t + h * a.d_o.h;
-                for (int d = lane; d < a.D; d += 64) {
-                    const float g = float(pd[d]);
-                    sum = fmaf(g, float(po[d]), sum);
-                    sq = fmaf(g, g, sq);
+                for (int d = in * V; d < a.D; d += LANES * V) {
+                    const Raw<T, V> x = load_chunk<T>(pd + d, a.D - d, a.D % V), y = load_chunk<T>(po + d, a.D - d, a.D % V);
+#pragma unroll
+                    for (int j = 0; j < V; ++j) {
+                        sum = fmaf(float(x[j]), float(y[j]), sum);
+                        if (kHalf<T>) sq = fmaf(float(x[j]), float(x[j]), sq);
+                    }
                 }
             }
 #pragma unroll
-            for (int s = 32; s; s >>= 1) {
-                sum += __shfl_xor(sum, s);
-                sq += __shfl_xor(sq, s);
-            }
-            most = fmaxf(most, sq);
-            if (lane == 0)
-                stat[nh * a.R + row] = {sees ? a.lse[(n * a.H + h) * a.Tq + t] * kLog2e : INFINITY, sum};
-        }
-    } else {
-        for (int i = wave; i < kStatRows; i += 4) {
-            const int64_t j = (b - row_blocks) * kStatRows + i;
-            if (j >= len) break;
-            const T *p = static_cast<const T *>(a.v.p) + n * a.v.n + j * a.v.t + hk * a.v.h;
-            float sq = 0.0f;
-            for (int d = lane; d < a.D; d += 64) sq = fmaf(float(p[d]), float(p[d]), sq);
+            for (int s = LANES / 2; s; s >>= 1) sum += __shfl_xor(sum, s);
+            if (in == 0 && at < a.R)
+                stat[int64_t(nh) * a.R + at] = {sees ? a.lse[(int64_t(n) * a.H + h) * a.Tq + t] * kLog2e : INFINITY, sum};
+        } else if (at < len) {
+            const T *p = static_cast<const T *>(a.v.p) + n * a.v.n + at * a.v.t + hk * a.v.h;
+            for (int d = in * V; d < a.D; d += LANES * V) {
+                const Raw<T, V> x = load_chunk<T>(p + d, a.D - d, a.D % V);
 #pragma unroll
-            for (int s = 32; s; s >>= 1) sq += __shfl_xor(sq, s);
+                for (int j = 0; j < V; ++j) sq = fmaf(float(x[j]), float(x[j]), sq);
+            }
+        }
+        if (kHalf<T>) {
+#pragma unroll
+            for (int s = LANES / 2; s; s >>= 1) sq += __shfl_xor(sq, s);
             most = fmaxf(most, sq);
         }
     }
     if constexpr (kHalf<T>) {
-        if (lane == 0) shared[wave] = most;
+        __shared__ float shared[256 / LANES];
+        if (in == 0) shared[first] = most;
         __syncthreads();
-        if (threadIdx.x == 0)
-            top[blockIdx.x] = sqrtf(fmaxf(fmaxf(shared[0], shared[1]), fmaxf(shared[2], shared[3])));
+        if (threadIdx.x == 0) {
+#pragma unroll
+            for (int i = 1; i < 256 / LANES; ++i) most = fmaxf(most, shared[i]);
+            top[blockIdx.x] = sqrtf(most);
+        }
     }
 }
 
 // The power of two dS of an image and key head is held by; the same in both kernels.
 template <class T, int THREADS>
-__device__ __forceinline__ int grad_shift(const Attention &a, const float *top, int64_t nh, int64_t row_blocks, int64_t blocks)
+__device__ __forceinline__ int grad_shift(const Attention &a, const float *top, int nh, int row_blocks, int blocks)
 {
     if constexpr (!kHalf<T>) {
         return 0;
     } else {
         __shared__ float shared[2][THREADS / 64];
         float most[2] = {0.0f, 0.0f};
-        for (int64_t b = threadIdx.x; b < blocks; b += THREADS) {
-            const int of = b < row_blocks ? 0 : 1;
-            most[of] = fmaxf(most[of], top[nh * blocks + b]);
+        const float *p = top + int64_t(nh) * blocks;
+        for (int b = threadIdx.x; b < blocks; b += THREADS) {
+            const float v = p[b];
+            most[0] = fmaxf(most[0], b < row_blocks ? v : 0.0f);
+            most[1] = fmaxf(most[1], b < row_blocks ? 0.0f : v);
         }
 #pragma unroll
         for (int of = 0; of < 2; ++of) {
@@ -118,336 +126,323 @@ __device__ __forceinline__ int grad_shift(const Attention &a, const float *top, 
     }
 }
 
-// dk and dv of a block of keys, from the rows [rt0, rt1) of RT.
-template <class T, int DP, int KB, int WAVES, int RT>
-__global__ __launch_bounds__(WAVES * 64) void key_grad_kernel(Attention a, const RowStat *stat, const float *top,
-                                                              int64_t row_blocks, int64_t blocks, int64_t tiles)
+// dk and dv of a block of keys, a wave 32 of them, from RT rows at a time.  The keys' operands stay in
+// registers, the values' too or, for longer heads (LDSV), in LDS.
+template <class T, int DP, int WAVES, int RT, bool LDSV>
+__global__ __launch_bounds__(WAVES * 64, DP * sizeof(T) <= 256 ? 2 : 1) void key_grad_kernel(
+    Attention a, const RowStat *stat, const float *top, float *part, int row_blocks, int blocks, int tiles, int splits, int chunk)
 {
     using L = Tile<T, DP>;
-    constexpr int KS = DP / 16, DB = DP / 32, RB = RT / 32, THREADS = WAVES * 64;
-    __shared__ __attribute__((aligned(16))) T lds[2][RT * DP];
-    __shared__ __attribute__((aligned(16))) float lse2[RT], delta[RT];
-    __shared__ int ends[RT];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, half = lane >> 5;
+    constexpr int KS = DP / 16, DB = DP / 32, RB = RT / 32, THREADS = WAVES * 64, KEYS = WAVES * 32;
+    __shared__ __attribute__((aligned(16))) T lds[2][2][RT * DP];
+    __shared__ __attribute__((aligned(16))) T values[LDSV ? KEYS * DP : 1];
+    __shared__ __attribute__((aligned(16))) float lse2[2][RT], delta[2][RT];
+    __shared__ __attribute__((aligned(16))) int ends[2][RT];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), half = lane >> 5;
 
-    int64_t w = xcd_remap(blockIdx.x, gridDim.x);
-    const int split = int(w % a.splits);
-    w /= a.splits;
-    const int64_t tile = w % tiles, nh = w / tiles, n = nh / a.Hkv, hk = nh % a.Hkv;
-    const int64_t len = a.length(n), start = a.start(n);
-    const int64_t block_key = tile * (WAVES * KB * 32), key0 = block_key + wave * (KB * 32);
+    int w = xcd_remap(blockIdx.x, gridDim.x);
+    const int split = w % splits;
+    w /= splits;
+    const int tile = w % tiles, nh = w / tiles, n = nh / a.Hkv, hk = nh - n * a.Hkv;
+    const int len = a.length(n), start = a.start(n), from_token = a.first_token(len, start);
+    const int block_key = tile * KEYS, key0 = block_key + wave * 32, key = key0 + (lane & 31);
+    // rows from the first that sees the block's first key on, of this split's chunk
+    const int from = a.causal ? max(0, min(block_key - start, a.Tq)) * a.G : 0;
+    const int rt0 = max(from, split * chunk) / RT, rt1 = block_key < len ? (min(a.R, split * chunk + chunk) + RT - 1) / RT : 0;
+    if (splits > 1 && rt0 >= rt1) return;  // the join passes over it
 
-    Frag<T> k[KB][KS], v[KB][KS];
+    Frag<T> k[KS], v[LDSV ? 1 : KS];
+    const T *kp = static_cast<const T *>(a.k.p) + n * a.k.n + key * a.k.t + hk * a.k.h;
+    const T *vp = static_cast<const T *>(a.v.p) + n * a.v.n + key * a.v.t + hk * a.v.h;
 #pragma unroll
-    for (int kb = 0; kb < KB; ++kb) {
-        const int64_t key = key0 + kb * 32 + (lane & 31);
-        const T *kp = static_cast<const T *>(a.k.p) + n * a.k.n + key * a.k.t + hk * a.k.h;
-        const T *vp = static_cast<const T *>(a.v.p) + n * a.v.n + key * a.v.t + hk * a.v.h;
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-            k[kb][ks] = load_frag<T>(kp, ks * 16 + half * 8, key < len ? a.D : 0);
-            v[kb][ks] = load_frag<T>(vp, ks * 16 + half * 8, key < len ? a.D : 0);
-        }
+    for (int ks = 0; ks < KS; ++ks) {
+        k[ks] = load_frag<T>(kp, ks * 16 + half * 8, key < len ? a.D : 0);
+        const Frag<T> f = load_frag<T>(vp, ks * 16 + half * 8, key < len ? a.D : 0);
+        if constexpr (LDSV) L::put(values, wave * 32 + (lane & 31), ks, half, f);  // its own lane reads it
+        else v[ks] = f;
     }
-    f32x16 dk[KB][DB], dv[KB][DB];
+    f32x16 dk[DB], dv[DB];
 #pragma unroll
-    for (int kb = 0; kb < KB; ++kb)
-#pragma unroll
-        for (int db = 0; db < DB; ++db) dk[kb][db] = dv[kb][db] = f32x16{};
+    for (int db = 0; db < DB; ++db) dk[db] = dv[db] = f32x16{};
 
     const int shift = grad_shift<T, THREADS>(a, top, nh, row_blocks, blocks);
     const float bias = kHalf<T> ? float(kHalfBias) : 0.0f, c = a.scale * kLog2e;
     const float factor = a.scale * exp2f(float(shift) - bias);
 
-    // rows from the first that sees the block's first key on; this split's share of them
-    int64_t from = 0;
-    if (a.causal) from = max(int64_t(0), min(block_key - start, a.Tq)) * a.G;
-    const int64_t t0 = from / RT, t1 = block_key < len ? (a.R + RT - 1) / RT : 0, each = t1 > t0 ? (t1 - t0 + a.splits - 1) / a.splits : 0;
-    const int64_t rt0 = t0 + split * each, rt1 = min(t1, rt0 + each);
-
     const T *qp = static_cast<const T *>(a.q.p) + n * a.q.n + hk * a.G * a.q.h;
     const T *dp = static_cast<const T *>(a.d_o.p) + n * a.d_o.n + hk * a.G * a.d_o.h;
-    Mover<T, DP, RT, THREADS> qm, dm;
+    const RowStat *sp = stat + int64_t(nh) * a.R;
+    Mover<T, DP, RT, THREADS> qm(tid), dm(tid);
     RowStat mine{INFINITY, 0.0f};
     int end = 0;
-    auto load = [&](int64_t rt) {
-        // rows that see nothing are zeros: what stands there takes no part
-        auto place = [&](int r, const T *p, const Strided &s) -> const T * {
-            const int64_t row = rt * RT + r, t = row / a.G;
-            return row < a.R && a.seen(len, start, t) > 0 ? p + t * s.t + row % a.G * s.h : nullptr;
-        };
-        qm.load(tid, a.D, [&](int r) { return place(r, qp, a.q); });
-        dm.load(tid, a.D, [&](int r) { return place(r, dp, a.d_o); });
+    auto load = [&](int rt) {
+        if (a.G == 1 && rt * RT >= from_token) {
+            qm.load(qp + int64_t(rt) * RT * a.q.t, a.q.t, a.R - rt * RT, a.D);
+            dm.load(dp + int64_t(rt) * RT * a.d_o.t, a.d_o.t, a.R - rt * RT, a.D);
+        } else {
+            // rows that see nothing are zeros: what stands there takes no part
+            auto place = [&](int r, const T *p, const Strided &s) -> const T * {
+                const int row = rt * RT + r, t = a.by_g.div(row);
+                return row < a.R && t >= from_token ? p + t * s.t + (row - t * a.G) * s.h : nullptr;
+            };
+            qm.load(a.D, [&](int r) { return place(r, qp, a.q); });
+            dm.load(a.D, [&](int r) { return place(r, dp, a.d_o); });
+        }
         if (tid < RT) {
-            const int64_t row = rt * RT + tid;
-            mine = row < a.R ? stat[nh * a.R + row] : RowStat{INFINITY, 0.0f};
+            const int row = rt * RT + tid;
+            mine = row < a.R ? sp[row] : RowStat{INFINITY, 0.0f};
             // how many of the keys from the block's first on the row sees
-            end = row < a.R ? int(max(int64_t(0), min(a.seen(len, start, row / a.G) - block_key, int64_t(WAVES * KB * 32)))) : 0;
+            end = row < a.R ? a.seen(len, start, a.by_g.div(row)) - block_key : 0;
         }
     };
-    auto store = [&]() {
-        qm.store(lds[0], tid);
-        dm.store(lds[1], tid);
+    auto store = [&](int buf) {
+        qm.store(lds[buf][0]);
+        dm.store(lds[buf][1]);
         if (tid < RT) {
-            lse2[tid] = mine.lse2 - bias;
-            delta[tid] = mine.delta * factor;
-            ends[tid] = end;
+            lse2[buf][tid] = mine.lse2 - bias;
+            delta[buf][tid] = mine.delta * factor;
+            ends[buf][tid] = end;
         }
     };
 
-    if (rt0 < rt1) load(rt0);
-    for (int64_t rt = rt0; rt < rt1; ++rt) {
+    if (rt0 < rt1) {
+        load(rt0);
+        store(0);
+    }
+    for (int rt = rt0; rt < rt1; ++rt) {
         __syncthreads();
-        store();
-        __syncthreads();
+        const int buf = (rt - rt0) & 1;
         if (rt + 1 < rt1) load(rt + 1);
-        const T *ql = lds[0], *dl = lds[1];
-        // the tile's first row sees fewest keys, and its last row exists or there are rows to hide
-        const bool whole = key0 + KB * 32 <= a.seen(len, start, rt * RT / a.G);
+        const T *ql = lds[buf][0], *dl = lds[buf][1];
+        // the tile's first row sees fewest keys; rows that do not exist have P = 0
+        const bool whole = key0 + 32 <= a.seen(len, start, a.by_g.div(rt * RT));
 #pragma unroll
         for (int rb = 0; rb < RB; ++rb) {
-            f32x16 s[KB], g[KB];
+            f32x16 s = {}, g = {};
 #pragma unroll
-            for (int kb = 0; kb < KB; ++kb) s[kb] = g[kb] = f32x16{};
+            for (int ks = 0; ks < KS; ++ks) s = mma(L::by_rows(ql, rb * 32 + (lane & 31), ks, half), k[ks], s);
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) {
-                const Frag<T> qf = L::by_rows(ql, rb * 32 + (lane & 31), ks, half);
                 const Frag<T> df = L::by_rows(dl, rb * 32 + (lane & 31), ks, half);
-#pragma unroll
-                for (int kb = 0; kb < KB; ++kb) {
-                    s[kb] = mma(qf, k[kb][ks], s[kb]);
-                    g[kb] = mma(df, v[kb][ks], g[kb]);
-                }
+                if constexpr (LDSV) g = mma(df, L::by_rows(values, wave * 32 + (lane & 31), ks, half), g);
+                else g = mma(df, v[ks], g);
             }
 #pragma unroll
             for (int r4 = 0; r4 < 4; ++r4) {
                 const int at = rb * 32 + 8 * r4 + 4 * half;
-                const f32x4 le = *reinterpret_cast<const f32x4 *>(lse2 + at), de = *reinterpret_cast<const f32x4 *>(delta + at);
+                const f32x4 le = *reinterpret_cast<const f32x4 *>(lse2[buf] + at), de = *reinterpret_cast<const f32x4 *>(delta[buf] + at);
 #pragma unroll
-                for (int kb = 0; kb < KB; ++kb)
+                for (int j = 0; j < 4; ++j) {
+                    const int r = 4 * r4 + j;
+                    const float p = exp2_fast(fmaf(s[r], c, -le[j]));
+                    s[r] = p;
+                    g[r] = p * fmaf(g[r], factor, -de[j]);
+                }
+            }
+            if (!whole) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int r = 4 * r4 + j;
-                        const float p = exp2_fast(fmaf(s[kb][r], c, -le[j]));
-                        s[kb][r] = p;
-                        g[kb][r] = p * fmaf(g[kb][r], factor, -de[j]);
-                    }
-                if (!whole) {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int e = ends[at + j] - wave * (KB * 32) - (lane & 31);
-#pragma unroll
-                        for (int kb = 0; kb < KB; ++kb) {
-                            s[kb][4 * r4 + j] = kb * 32 < e ? s[kb][4 * r4 + j] : 0.0f;
-                            g[kb][4 * r4 + j] = kb * 32 < e ? g[kb][4 * r4 + j] : 0.0f;
-                        }
-                    }
+                for (int r = 0; r < 16; ++r) {
+                    const bool sees = key - block_key < ends[buf][rb * 32 + c_row(r, half)];
+                    s[r] = sees ? s[r] : 0.0f;
+                    g[r] = sees ? g[r] : 0.0f;
                 }
             }
 #pragma unroll
             for (int st = 0; st < 2; ++st) {
-                Frag<T> pf[KB], gf[KB];
-#pragma unroll
-                for (int kb = 0; kb < KB; ++kb) {
-                    pf[kb] = operand<T>(s[kb], st);
-                    gf[kb] = operand<T>(g[kb], st);
-                }
+                const Frag<T> pf = operand<T>(s, st), gf = operand<T>(g, st);
 #pragma unroll
                 for (int db = 0; db < DB; ++db) {
-                    const Frag<T> df = L::by_columns(dl, rb * 32 + st * 16, db, lane);
-#pragma unroll
-                    for (int kb = 0; kb < KB; ++kb) dv[kb][db] = mma(df, pf[kb], dv[kb][db]);
-                    const Frag<T> qf = L::by_columns(ql, rb * 32 + st * 16, db, lane);
-#pragma unroll
-                    for (int kb = 0; kb < KB; ++kb) dk[kb][db] = mma(qf, gf[kb], dk[kb][db]);
+                    dv[db] = mma(L::by_columns(dl, rb * 32 + st * 16, db, lane), pf, dv[db]);
+                    dk[db] = mma(L::by_columns(ql, rb * 32 + st * 16, db, lane), gf, dk[db]);
                 }
             }
         }
+        if (rt + 1 < rt1) store(buf ^ 1);
     }
+    if (key >= a.Tk) return;
     const float undo_k = exp2f(-float(shift)), undo_v = exp2f(-bias);
-#pragma unroll
-    for (int kb = 0; kb < KB; ++kb) {
-        const int64_t key = key0 + kb * 32 + (lane & 31);
-        if (key >= a.Tk) continue;
-        if (a.splits == 1) {
-            const int64_t at = ((n * a.Tk + key) * a.Hkv + hk) * a.D;
-            store_columns<T, DB>(static_cast<T *>(a.dk) + at, dk[kb], undo_k, a.D, half);
-            store_columns<T, DB>(static_cast<T *>(a.dv) + at, dv[kb], undo_v, a.D, half);
-        } else {
-            const int64_t all = a.N * a.Tk * a.Hkv * a.D, at = ((n * a.Tk + key) * a.Hkv + hk) * a.D;
-            float *part = a.part + int64_t(split) * 2 * all + at;
-            store_columns<float, DB>(part, dk[kb], undo_k, a.D, half);
-            store_columns<float, DB>(part + all, dv[kb], undo_v, a.D, half);
-        }
+    const int64_t at = ((int64_t(n) * a.Tk + key) * a.Hkv + hk) * a.D;
+    if (splits == 1) {
+        store_columns<T, DB>(static_cast<T *>(a.dk) + at, dk, undo_k, a.D, half);
+        store_columns<T, DB>(static_cast<T *>(a.dv) + at, dv, undo_v, a.D, half);
+    } else {
+        const int64_t all = int64_t(a.N) * a.Tk * a.Hkv * a.D;
+        float *to = part + int64_t(split) * 2 * all + at;
+        store_columns<float, DB>(to, dk, undo_k, a.D, half);
+        store_columns<float, DB>(to + all, dv, undo_v, a.D, half);
     }
 }
 
-// dq of a block of rows, from the keys of this split.
-template <class T, int DP, int QB, int WAVES, int KT>
-__global__ __launch_bounds__(WAVES * 64) void row_grad_kernel(Attention a, const RowStat *stat, const float *top,
-                                                              int64_t row_blocks, int64_t blocks, int64_t tiles)
+// dq of a block of rows, a wave 32 of them, from KT keys at a time.
+template <class T, int DP, int WAVES, int KT>
+__global__ __launch_bounds__(WAVES * 64, DP * sizeof(T) <= 256 ? 2 : 1) void row_grad_kernel(
+    Attention a, const RowStat *stat, const float *top, float *part, int row_blocks, int blocks, int tiles, int splits, int chunk)
 {
     using L = Tile<T, DP>;
-    constexpr int KS = DP / 16, DB = DP / 32, KB = KT / 32, THREADS = WAVES * 64;
-    __shared__ __attribute__((aligned(16))) T lds[2][KT * DP];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, half = lane >> 5;
+    constexpr int KS = DP / 16, DB = DP / 32, KB = KT / 32, THREADS = WAVES * 64, ROWS = WAVES * 32;
+    __shared__ __attribute__((aligned(16))) T lds[2][2][KT * DP];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), half = lane >> 5;
 
-    int64_t w = xcd_remap(blockIdx.x, gridDim.x);
-    const int split = int(w % a.splits);
-    w /= a.splits;
-    const int64_t tile = tiles - 1 - w % tiles, nh = w / tiles, n = nh / a.Hkv, hk = nh % a.Hkv;
-    const int64_t len = a.length(n), start = a.start(n);
-    const int64_t row0 = tile * (WAVES * QB * 32) + wave * (QB * 32);
+    int w = xcd_remap(blockIdx.x, gridDim.x);
+    const int split = w % splits;
+    w /= splits;
+    const int tile = tiles - 1 - w % tiles, nh = w / tiles, n = nh / a.Hkv, hk = nh - n * a.Hkv;
+    const int len = a.length(n), start = a.start(n), from_token = a.first_token(len, start);
+    const int block_row = tile * ROWS, row0 = block_row + wave * 32;
+    // keys the block looks at, of this split's chunk
+    const int want = min(a.seen(len, start, a.by_g.div(min(block_row + ROWS, a.R) - 1)), split * chunk + chunk);
+    const int kt0 = split * chunk / KT, kt1 = (want + KT - 1) / KT;
+    if (splits > 1 && kt0 >= kt1) return;  // the join passes over it
 
     const int shift = grad_shift<T, THREADS>(a, top, nh, row_blocks, blocks);
     const float bias = kHalf<T> ? float(kHalfBias) : 0.0f, c = a.scale * kLog2e;
     const float factor = a.scale * exp2f(float(shift) - bias);
 
-    Frag<T> q[QB][KS], d_o[QB][KS];
-    int64_t seen[QB];
-    float lse2[QB], delta[QB];
+    const int row = row0 + (lane & 31), t = a.by_g.div(row), h = hk * a.G + row - t * a.G;
+    const bool sees = row < a.R && t >= from_token;
+    const int seen = sees ? a.seen(len, start, t) : 0;
+    const RowStat mine = row < a.R ? stat[int64_t(nh) * a.R + row] : RowStat{INFINITY, 0.0f};
+    const float lse2 = mine.lse2 - bias, delta = mine.delta * factor;
+    Frag<T> q[KS], d_o[KS];
+    const T *qp = static_cast<const T *>(a.q.p) + n * a.q.n + t * a.q.t + h * a.q.h;
+    const T *dp = static_cast<const T *>(a.d_o.p) + n * a.d_o.n + t * a.d_o.t + h * a.d_o.h;
 #pragma unroll
-    for (int qb = 0; qb < QB; ++qb) {
-        const int64_t row = row0 + qb * 32 + (lane & 31), t = row / a.G, h = hk * a.G + row % a.G;
-        seen[qb] = row < a.R ? a.seen(len, start, t) : 0;
-        const RowStat st = row < a.R ? stat[nh * a.R + row] : RowStat{INFINITY, 0.0f};
-        lse2[qb] = st.lse2 - bias;
-        delta[qb] = st.delta * factor;
-        const T *qp = static_cast<const T *>(a.q.p) + n * a.q.n + t * a.q.t + h * a.q.h;
-        const T *dp = static_cast<const T *>(a.d_o.p) + n * a.d_o.n + t * a.d_o.t + h * a.d_o.h;
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-            q[qb][ks] = load_frag<T>(qp, ks * 16 + half * 8, seen[qb] > 0 ? a.D : 0);
-            d_o[qb][ks] = load_frag<T>(dp, ks * 16 + half * 8, seen[qb] > 0 ? a.D : 0);
-        }
+    for (int ks = 0; ks < KS; ++ks) {
+        q[ks] = load_frag<T>(qp, ks * 16 + half * 8, sees ? a.D : 0);
+        d_o[ks] = load_frag<T>(dp, ks * 16 + half * 8, sees ? a.D : 0);
     }
-    const int64_t last = min(tile * (WAVES * QB * 32) + WAVES * QB * 32, a.R) - 1;
-    const int64_t want = (a.seen(len, start, last / a.G) + KT - 1) / KT, each = (want + a.splits - 1) / a.splits;
-    const int64_t kt0 = split * each, kt1 = min(want, kt0 + each);
-    const int64_t first_seen = row0 < a.R ? a.seen(len, start, row0 / a.G) : 0;
-    const int64_t last_seen = row0 < a.R ? a.seen(len, start, (min(row0 + QB * 32, a.R) - 1) / a.G) : 0;
-    const int64_t whole = first_seen / KT, none = (last_seen + KT - 1) / KT;
+    const bool rows = row0 < a.R;
+    const int whole = rows ? a.seen(len, start, a.by_g.div(row0)) / KT : 0;
+    const int none = rows ? (a.seen(len, start, a.by_g.div(min(row0 + 32, a.R) - 1)) + KT - 1) / KT : 0;
 
     const T *kp = static_cast<const T *>(a.k.p) + n * a.k.n + hk * a.k.h;
     const T *vp = static_cast<const T *>(a.v.p) + n * a.v.n + hk * a.v.h;
-    Mover<T, DP, KT, THREADS> km, vm;
-    auto load = [&](int64_t kt) {
-        km.load(tid, a.D, [&](int r) { return kt * KT + r < len ? kp + (kt * KT + r) * a.k.t : nullptr; });
-        vm.load(tid, a.D, [&](int r) { return kt * KT + r < len ? vp + (kt * KT + r) * a.v.t : nullptr; });
+    Mover<T, DP, KT, THREADS> km(tid), vm(tid);
+    auto load = [&](int kt) {
+        km.load(kp + int64_t(kt) * KT * a.k.t, a.k.t, len - kt * KT, a.D);
+        vm.load(vp + int64_t(kt) * KT * a.v.t, a.v.t, len - kt * KT, a.D);
     };
-    f32x16 dq[QB][DB];
+    f32x16 dq[DB];
 #pragma unroll
-    for (int qb = 0; qb < QB; ++qb)
-#pragma unroll
-        for (int db = 0; db < DB; ++db) dq[qb][db] = f32x16{};
+    for (int db = 0; db < DB; ++db) dq[db] = f32x16{};
 
-    if (kt0 < kt1) load(kt0);
-    for (int64_t kt = kt0; kt < kt1; ++kt) {
+    if (kt0 < kt1) {
+        load(kt0);
+        km.store(lds[0][0]);
+        vm.store(lds[0][1]);
+    }
+    for (int kt = kt0; kt < kt1; ++kt) {
         __syncthreads();
-        km.store(lds[0], tid);
-        vm.store(lds[1], tid);
-        __syncthreads();
+        const int buf = (kt - kt0) & 1;
         if (kt + 1 < kt1) load(kt + 1);
-        if (kt >= none) continue;
-        const T *kl = lds[0], *vl = lds[1];
+        if (kt < none) {
+            const T *kl = lds[buf][0], *vl = lds[buf][1];
 #pragma unroll
-        for (int kb = 0; kb < KB; ++kb) {
-            f32x16 s[QB], g[QB];
+            for (int kb = 0; kb < KB; ++kb) {
+                f32x16 s = {}, g = {};
 #pragma unroll
-            for (int qb = 0; qb < QB; ++qb) s[qb] = g[qb] = f32x16{};
+                for (int ks = 0; ks < KS; ++ks) s = mma(L::by_rows(kl, kb * 32 + (lane & 31), ks, half), q[ks], s);
 #pragma unroll
-            for (int ks = 0; ks < KS; ++ks) {
-                const Frag<T> kf = L::by_rows(kl, kb * 32 + (lane & 31), ks, half);
-                const Frag<T> vf = L::by_rows(vl, kb * 32 + (lane & 31), ks, half);
-#pragma unroll
-                for (int qb = 0; qb < QB; ++qb) {
-                    s[qb] = mma(kf, q[qb][ks], s[qb]);
-                    g[qb] = mma(vf, d_o[qb][ks], g[qb]);
-                }
-            }
-#pragma unroll
-            for (int qb = 0; qb < QB; ++qb) {
+                for (int ks = 0; ks < KS; ++ks) g = mma(L::by_rows(vl, kb * 32 + (lane & 31), ks, half), d_o[ks], g);
 #pragma unroll
                 for (int r = 0; r < 16; ++r) {
-                    const float p = exp2_fast(fmaf(s[qb][r], c, -lse2[qb]));
-                    g[qb][r] = p * fmaf(g[qb][r], factor, -delta[qb]);
+                    const float p = exp2_fast(fmaf(s[r], c, -lse2));
+                    g[r] = p * fmaf(g[r], factor, -delta);
                 }
                 if (kt >= whole) {
-                    const int end = int(max(int64_t(0), min(seen[qb] - kt * KT, int64_t(KT))));
+                    const int end = seen - kt * KT;
 #pragma unroll
-                    for (int r = 0; r < 16; ++r) g[qb][r] = kb * 32 + c_row(r, half) < end ? g[qb][r] : 0.0f;
+                    for (int r = 0; r < 16; ++r) g[r] = kb * 32 + c_row(r, half) < end ? g[r] : 0.0f;
                 }
-            }
 #pragma unroll
-            for (int st = 0; st < 2; ++st) {
-                Frag<T> gf[QB];
+                for (int st = 0; st < 2; ++st) {
+                    const Frag<T> gf = operand<T>(g, st);
 #pragma unroll
-                for (int qb = 0; qb < QB; ++qb) gf[qb] = operand<T>(g[qb], st);
-#pragma unroll
-                for (int db = 0; db < DB; ++db) {
-                    const Frag<T> kf = L::by_columns(kl, kb * 32 + st * 16, db, lane);
-#pragma unroll
-                    for (int qb = 0; qb < QB; ++qb) dq[qb][db] = mma(kf, gf[qb], dq[qb][db]);
+                    for (int db = 0; db < DB; ++db) dq[db] = mma(L::by_columns(kl, kb * 32 + st * 16, db, lane), gf, dq[db]);
                 }
             }
         }
+        if (kt + 1 < kt1) {
+            km.store(lds[buf ^ 1][0]);
+            vm.store(lds[buf ^ 1][1]);
+        }
     }
+    if (row >= a.R) return;
     const float undo = exp2f(-float(shift));
-#pragma unroll
-    for (int qb = 0; qb < QB; ++qb) {
-        const int64_t row = row0 + qb * 32 + (lane & 31), t = row / a.G, h = hk * a.G + row % a.G;
-        if (row >= a.R) continue;
-        const int64_t at = ((n * a.Tq + t) * a.H + h) * a.D;
-        if (a.splits == 1) store_columns<T, DB>(static_cast<T *>(a.dq) + at, dq[qb], undo, a.D, half);
-        else store_columns<float, DB>(a.part + int64_t(split) * a.N * a.Tq * a.H * a.D + at, dq[qb], undo, a.D, half);
-    }
+    const int64_t at = ((int64_t(n) * a.Tq + t) * a.H + h) * a.D;
+    if (splits == 1) store_columns<T, DB>(static_cast<T *>(a.dq) + at, dq, undo, a.D, half);
+    else store_columns<float, DB>(part + int64_t(split) * a.N * a.Tq * a.H * a.D + at, dq, undo, a.D, half);
 }
 
-// Sums of `splits` partial results of `count` values each, in their order; the first `first` of
-// them go to y0, the others to y1.
+// Sums of partial results, in their order, a block a token: first the tokens of the keys (dk and dv), then
+// those of the queries.  Chunks that a block of `span` keys or rows had nothing of are passed over.
 template <class T>
-__global__ __launch_bounds__(256) void grad_join_kernel(const float *part, int splits, int64_t count, int64_t first, T *y0, T *y1)
+__global__ __launch_bounds__(256) void grad_join_kernel(Attention a, AttendGradPlan p, const float *key_part, const float *row_part,
+                                                        int span, int key_tokens, Div31 by_d)
 {
-    for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < count; i += int64_t(gridDim.x) * 256) {
-        float sum = 0.0f;
-        for (int s = 0; s < splits; ++s) sum += part[s * count + i];
-        (i < first ? y0[i] : y1[i - first]) = T(sum);
+    int token = blockIdx.x;
+    if (token < key_tokens) {
+        const int n = token / a.Tk, block_key = (token - n * a.Tk) / span * span;
+        const int len = a.length(n), start = a.start(n);
+        const int from = a.causal ? max(0, min(block_key - start, a.Tq)) * a.G : 0;
+        const int s0 = from / p.row_chunk, s1 = block_key < len ? p.row_splits : 0;
+        const int count = a.Hkv * a.D;
+        const int64_t all = int64_t(a.N) * a.Tk * count, base = int64_t(token) * count;
+        for (int i = threadIdx.x; i < 2 * count; i += 256) {
+            const int64_t at = i < count ? base + i : all + base + i - count;
+            float sum = 0.0f;
+#pragma unroll 4
+            for (int s = s0; s < s1; ++s) sum += key_part[s * 2 * all + at];
+            (i < count ? static_cast<T *>(a.dk)[at] : static_cast<T *>(a.dv)[at - all]) = T(sum);
+        }
+    } else {
+        token -= key_tokens;
+        const int n = token / a.Tq, t = token - n * a.Tq, len = a.length(n), start = a.start(n);
+        const int count = a.H * a.D;
+        const int64_t all = int64_t(a.N) * a.Tq * count, base = int64_t(token) * count;
+        for (int i = threadIdx.x; i < count; i += 256) {
+            const int h = by_d.div(i), row = t * a.G + h - a.by_g.div(h) * a.G;
+            const int want = a.seen(len, start, a.by_g.div(min(row / span * span + span, a.R) - 1));
+            const int s1 = min(p.key_splits, (want + p.key_chunk - 1) / p.key_chunk);
+            float sum = 0.0f;
+#pragma unroll 4
+            for (int s = 0; s < s1; ++s) sum += row_part[s * all + base + i];
+            static_cast<T *>(a.dq)[base + i] = T(sum);
+        }
     }
 }
 
 template <class T>
-void launch_attend_grad(Attention a, const AttendGradPlan &p, char *ws, hipStream_t st)
+void launch_attend_grad(const Attention &a, const AttendGradPlan &p, char *ws, hipStream_t st)
 {
     RowStat *stat = reinterpret_cast<RowStat *>(ws + p.stat);
     float *top = reinterpret_cast<float *>(ws + p.top);
-    const int64_t row_blocks = (a.R + kStatRows - 1) / kStatRows;
-    const int64_t blocks = row_blocks + (kHalf<T> ? (a.Tk + kStatRows - 1) / kStatRows : 0);
-    const int64_t heads = a.N * a.Hkv;
-    if (a.R > 0 && heads * blocks > 0) stat_kernel<T><<<unsigned(heads * blocks), 256, 0, st>>>(a, stat, top, row_blocks, blocks);
-    a.part = reinterpret_cast<float *>(ws + p.part);
-    auto join = [&](int splits, int64_t count, int64_t first, void *y0, void *y1) {
-        const int64_t want = (count + 255) / 256;
-        grad_join_kernel<T><<<unsigned(want < 4096 ? want : 4096), 256, 0, st>>>(a.part, splits, count, first, static_cast<T *>(y0),
-                                                                                 static_cast<T *>(y1));
-    };
+    float *key_part = reinterpret_cast<float *>(ws + p.key_part), *row_part = reinterpret_cast<float *>(ws + p.row_part);
+    const int heads = a.N * a.Hkv, row_blocks = (a.R + kStatRows - 1) / kStatRows;
+    const int blocks = row_blocks + (kHalf<T> ? (a.Tk + kStatRows - 1) / kStatRows : 0);
+    if (heads * int64_t(blocks) > 0) {
+        if (a.D * int(sizeof(T)) <= 128) stat_kernel<T, 8><<<unsigned(heads * blocks), 256, 0, st>>>(a, stat, top, row_blocks, blocks);
+        else stat_kernel<T, 16><<<unsigned(heads * blocks), 256, 0, st>>>(a, stat, top, row_blocks, blocks);
+    }
     with_head(a.D, [&](auto head) {
-        constexpr int DP = decltype(head)::value;
-        constexpr int TILE = DP * sizeof(T) > 512 ? 32 : 64;
-        constexpr int BLOCK = 128;
-        const int64_t key_tiles = (a.Tk + BLOCK - 1) / BLOCK, row_tiles = (a.R + BLOCK - 1) / BLOCK;
-        if (key_tiles > 0) {
-            a.splits = p.row_splits;
-            key_grad_kernel<T, DP, 1, 4, TILE><<<unsigned(heads * key_tiles * a.splits), 256, 0, st>>>(a, stat, top, row_blocks, blocks, key_tiles);
-            const int64_t count = a.N * a.Tk * a.Hkv * a.D;
-            if (a.splits > 1) join(a.splits, 2 * count, count, a.dk, a.dv);
-        }
-        if (row_tiles > 0) {
-            a.splits = p.key_splits;
-            row_grad_kernel<T, DP, 1, 4, TILE><<<unsigned(heads * row_tiles * a.splits), 256, 0, st>>>(a, stat, top, row_blocks, blocks, row_tiles);
-            const int64_t count = a.N * a.R * a.Hkv * a.D;
-            if (a.splits > 1) join(a.splits, count, count, a.dq, a.dq);
-        }
+        constexpr int DP = decltype(head)::value, BYTES = DP * int(sizeof(T));
+        constexpr bool LDSV = BYTES > 128 && BYTES <= 512;
+        auto go = [&](auto waves) {
+            constexpr int W = decltype(waves)::value, SPAN = W * 32, TILE = W == 1 || BYTES > 128 ? 32 : 64;
+            const int key_tiles = (a.Tk + SPAN - 1) / SPAN, row_tiles = (a.R + SPAN - 1) / SPAN;
+            if (key_tiles > 0)
+                key_grad_kernel<T, DP, W, TILE, LDSV><<<unsigned(heads * key_tiles * p.row_splits), W * 64, 0, st>>>(
+                    a, stat, top, key_part, row_blocks, blocks, key_tiles, p.row_splits, p.row_chunk);
+            if (row_tiles > 0)
+                row_grad_kernel<T, DP, W, TILE><<<unsigned(heads * row_tiles * p.key_splits), W * 64, 0, st>>>(
+                    a, stat, top, row_part, row_blocks, blocks, row_tiles, p.key_splits, p.key_chunk);
+        };
+        if (p.waves == 1) go(std::integral_constant<int, 1>{});
+        else go(std::integral_constant<int, 4>{});
     });
+    const int key_tokens = p.row_splits > 1 ? a.N * a.Tk : 0, row_tokens = p.key_splits > 1 ? a.N * a.Tq : 0;
+    if (key_tokens + row_tokens > 0)
+        grad_join_kernel<T><<<unsigned(key_tokens + row_tokens), 256, 0, st>>>(a, p, key_part, row_part, 32 * p.waves, key_tokens, Div31(a.D));
 }
 
 }  // namespace ct
