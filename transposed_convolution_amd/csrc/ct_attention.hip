@@ -11,10 +11,7 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 size_t align16(size_t n) { return (n + 15) & ~size_t(15); }
 }  // namespace
 
-// Blocks wanted before a call's work is split over its keys (and joined by a second kernel), and the
-// keys a split should have.
-constexpr int64_t kWantBlocks = 512, kWantFewBlocks = 512, kLeastKeys = 256, kLeastFewKeys = 128;
-constexpr int kMostSplits = 64;
+constexpr int kMostSplits = 64;  // attend_join_kernel has a lane for each
 
 AttendPlan attend_plan(const Attention &a, int dtype)
 {
@@ -22,9 +19,16 @@ AttendPlan attend_plan(const Attention &a, int dtype)
     const int64_t heads = int64_t(a.N) * a.Hkv;
     p.few = a.R <= 32;
     p.tiles = p.few ? 1 : int(ceil_div(a.R, 128));
-    const int64_t base = heads * p.tiles, wanted = p.few ? kWantFewBlocks : kWantBlocks, least = p.few ? kLeastFewKeys : kLeastKeys;
-    if (base > 0 && base < wanted)
-        p.splits = int(std::max<int64_t>(1, std::min({ceil_div(wanted, base), ceil_div(a.Tk, least), int64_t(kMostSplits)})));
+    // Blocks wanted before a call's work is split over its keys (and joined by a second kernel), and
+    // the keys a split should have: float32 products take 16 times as long.
+    const int64_t base = heads * p.tiles, wanted = p.few && padded_head(a.D) * float_size(dtype) > 256 ? 256 : 512,
+                  least = p.few ? 128 : dtype == CT_FLOAT32 ? 64 : 256;
+    int64_t splits = 1;
+    if (base > 0 && base < wanted && !(p.few && a.Tk <= 512)) splits = std::max<int64_t>(1, std::min({ceil_div(wanted, base), ceil_div(a.Tk, least), int64_t(kMostSplits)}));
+    // chunks are whole steps of a block
+    const int64_t step = p.few ? 128 : 64;
+    p.chunk = int(splits > 1 ? ceil_div(ceil_div(a.Tk, splits), step) * step : std::max(1, a.Tk));
+    p.splits = int(std::max<int64_t>(1, ceil_div(a.Tk, p.chunk)));
     if (p.splits > 1) p.bytes = size_t(p.splits) * size_t(heads * a.R) * size_t(a.D + 2) * 4;
     return p;
 }
@@ -35,17 +39,20 @@ AttendGradPlan attend_grad_plan(const Attention &a, int dtype)
     const int64_t heads = int64_t(a.N) * a.Hkv;
     // Blocks of 4 waves share what they read, blocks of one wave make more of a small call: those
     // are taken where 4-wave blocks, split as far as is sensible, would not fill the chip.
-    auto chunk = [&](int waves, int64_t blocks, int64_t length) {
-        const int64_t wanted = waves == 1 ? 2048 : 512, least = waves == 1 ? 64 : 512, step = 64;
+    const size_t bytes = padded_head(a.D) * float_size(dtype);
+    const int64_t most = std::max(a.Tk, a.R);
+    const bool fills = heads * ceil_div(most, 128) * std::max<int64_t>(1, std::min<int64_t>(a.Tk, a.R) / 512) >= 256;
+    p.waves = fills || bytes > kOneWaveBytes ? 4 : 1;
+    p.key_span = p.waves == 1 ? 32 : padded_head(a.D) == 256 && dtype != CT_FLOAT32 ? 64 : 128;
+    p.row_span = p.waves == 1 ? 32 : 128;
+    auto chunk = [&](int64_t blocks, int64_t length) {
+        const int64_t wanted = p.waves == 1 ? 2048 : a.causal ? 1536 : 512, least = fills ? 512 : 64, step = 64;
         if (blocks == 0 || length == 0 || blocks >= wanted) return std::max<int64_t>(1, length);
-        const int64_t splits = std::max<int64_t>(1, std::min({wanted * 2 / blocks, ceil_div(length, least), int64_t(kMostSplits)}));
+        const int64_t splits = std::max<int64_t>(1, std::min({ceil_div(wanted, blocks), ceil_div(length, least), int64_t(kMostSplits)}));
         return ceil_div(ceil_div(length, splits), step) * step;
     };
-    const int64_t most = std::max(a.Tk, a.R);
-    p.waves = heads * ceil_div(most, 128) * std::max<int64_t>(1, std::min<int64_t>(a.Tk, a.R) / 512) >= 256 ? 4 : 1;
-    const int64_t span = 32 * p.waves;
-    p.row_chunk = int(chunk(p.waves, heads * ceil_div(a.Tk, span), a.R));
-    p.key_chunk = int(chunk(p.waves, heads * ceil_div(a.R, span), a.Tk));
+    p.row_chunk = int(chunk(heads * ceil_div(a.Tk, p.key_span), a.R));
+    p.key_chunk = int(chunk(heads * ceil_div(a.R, p.row_span), a.Tk));
     p.row_splits = int(std::max<int64_t>(1, ceil_div(a.R, p.row_chunk)));
     p.key_splits = int(std::max<int64_t>(1, ceil_div(a.Tk, p.key_chunk)));
     size_t at = 0;
@@ -256,6 +263,7 @@ extern "C" ct_status attention_workspace_size(ct_dtype dtype, const int64_t *q_s
     const ct_status st = sizes(dt, q_shape, kv_tokens, kv_heads, &a, &err);
     if (st != CT_OK) return fail(st, err);
     const bool rows = a.N > 0 && a.Tq > 0, keys = a.N > 0 && a.Tk > 0;
+    a.causal = 1;  // whose plans have at least as many parts
     *bytes_out = backward ? (rows || keys ? ct::attend_grad_plan(a, dt).bytes : 0) : (rows ? ct::attend_plan(a, dt).bytes : 0);
     return CT_OK;
 }

@@ -353,7 +353,7 @@ inline void with_head(int64_t D, F &&f)
 // rows) go to different blocks and are joined by a second kernel.
 struct AttendPlan {
     bool few = false;
-    int tiles = 0, splits = 1;
+    int tiles = 0, splits = 1, chunk = 1;  // chunk: keys a split
     size_t bytes = 0;    // workspace: the parts of splits
 };
 AttendPlan attend_plan(const Attention &a, int dtype);
@@ -363,10 +363,12 @@ void launch_attend(const Attention &a, const AttendPlan &p, float *part, hipStre
 // The gradient: key blocks take the rows in chunks, row blocks the keys; more than one chunk leaves
 // parts that are joined.
 struct AttendGradPlan {
-    int waves = 4, row_chunk = 1, key_chunk = 1;
+    int waves = 4, key_span = 128, row_span = 128;  // keys and rows of a block
+    int row_chunk = 1, key_chunk = 1;
     int key_splits = 1, row_splits = 1;             // of the query gradient, of the key and value gradient
     size_t stat = 0, top = 0, key_part = 0, row_part = 0, bytes = 0;  // offsets in the workspace, and its size
 };
+constexpr size_t kOneWaveBytes = 256;  // longer heads do not fit the registers of the one-wave kernel
 AttendGradPlan attend_grad_plan(const Attention &a, int dtype);
 template <class T>
 void launch_attend_grad(const Attention &a, const AttendGradPlan &p, char *ws, hipStream_t st);

@@ -109,7 +109,7 @@ __device__ __forceinline__ void finish(const Attention &a, float *part, int spli
 // A wave holds 32 rows, a block goes through the keys KT at a time; the next tile is on its way while one
 // is worked on.
 template <class T, int DP, int WAVES, int KT>
-__global__ __launch_bounds__(WAVES * 64, DP * sizeof(T) <= 256 ? 2 : 1) void attend_kernel(Attention a, float *part, int tiles, int splits)
+__global__ __launch_bounds__(WAVES * 64, DP * sizeof(T) <= 256 ? 2 : 1) void attend_kernel(Attention a, float *part, int tiles, int splits, int chunk)
 {
     using L = Tile<T, DP>;
     constexpr int KS = DP / 16, DB = DP / 32, KB = KT / 32, THREADS = WAVES * 64, ROWS = WAVES * 32;
@@ -132,9 +132,10 @@ __global__ __launch_bounds__(WAVES * 64, DP * sizeof(T) <= 256 ? 2 : 1) void att
     const T *qp = static_cast<const T *>(a.q.p) + n * a.q.n + t * a.q.t + (hk * a.G + row - t * a.G) * a.q.h;
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) q[ks] = load_frag<T>(qp, ks * 16 + half * 8, there ? a.D : 0);
-    // keys the block looks at, and this split's share of them in whole tiles
-    const int want = (a.seen(len, start, a.by_g.div(min(block_row + ROWS, a.R) - 1)) + KT - 1) / KT;
-    const int each = (want + splits - 1) / splits, kt0 = split * each, kt1 = min(want, kt0 + each);
+    // keys the block looks at, of this split's chunk
+    const int want = min(a.seen(len, start, a.by_g.div(min(block_row + ROWS, a.R) - 1)), split * chunk + chunk);
+    if (split > 0 && split * chunk >= want) return;  // the join passes over it
+    const int kt0 = split * chunk / KT, kt1 = (want + KT - 1) / KT;
     // of this wave's rows: tiles before `whole` are seen by every row, tiles from `none` on by none
     const bool rows = row0 < a.R;
     const int whole = rows ? a.seen(len, start, a.by_g.div(row0)) / KT : 0;
@@ -192,18 +193,18 @@ __global__ __launch_bounds__(WAVES * 64, DP * sizeof(T) <= 256 ? 2 : 1) void att
 }
 
 // Up to 32 rows a key head (a token or a few over a cache): every wave takes 32 keys of its own at a
-// time, keys straight into registers, values through LDS of its own; the block's waves are joined
-// at the end.  Bound by memory and its latency: nothing waits for another wave on the way.
+// time, through LDS of its own, and the block's waves are joined at the end.  Bound by memory and its
+// latency: nothing waits for another wave on the way.
 template <class T, int DP, int WAVES>
-__global__ __launch_bounds__(WAVES * 64, DP * sizeof(T) <= 256 ? 2 : 1) void attend_few_kernel(Attention a, float *part, int splits)
+__global__ __launch_bounds__(WAVES * 64, DP * sizeof(T) <= 256 ? 2 : 1) void attend_few_kernel(Attention a, float *part, int splits, int chunk)
 {
     using L = Tile<T, DP>;
     constexpr int KS = DP / 16, DB = DP / 32;
-    // the tiles of the waves, and then their outputs: 32 rows of DP float32
-    __shared__ __attribute__((aligned(16))) char lds[WAVES * 32 * DP * 4];
+    // the waves' tiles of keys and values, and then their outputs: 32 rows of DP float32
+    __shared__ __attribute__((aligned(16))) char lds[WAVES * 32 * DP * 2 * sizeof(T)];
     __shared__ float ms[WAVES][32], ls[WAVES][32];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), half = lane >> 5;
-    T *vl = reinterpret_cast<T *>(lds) + wave * 32 * DP;
+    T *kl = reinterpret_cast<T *>(lds) + wave * 64 * DP, *vl = kl + 32 * DP;
 
     int w = xcd_remap(blockIdx.x, gridDim.x);
     const int split = w % splits, nh = w / splits, n = nh / a.Hkv, hk = nh % a.Hkv;
@@ -212,23 +213,19 @@ __global__ __launch_bounds__(WAVES * 64, DP * sizeof(T) <= 256 ? 2 : 1) void att
     const bool there = row < a.R;
     const int seen = there ? a.seen(len, start, t) : 0;
 
-    // tiles of 32 keys, dealt to the splits in runs and to a block's waves in turn
-    const int want = (a.seen(len, start, a.Tq - 1) + 31) / 32, each = (want + splits - 1) / splits;
-    const int kt0 = split * each + wave, kt1 = min(want, split * each + each);
+    // tiles of 32 keys of this split's chunk, dealt to the block's waves in turn
+    const int want = min(a.seen(len, start, a.Tq - 1), split * chunk + chunk);
+    if (split > 0 && split * chunk >= want) return;  // the join passes over it
+    const int kt0 = split * chunk / 32 + wave, kt1 = (want + 31) / 32;
     const int whole = a.seen(len, start, 0) / 32;
     const T *kp = static_cast<const T *>(a.k.p) + n * a.k.n + hk * a.k.h;
     const T *vp = static_cast<const T *>(a.v.p) + n * a.v.n + hk * a.v.h;
 
-    Frag<T> kf[KS], q[KS];
-    Mover<T, DP, 32, 64> vm(lane);
-    auto load = [&](int kt) {
-        const int key = kt * 32 + (lane & 31);
-        const T *p = kp + key * a.k.t;
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks) kf[ks] = load_frag<T>(p, ks * 16 + half * 8, key < len ? a.D : 0);
-        vm.load(vp + int64_t(kt) * 32 * a.v.t, a.v.t, len - kt * 32, a.D);
-    };
-    if (kt0 < kt1) load(kt0);
+    Frag<T> q[KS];
+    // one tile on its way at a time: the values while the scores are made, the next keys while the values
+    // are added, in the same registers
+    Mover<T, DP, 32, 64> mv(lane);
+    if (kt0 < kt1) mv.load(kp + int64_t(kt0) * 32 * a.k.t, a.k.t, len - kt0 * 32, a.D);
     const T *qp = static_cast<const T *>(a.q.p) + n * a.q.n + t * a.q.t + (hk * a.G + g) * a.q.h;
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) q[ks] = load_frag<T>(qp, ks * 16 + half * 8, there ? a.D : 0);
@@ -239,15 +236,18 @@ __global__ __launch_bounds__(WAVES * 64, DP * sizeof(T) <= 256 ? 2 : 1) void att
     Running run;
     const float c = a.scale * kLog2e;
     for (int kt = kt0; kt < kt1; kt += WAVES) {
+        // the wave's own tiles: what it stores and reads there stays in order
+        mv.store(kl);
+        mv.load(vp + int64_t(kt) * 32 * a.v.t, a.v.t, len - kt * 32, a.D);
         f32x16 s[1] = {f32x16{}};
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) s[0] = mma(kf[ks], q[ks], s[0]);
-        vm.store(vl);
-        if (kt + WAVES < kt1) load(kt + WAVES);
+        for (int ks = 0; ks < KS; ++ks) s[0] = mma(L::by_rows(kl, lane & 31, ks, half), q[ks], s[0]);
         if (kt >= whole) hide(s, seen - kt * 32, half);
         run.look(s, o, c);
         run.weigh<T>(s, c);
-        // the wave's own tile: its stores are seen by its later reads in order
+        mv.store(vl);
+        const int next = kt + WAVES;
+        if (next < kt1) mv.load(kp + int64_t(next) * 32 * a.k.t, a.k.t, len - next * 32, a.D);
 #pragma unroll
         for (int st = 0; st < 2; ++st) {
             const Frag<T> p = operand<T>(s[0], st);
@@ -303,48 +303,63 @@ __global__ __launch_bounds__(WAVES * 64, DP * sizeof(T) <= 256 ? 2 : 1) void att
     if (there) finish<T, DB>(a, part, splits, split, nh, n, hk, row, half, m, l, o);
 }
 
-// The splits of a row, one wave a row: weights 2^(m - largest m).  A lane reads the statistics of one
-// split; C elements a lane, the parts of 8 splits asked for at a time.
-template <class T, int C>
-__global__ __launch_bounds__(64) void attend_join_kernel(Attention a, float *part, int splits)
+// The splits of a row, a block a row: weights 2^(m - largest m).  A lane reads the statistics of one split; the
+// waves (one for a few splits, four for many) take the parts in turn, 8 asked for at a time.  Chunks that a block of `span` rows had nothing of
+// are passed over.
+template <class T, int C, int WAVES>
+__global__ __launch_bounds__(WAVES * 64) void attend_join_kernel(Attention a, float *part, int splits, int chunk, int span)
 {
     const Parts ps(part, a, splits);
-    const int lane = threadIdx.x;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int64_t id = blockIdx.x;
     const int nh = int(id / a.R), row = int(id - int64_t(nh) * a.R), n = nh / a.Hkv, t = a.by_g.div(row);
     const int h = (nh - n * a.Hkv) * a.G + row - t * a.G;
+    const int want = a.seen(a.length(n), a.start(n), a.by_g.div(min(row / span * span + span, a.R) - 1));
+    const int count = max(1, (want + chunk - 1) / chunk);  // the first split always leaves its part
+    // a plan has at most 64 splits: one a lane
+    const bool mine = lane < count;
+    const float m = mine ? ps.stat[2 * (lane * ps.rows + id)] : -INFINITY, l = mine ? ps.stat[2 * (lane * ps.rows + id) + 1] : 0.0f;
     constexpr int AT_ONCE = 8;
-    float v[AT_ONCE][C];
-    auto load = [&](int s0) {
+    float acc[C] = {};
+    for (int s0 = wave; s0 < count; s0 += WAVES * AT_ONCE) {
+        float v[AT_ONCE][C];
 #pragma unroll
         for (int k = 0; k < AT_ONCE; ++k)
 #pragma unroll
             for (int i = 0; i < C; ++i) {
-                const int d = i * 64 + lane;
-                v[k][i] = s0 + k < splits && d < a.D ? ps.out[((s0 + k) * ps.rows + id) * a.D + d] : 0.0f;
+                const int s = s0 + WAVES * k, d = i * 64 + lane;
+                v[k][i] = s < count && d < a.D ? ps.out[(s * ps.rows + id) * a.D + d] : 0.0f;
             }
-    };
-    load(0);
-    // a plan has at most 64 splits: one a lane
-    const bool mine = lane < splits;
-    const float m = mine ? ps.stat[2 * (lane * ps.rows + id)] : -INFINITY, l = mine ? ps.stat[2 * (lane * ps.rows + id) + 1] : 0.0f;
-    float top = m;
+        float top = m;
 #pragma unroll
-    for (int s = 32; s; s >>= 1) top = fmaxf(top, __shfl_xor(top, s));
-    const float f = l == 0.0f ? 0.0f : exp2_fast(m - top);  // nothing seen there: nothing to add
-    float sum = l * f;
-#pragma unroll
-    for (int s = 32; s; s >>= 1) sum += __shfl_xor(sum, s);
-    float acc[C] = {};
-    for (int s0 = 0; s0 < splits; s0 += AT_ONCE) {
-        if (s0) load(s0);
+        for (int x = 32; x; x >>= 1) top = fmaxf(top, __shfl_xor(top, x));
+        const float f = l == 0.0f ? 0.0f : exp2_fast(m - top);  // nothing seen there: nothing to add
 #pragma unroll
         for (int k = 0; k < AT_ONCE; ++k) {
-            const float wt = __shfl(f, (s0 + k) & 63);
+            const float wt = __shfl(f, (s0 + WAVES * k) & 63);
 #pragma unroll
             for (int i = 0; i < C; ++i) acc[i] = fmaf(v[k][i], wt, acc[i]);
         }
     }
+    if constexpr (WAVES > 1) {
+        __shared__ float shared[WAVES - 1][C][64];
+        if (wave > 0) {
+#pragma unroll
+            for (int i = 0; i < C; ++i) shared[wave - 1][i][lane] = acc[i];
+        }
+        __syncthreads();
+        if (wave > 0) return;
+#pragma unroll
+        for (int x = 0; x < WAVES - 1; ++x)
+#pragma unroll
+            for (int i = 0; i < C; ++i) acc[i] += shared[x][i][lane];
+    }
+    float top = m;
+#pragma unroll
+    for (int x = 32; x; x >>= 1) top = fmaxf(top, __shfl_xor(top, x));
+    float sum = l == 0.0f ? 0.0f : l * exp2_fast(m - top);
+#pragma unroll
+    for (int x = 32; x; x >>= 1) sum += __shfl_xor(sum, x);
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
     T *out = static_cast<T *>(a.out) + ((int64_t(n) * a.Tq + t) * a.H + h) * a.D;
 #pragma unroll
@@ -359,9 +374,11 @@ void launch_attend(const Attention &a, const AttendPlan &p, float *part, hipStre
     const int heads = a.N * a.Hkv;
     with_head(a.D, [&](auto head) {
         constexpr int DP = decltype(head)::value, KT = DP * sizeof(T) > 256 ? 32 : 64, C = (DP + 63) / 64;
-        if (p.few) attend_few_kernel<T, DP, 4><<<unsigned(heads * p.splits), 256, 0, st>>>(a, part, p.splits);
-        else attend_kernel<T, DP, 4, KT><<<unsigned(heads * p.tiles * p.splits), 256, 0, st>>>(a, part, p.tiles, p.splits);
-        if (p.splits > 1) attend_join_kernel<T, C><<<unsigned(heads * a.R), 64, 0, st>>>(a, part, p.splits);
+        constexpr int FW = DP * sizeof(T) > 512 ? 2 : 4;  // their tiles fit LDS
+        if (p.few) attend_few_kernel<T, DP, FW><<<unsigned(heads * p.splits), FW * 64, 0, st>>>(a, part, p.splits, p.chunk);
+        else attend_kernel<T, DP, 4, KT><<<unsigned(heads * p.tiles * p.splits), 256, 0, st>>>(a, part, p.tiles, p.splits, p.chunk);
+        if (p.splits > 16) attend_join_kernel<T, C, 4><<<unsigned(heads * a.R), 256, 0, st>>>(a, part, p.splits, p.chunk, p.few ? 32 : 128);
+        else if (p.splits > 1) attend_join_kernel<T, C, 1><<<unsigned(heads * a.R), 64, 0, st>>>(a, part, p.splits, p.chunk, p.few ? 32 : 128);
     });
 }
 

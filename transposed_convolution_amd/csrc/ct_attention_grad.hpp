@@ -126,52 +126,85 @@ __device__ __forceinline__ int grad_shift(const Attention &a, const float *top, 
     }
 }
 
-// dk and dv of a block of keys, a wave 32 of them, from RT rows at a time.  The keys' operands stay in
-// registers, the values' too or, for longer heads (LDSV), in LDS.
-template <class T, int DP, int WAVES, int RT, bool LDSV>
-__global__ __launch_bounds__(WAVES * 64, DP * sizeof(T) <= 256 ? 2 : 1) void key_grad_kernel(
-    Attention a, const RowStat *stat, const float *top, float *part, int row_blocks, int blocks, int tiles, int splits, int chunk)
+// What the blocks of a call share, and how the work of one kind of block is cut.
+struct GradShared {
+    const RowStat *stat;
+    const float *top;
+    int row_blocks, blocks;
+};
+struct Share {
+    int tiles, splits, chunk;
+};
+
+// How long heads are held: the two accumulators of a wave's 32 keys take a register for each element of the
+// head, and its keys' and values' operands a quarter of one a byte.  Up to 128 bytes a head all of it
+// fits beside the scores at two waves a SIMD; beyond, the values' operands are read from LDS each time; at
+// 256 elements of 16 bits the keys' too, and two waves share the 32 keys, each with half of the columns (both make
+// all scores: 6 products for 4, where one wave kept 900 bytes in scratch and took 2.3 times as long).
+template <class T, int DP>
+struct KeyPlan {
+    static constexpr int kBytes = DP * int(sizeof(T));
+    static constexpr int kParts = DP == 256 && sizeof(T) == 2 ? 2 : 1;
+    static constexpr bool kValues = kBytes > 128 && kBytes <= 512, kKeys = kParts == 2;  // in LDS
+    static constexpr int kSpan = 128 / kParts;                                           // keys of a block of 4 waves
+};
+
+// dk and dv of a block of keys from RT rows at a time.
+template <class T, int DP, int WAVES, int RT>
+struct KeyGrad {
+using Plan = KeyPlan<T, DP>;
+static constexpr int PARTS = WAVES == 1 ? 1 : Plan::kParts, KEYS = WAVES / PARTS * 32;
+static constexpr bool LDSV = Plan::kValues, LDSK = Plan::kKeys;
+// two buffers where other waves are to be waited for and registers are not short
+static constexpr int BUFS = WAVES == 1 || Plan::kBytes > 128 ? 1 : 2;
+struct Lds {
+    T tile[BUFS][2][RT * DP], values[LDSV ? KEYS * DP : 8], keys[LDSK ? KEYS * DP : 8];
+    float lse2[BUFS][RT], delta[BUFS][RT];
+    int ends[BUFS][RT];
+};
+__device__ static __forceinline__ void run(const Attention &a, const GradShared &shared, float *part, Share sh, int block, int count, Lds &lds)
 {
     using L = Tile<T, DP>;
-    constexpr int KS = DP / 16, DB = DP / 32, RB = RT / 32, THREADS = WAVES * 64, KEYS = WAVES * 32;
-    __shared__ __attribute__((aligned(16))) T lds[2][2][RT * DP];
-    __shared__ __attribute__((aligned(16))) T values[LDSV ? KEYS * DP : 1];
-    __shared__ __attribute__((aligned(16))) float lse2[2][RT], delta[2][RT];
-    __shared__ __attribute__((aligned(16))) int ends[2][RT];
+    constexpr int KS = DP / 16, DB = DP / 32 / PARTS, RB = RT / 32, THREADS = WAVES * 64;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), half = lane >> 5;
+    const int tiles = sh.tiles, splits = sh.splits, chunk = sh.chunk;
 
-    int w = xcd_remap(blockIdx.x, gridDim.x);
+    int w = xcd_remap(block, count);
     const int split = w % splits;
     w /= splits;
     const int tile = w % tiles, nh = w / tiles, n = nh / a.Hkv, hk = nh - n * a.Hkv;
     const int len = a.length(n), start = a.start(n), from_token = a.first_token(len, start);
-    const int block_key = tile * KEYS, key0 = block_key + wave * 32, key = key0 + (lane & 31);
+    const int group = wave / PARTS * 32 + (lane & 31), column = wave % PARTS * DB;  // the lane's key, the wave's first 32 columns
+    const int block_key = tile * KEYS, key0 = block_key + wave / PARTS * 32, key = block_key + group;
     // rows from the first that sees the block's first key on, of this split's chunk
     const int from = a.causal ? max(0, min(block_key - start, a.Tq)) * a.G : 0;
     const int rt0 = max(from, split * chunk) / RT, rt1 = block_key < len ? (min(a.R, split * chunk + chunk) + RT - 1) / RT : 0;
     if (splits > 1 && rt0 >= rt1) return;  // the join passes over it
 
-    Frag<T> k[KS], v[LDSV ? 1 : KS];
+    Frag<T> k[LDSK ? 1 : KS], v[LDSV ? 1 : KS];
     const T *kp = static_cast<const T *>(a.k.p) + n * a.k.n + key * a.k.t + hk * a.k.h;
     const T *vp = static_cast<const T *>(a.v.p) + n * a.v.n + key * a.v.t + hk * a.v.h;
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
-        k[ks] = load_frag<T>(kp, ks * 16 + half * 8, key < len ? a.D : 0);
-        const Frag<T> f = load_frag<T>(vp, ks * 16 + half * 8, key < len ? a.D : 0);
-        if constexpr (LDSV) L::put(values, wave * 32 + (lane & 31), ks, half, f);  // its own lane reads it
-        else v[ks] = f;
+        // a lane reads from LDS what it put there (or the other wave of its keys, behind the loop's first barrier)
+        const Frag<T> f = load_frag<T>(kp, ks * 16 + half * 8, key < len ? a.D : 0);
+        if constexpr (LDSK) L::put(lds.keys, group, ks, half, f);
+        else k[ks] = f;
+        const Frag<T> g = load_frag<T>(vp, ks * 16 + half * 8, key < len ? a.D : 0);
+        if constexpr (LDSV) L::put(lds.values, group, ks, half, g);
+        else v[ks] = g;
     }
     f32x16 dk[DB], dv[DB];
 #pragma unroll
     for (int db = 0; db < DB; ++db) dk[db] = dv[db] = f32x16{};
 
-    const int shift = grad_shift<T, THREADS>(a, top, nh, row_blocks, blocks);
+    const int shift = grad_shift<T, THREADS>(a, shared.top, nh, shared.row_blocks, shared.blocks);
     const float bias = kHalf<T> ? float(kHalfBias) : 0.0f, c = a.scale * kLog2e;
     const float factor = a.scale * exp2f(float(shift) - bias);
 
     const T *qp = static_cast<const T *>(a.q.p) + n * a.q.n + hk * a.G * a.q.h;
     const T *dp = static_cast<const T *>(a.d_o.p) + n * a.d_o.n + hk * a.G * a.d_o.h;
-    const RowStat *sp = stat + int64_t(nh) * a.R;
+    const RowStat *sp = shared.stat + int64_t(nh) * a.R;
     Mover<T, DP, RT, THREADS> qm(tid), dm(tid);
     RowStat mine{INFINITY, 0.0f};
     int end = 0;
@@ -196,41 +229,49 @@ __global__ __launch_bounds__(WAVES * 64, DP * sizeof(T) <= 256 ? 2 : 1) void key
         }
     };
     auto store = [&](int buf) {
-        qm.store(lds[buf][0]);
-        dm.store(lds[buf][1]);
+        qm.store(lds.tile[buf][0]);
+        dm.store(lds.tile[buf][1]);
         if (tid < RT) {
-            lse2[buf][tid] = mine.lse2 - bias;
-            delta[buf][tid] = mine.delta * factor;
-            ends[buf][tid] = end;
+            lds.lse2[buf][tid] = mine.lse2 - bias;
+            lds.delta[buf][tid] = mine.delta * factor;
+            lds.ends[buf][tid] = end;
         }
     };
 
     if (rt0 < rt1) {
         load(rt0);
-        store(0);
+        if (BUFS == 2) store(0);
     }
     for (int rt = rt0; rt < rt1; ++rt) {
         __syncthreads();
-        const int buf = (rt - rt0) & 1;
+        const int buf = BUFS == 2 ? (rt - rt0) & 1 : 0;
+        if (BUFS == 1) {
+            store(0);
+            __syncthreads();
+        }
         if (rt + 1 < rt1) load(rt + 1);
-        const T *ql = lds[buf][0], *dl = lds[buf][1];
+        const T *ql = lds.tile[buf][0], *dl = lds.tile[buf][1];
         // the tile's first row sees fewest keys; rows that do not exist have P = 0
         const bool whole = key0 + 32 <= a.seen(len, start, a.by_g.div(rt * RT));
 #pragma unroll
         for (int rb = 0; rb < RB; ++rb) {
             f32x16 s = {}, g = {};
 #pragma unroll
-            for (int ks = 0; ks < KS; ++ks) s = mma(L::by_rows(ql, rb * 32 + (lane & 31), ks, half), k[ks], s);
+            for (int ks = 0; ks < KS; ++ks) {
+                const Frag<T> qf = L::by_rows(ql, rb * 32 + (lane & 31), ks, half);
+                if constexpr (LDSK) s = mma(qf, L::by_rows(lds.keys, group, ks, half), s);
+                else s = mma(qf, k[ks], s);
+            }
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) {
                 const Frag<T> df = L::by_rows(dl, rb * 32 + (lane & 31), ks, half);
-                if constexpr (LDSV) g = mma(df, L::by_rows(values, wave * 32 + (lane & 31), ks, half), g);
+                if constexpr (LDSV) g = mma(df, L::by_rows(lds.values, group, ks, half), g);
                 else g = mma(df, v[ks], g);
             }
 #pragma unroll
             for (int r4 = 0; r4 < 4; ++r4) {
                 const int at = rb * 32 + 8 * r4 + 4 * half;
-                const f32x4 le = *reinterpret_cast<const f32x4 *>(lse2[buf] + at), de = *reinterpret_cast<const f32x4 *>(delta[buf] + at);
+                const f32x4 le = *reinterpret_cast<const f32x4 *>(lds.lse2[buf] + at), de = *reinterpret_cast<const f32x4 *>(lds.delta[buf] + at);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const int r = 4 * r4 + j;
@@ -242,7 +283,7 @@ __global__ __launch_bounds__(WAVES * 64, DP * sizeof(T) <= 256 ? 2 : 1) void key
             if (!whole) {
 #pragma unroll
                 for (int r = 0; r < 16; ++r) {
-                    const bool sees = key - block_key < ends[buf][rb * 32 + c_row(r, half)];
+                    const bool sees = key - block_key < lds.ends[buf][rb * 32 + c_row(r, half)];
                     s[r] = sees ? s[r] : 0.0f;
                     g[r] = sees ? g[r] : 0.0f;
                 }
@@ -252,38 +293,44 @@ __global__ __launch_bounds__(WAVES * 64, DP * sizeof(T) <= 256 ? 2 : 1) void key
                 const Frag<T> pf = operand<T>(s, st), gf = operand<T>(g, st);
 #pragma unroll
                 for (int db = 0; db < DB; ++db) {
-                    dv[db] = mma(L::by_columns(dl, rb * 32 + st * 16, db, lane), pf, dv[db]);
-                    dk[db] = mma(L::by_columns(ql, rb * 32 + st * 16, db, lane), gf, dk[db]);
+                    dv[db] = mma(L::by_columns(dl, rb * 32 + st * 16, column + db, lane), pf, dv[db]);
+                    dk[db] = mma(L::by_columns(ql, rb * 32 + st * 16, column + db, lane), gf, dk[db]);
                 }
             }
         }
-        if (rt + 1 < rt1) store(buf ^ 1);
+        if (BUFS == 2 && rt + 1 < rt1) store(buf ^ 1);
     }
     if (key >= a.Tk) return;
     const float undo_k = exp2f(-float(shift)), undo_v = exp2f(-bias);
-    const int64_t at = ((int64_t(n) * a.Tk + key) * a.Hkv + hk) * a.D;
+    const int64_t at = ((int64_t(n) * a.Tk + key) * a.Hkv + hk) * a.D + column * 32;
+    const int D = a.D - column * 32;
     if (splits == 1) {
-        store_columns<T, DB>(static_cast<T *>(a.dk) + at, dk, undo_k, a.D, half);
-        store_columns<T, DB>(static_cast<T *>(a.dv) + at, dv, undo_v, a.D, half);
+        store_columns<T, DB>(static_cast<T *>(a.dk) + at, dk, undo_k, D, half);
+        store_columns<T, DB>(static_cast<T *>(a.dv) + at, dv, undo_v, D, half);
     } else {
         const int64_t all = int64_t(a.N) * a.Tk * a.Hkv * a.D;
         float *to = part + int64_t(split) * 2 * all + at;
-        store_columns<float, DB>(to, dk, undo_k, a.D, half);
-        store_columns<float, DB>(to + all, dv, undo_v, a.D, half);
+        store_columns<float, DB>(to, dk, undo_k, D, half);
+        store_columns<float, DB>(to + all, dv, undo_v, D, half);
     }
 }
+};
 
 // dq of a block of rows, a wave 32 of them, from KT keys at a time.
 template <class T, int DP, int WAVES, int KT>
-__global__ __launch_bounds__(WAVES * 64, DP * sizeof(T) <= 256 ? 2 : 1) void row_grad_kernel(
-    Attention a, const RowStat *stat, const float *top, float *part, int row_blocks, int blocks, int tiles, int splits, int chunk)
+struct RowGrad {
+static constexpr int BUFS = WAVES == 1 ? 1 : 2;
+struct Lds {
+    T tile[BUFS][2][KT * DP];
+};
+__device__ static __forceinline__ void run(const Attention &a, const GradShared &shared, float *part, Share sh, int block, int count, Lds &lds)
 {
     using L = Tile<T, DP>;
     constexpr int KS = DP / 16, DB = DP / 32, KB = KT / 32, THREADS = WAVES * 64, ROWS = WAVES * 32;
-    __shared__ __attribute__((aligned(16))) T lds[2][2][KT * DP];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), half = lane >> 5;
+    const int tiles = sh.tiles, splits = sh.splits, chunk = sh.chunk;
 
-    int w = xcd_remap(blockIdx.x, gridDim.x);
+    int w = xcd_remap(block, count);
     const int split = w % splits;
     w /= splits;
     const int tile = tiles - 1 - w % tiles, nh = w / tiles, n = nh / a.Hkv, hk = nh - n * a.Hkv;
@@ -294,14 +341,14 @@ __global__ __launch_bounds__(WAVES * 64, DP * sizeof(T) <= 256 ? 2 : 1) void row
     const int kt0 = split * chunk / KT, kt1 = (want + KT - 1) / KT;
     if (splits > 1 && kt0 >= kt1) return;  // the join passes over it
 
-    const int shift = grad_shift<T, THREADS>(a, top, nh, row_blocks, blocks);
+    const int shift = grad_shift<T, THREADS>(a, shared.top, nh, shared.row_blocks, shared.blocks);
     const float bias = kHalf<T> ? float(kHalfBias) : 0.0f, c = a.scale * kLog2e;
     const float factor = a.scale * exp2f(float(shift) - bias);
 
     const int row = row0 + (lane & 31), t = a.by_g.div(row), h = hk * a.G + row - t * a.G;
     const bool sees = row < a.R && t >= from_token;
     const int seen = sees ? a.seen(len, start, t) : 0;
-    const RowStat mine = row < a.R ? stat[int64_t(nh) * a.R + row] : RowStat{INFINITY, 0.0f};
+    const RowStat mine = row < a.R ? shared.stat[int64_t(nh) * a.R + row] : RowStat{INFINITY, 0.0f};
     const float lse2 = mine.lse2 - bias, delta = mine.delta * factor;
     Frag<T> q[KS], d_o[KS];
     const T *qp = static_cast<const T *>(a.q.p) + n * a.q.n + t * a.q.t + h * a.q.h;
@@ -326,17 +373,24 @@ __global__ __launch_bounds__(WAVES * 64, DP * sizeof(T) <= 256 ? 2 : 1) void row
 #pragma unroll
     for (int db = 0; db < DB; ++db) dq[db] = f32x16{};
 
+    auto store = [&](int buf) {
+        km.store(lds.tile[buf][0]);
+        vm.store(lds.tile[buf][1]);
+    };
     if (kt0 < kt1) {
         load(kt0);
-        km.store(lds[0][0]);
-        vm.store(lds[0][1]);
+        if (BUFS == 2) store(0);
     }
     for (int kt = kt0; kt < kt1; ++kt) {
         __syncthreads();
-        const int buf = (kt - kt0) & 1;
+        const int buf = BUFS == 2 ? (kt - kt0) & 1 : 0;
+        if (BUFS == 1) {
+            store(0);
+            __syncthreads();
+        }
         if (kt + 1 < kt1) load(kt + 1);
         if (kt < none) {
-            const T *kl = lds[buf][0], *vl = lds[buf][1];
+            const T *kl = lds.tile[buf][0], *vl = lds.tile[buf][1];
 #pragma unroll
             for (int kb = 0; kb < KB; ++kb) {
                 f32x16 s = {}, g = {};
@@ -362,10 +416,7 @@ __global__ __launch_bounds__(WAVES * 64, DP * sizeof(T) <= 256 ? 2 : 1) void row
                 }
             }
         }
-        if (kt + 1 < kt1) {
-            km.store(lds[buf ^ 1][0]);
-            vm.store(lds[buf ^ 1][1]);
-        }
+        if (BUFS == 2 && kt + 1 < kt1) store(buf ^ 1);
     }
     if (row >= a.R) return;
     const float undo = exp2f(-float(shift));
@@ -373,16 +424,45 @@ __global__ __launch_bounds__(WAVES * 64, DP * sizeof(T) <= 256 ? 2 : 1) void row
     if (splits == 1) store_columns<T, DB>(static_cast<T *>(a.dq) + at, dq, undo, a.D, half);
     else store_columns<float, DB>(part + int64_t(split) * a.N * a.Tq * a.H * a.D + at, dq, undo, a.D, half);
 }
+};
+
+// The kernels: each kind of block by itself, or, for small calls, both in one launch.
+template <class T, int DP, int WAVES, int RT>
+__global__ __launch_bounds__(WAVES * 64, DP * sizeof(T) <= 256 ? 2 : 1) void key_grad_kernel(Attention a, GradShared shared, float *part, Share sh)
+{
+    using K = KeyGrad<T, DP, WAVES, RT>;
+    __shared__ __attribute__((aligned(16))) char lds[sizeof(typename K::Lds)];
+    K::run(a, shared, part, sh, blockIdx.x, gridDim.x, *reinterpret_cast<typename K::Lds *>(lds));
+}
+template <class T, int DP, int WAVES, int KT>
+__global__ __launch_bounds__(WAVES * 64, DP * sizeof(T) <= 256 ? 2 : 1) void row_grad_kernel(Attention a, GradShared shared, float *part, Share sh)
+{
+    using K = RowGrad<T, DP, WAVES, KT>;
+    __shared__ __attribute__((aligned(16))) char lds[sizeof(typename K::Lds)];
+    K::run(a, shared, part, sh, blockIdx.x, gridDim.x, *reinterpret_cast<typename K::Lds *>(lds));
+}
+template <class T, int DP>
+__global__ __launch_bounds__(64) void both_grad_kernel(Attention a, GradShared shared, float *key_part, Share keys, int key_count,
+                                                       float *row_part, Share rows)
+{
+    using K = KeyGrad<T, DP, 1, 32>;
+    using R = RowGrad<T, DP, 1, 32>;
+    constexpr size_t BYTES = sizeof(typename K::Lds) > sizeof(typename R::Lds) ? sizeof(typename K::Lds) : sizeof(typename R::Lds);
+    __shared__ __attribute__((aligned(16))) char lds[BYTES];
+    const int b = blockIdx.x;
+    if (b < key_count) K::run(a, shared, key_part, keys, b, key_count, *reinterpret_cast<typename K::Lds *>(lds));
+    else R::run(a, shared, row_part, rows, b - key_count, int(gridDim.x) - key_count, *reinterpret_cast<typename R::Lds *>(lds));
+}
 
 // Sums of partial results, in their order, a block a token: first the tokens of the keys (dk and dv), then
-// those of the queries.  Chunks that a block of `span` keys or rows had nothing of are passed over.
+// those of the queries.  Chunks that a block of keys or rows had nothing of are passed over.
 template <class T>
 __global__ __launch_bounds__(256) void grad_join_kernel(Attention a, AttendGradPlan p, const float *key_part, const float *row_part,
-                                                        int span, int key_tokens, Div31 by_d)
+                                                        int key_tokens, Div31 by_d)
 {
     int token = blockIdx.x;
     if (token < key_tokens) {
-        const int n = token / a.Tk, block_key = (token - n * a.Tk) / span * span;
+        const int n = token / a.Tk, block_key = (token - n * a.Tk) / p.key_span * p.key_span;
         const int len = a.length(n), start = a.start(n);
         const int from = a.causal ? max(0, min(block_key - start, a.Tq)) * a.G : 0;
         const int s0 = from / p.row_chunk, s1 = block_key < len ? p.row_splits : 0;
@@ -402,7 +482,7 @@ __global__ __launch_bounds__(256) void grad_join_kernel(Attention a, AttendGradP
         const int64_t all = int64_t(a.N) * a.Tq * count, base = int64_t(token) * count;
         for (int i = threadIdx.x; i < count; i += 256) {
             const int h = by_d.div(i), row = t * a.G + h - a.by_g.div(h) * a.G;
-            const int want = a.seen(len, start, a.by_g.div(min(row / span * span + span, a.R) - 1));
+            const int want = a.seen(len, start, a.by_g.div(min(row / p.row_span * p.row_span + p.row_span, a.R) - 1));
             const int s1 = min(p.key_splits, (want + p.key_chunk - 1) / p.key_chunk);
             float sum = 0.0f;
 #pragma unroll 4
@@ -424,25 +504,24 @@ void launch_attend_grad(const Attention &a, const AttendGradPlan &p, char *ws, h
         if (a.D * int(sizeof(T)) <= 128) stat_kernel<T, 8><<<unsigned(heads * blocks), 256, 0, st>>>(a, stat, top, row_blocks, blocks);
         else stat_kernel<T, 16><<<unsigned(heads * blocks), 256, 0, st>>>(a, stat, top, row_blocks, blocks);
     }
+    const GradShared shared = {stat, top, row_blocks, blocks};
+    const int key_tiles = (a.Tk + p.key_span - 1) / p.key_span, row_tiles = (a.R + p.row_span - 1) / p.row_span;
+    const Share keys = {key_tiles, p.row_splits, p.row_chunk}, rows = {row_tiles, p.key_splits, p.key_chunk};
+    const int key_count = heads * key_tiles * p.row_splits, row_count = heads * row_tiles * p.key_splits;
     with_head(a.D, [&](auto head) {
-        constexpr int DP = decltype(head)::value, BYTES = DP * int(sizeof(T));
-        constexpr bool LDSV = BYTES > 128 && BYTES <= 512;
-        auto go = [&](auto waves) {
-            constexpr int W = decltype(waves)::value, SPAN = W * 32, TILE = W == 1 || BYTES > 128 ? 32 : 64;
-            const int key_tiles = (a.Tk + SPAN - 1) / SPAN, row_tiles = (a.R + SPAN - 1) / SPAN;
-            if (key_tiles > 0)
-                key_grad_kernel<T, DP, W, TILE, LDSV><<<unsigned(heads * key_tiles * p.row_splits), W * 64, 0, st>>>(
-                    a, stat, top, key_part, row_blocks, blocks, key_tiles, p.row_splits, p.row_chunk);
-            if (row_tiles > 0)
-                row_grad_kernel<T, DP, W, TILE><<<unsigned(heads * row_tiles * p.key_splits), W * 64, 0, st>>>(
-                    a, stat, top, row_part, row_blocks, blocks, row_tiles, p.key_splits, p.key_chunk);
-        };
-        if (p.waves == 1) go(std::integral_constant<int, 1>{});
-        else go(std::integral_constant<int, 4>{});
+        constexpr int DP = decltype(head)::value, TILE = DP * sizeof(T) > 128 ? 32 : 64;
+        if constexpr (DP * sizeof(T) <= kOneWaveBytes) {
+            if (p.waves == 1) {
+                both_grad_kernel<T, DP><<<unsigned(key_count + row_count), 64, 0, st>>>(a, shared, key_part, keys, key_count, row_part, rows);
+                return;
+            }
+        }
+        if (key_count) key_grad_kernel<T, DP, 4, TILE><<<unsigned(key_count), 256, 0, st>>>(a, shared, key_part, keys);
+        if (row_count) row_grad_kernel<T, DP, 4, TILE><<<unsigned(row_count), 256, 0, st>>>(a, shared, row_part, rows);
     });
     const int key_tokens = p.row_splits > 1 ? a.N * a.Tk : 0, row_tokens = p.key_splits > 1 ? a.N * a.Tq : 0;
     if (key_tokens + row_tokens > 0)
-        grad_join_kernel<T><<<unsigned(key_tokens + row_tokens), 256, 0, st>>>(a, p, key_part, row_part, 32 * p.waves, key_tokens, Div31(a.D));
+        grad_join_kernel<T><<<unsigned(key_tokens + row_tokens), 256, 0, st>>>(a, p, key_part, row_part, key_tokens, Div31(a.D));
 }
 
 }  // namespace ct
