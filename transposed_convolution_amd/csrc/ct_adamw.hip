@@ -8,6 +8,7 @@
 // the step itself takes the new states before they are rounded.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <string>
 #include <type_traits>
@@ -19,8 +20,10 @@ namespace {
 using ct::Raw;
 
 constexpr int kThreads = 256, kScaleBlock = 256;
-constexpr int kEntries = 40;      // tensors a launch takes: their descriptions are its arguments (below 4 KB)
-constexpr int kRun32 = 2048, kRun8 = 2048;  // elements a block updates
+// Tensors a launch takes: their descriptions are its arguments (below 4 KB), and a launch with few arguments is
+// quicker.
+constexpr int kEntries = 40, kFewEntries = 8;
+constexpr int kRun32 = 1024, kRun8 = 2048;  // elements a block updates
 constexpr float kTop = 448.0f, kLeastScale = 0x1p-126f, kLeastCode = 0x1p-9f;
 
 struct Entry {
@@ -34,9 +37,7 @@ struct Entry {
     float decay;
 };
 
-struct Step {
-    Entry e[kEntries];
-    unsigned first[kEntries + 1];  // first block of each tensor
+struct Hyper {
     int entries;
     float b1, c1, b2, c2, eps, lr, grad_scale;  // c1 = 1 - b1, c2 = 1 - b2
     float first_bias, second_root;              // 1 - b1^t and 1 / sqrt(1 - b2^t) of a host step
@@ -45,9 +46,14 @@ struct Step {
     const float *lr_at, *scale_at;  // device values in place of lr and grad_scale, or null
     int copy_type;
 };
+template <int N>
+struct Step : Hyper {
+    unsigned first[N + 1];  // first block of each tensor
+    Entry e[N];
+};
 
 // lr / (1 - b1^t), 1 / sqrt(1 - b2^t), grad_scale, lr: by one thread a block, behind its loads.
-__device__ __forceinline__ void constants(const Step &s, float (&out)[4])
+__device__ __forceinline__ void constants(const Hyper &s, float (&out)[4])
 {
     float first = s.first_bias, root = s.second_root;
     if (s.step) {
@@ -63,14 +69,15 @@ __device__ __forceinline__ void constants(const Step &s, float (&out)[4])
 }
 
 // m and v as written, in that order and without fused steps, so that a plain float32 form gives the same bits.
-__device__ __forceinline__ void moments(const Step &s, float g, float &m, float &v)
+__device__ __forceinline__ void moments(const Hyper &s, float g, float &m, float &v)
 {
 #pragma clang fp contract(off)
     m = m * s.b1 + g * s.c1;
     v = v * s.b2 + (g * g) * s.c2;
 }
 
-__device__ __forceinline__ int entry_of(const Step &s, unsigned block)
+template <int N>
+__device__ __forceinline__ int entry_of(const Step<N> &s, unsigned block)
 {
     int lo = 0, hi = s.entries - 1;
     while (lo < hi) {
@@ -105,7 +112,7 @@ __device__ __forceinline__ void store(void *p, int64_t i, int valid, const Raw<T
         if (j < valid) at[j] = r[j];
 }
 template <int V>
-__device__ __forceinline__ void store_copy(const Step &s, const Entry &e, int64_t i, int valid, const float (&p)[V])
+__device__ __forceinline__ void store_copy(const Hyper &s, const Entry &e, int64_t i, int valid, const float (&p)[V])
 {
     if (!e.copy) return;
     if (s.copy_type == CT_FLOAT16) {
@@ -121,8 +128,8 @@ __device__ __forceinline__ void store_copy(const Step &s, const Entry &e, int64_
     }
 }
 
-template <class P, class G>
-__global__ __launch_bounds__(kThreads) void adamw32_kernel(Step s)
+template <class P, class G, int TENSORS>
+__global__ __launch_bounds__(kThreads) void adamw32_kernel(Step<TENSORS> s)
 {
     constexpr int V = 4, N = kRun32 / (kThreads * V);
     const int k = entry_of(s, blockIdx.x);
@@ -201,9 +208,24 @@ __device__ __forceinline__ float scale_of(float top)
     return s < kLeastScale ? kLeastScale : s;
 }
 
+// x / s from the rounded 1 / s: the product, and its remainder's share.  A division each would take three
+// times the instructions, and the call is as much bound by them as by memory.
+__device__ __forceinline__ float quotient(float x, float s, float inv)
+{
+    const float q = x * inv;
+    return fmaf(fmaf(-q, s, x), inv, q);
+}
+
+// m over the denominator: sqrt(v) is at least 2^-75 where v is not 0, so the reciprocal instruction, good to
+// a unit, never meets a denormal number.
+__device__ __forceinline__ float update(float m, float root_v, float root, float eps, float rate)
+{
+    return m * __builtin_amdgcn_rcpf(fmaf(root_v, root, eps)) * rate;
+}
+
 // A wave updates the 256 elements of a scale at a time, four a lane.
-template <class P, class G>
-__global__ __launch_bounds__(kThreads) void adamw8_kernel(Step s)
+template <class P, class G, int TENSORS>
+__global__ __launch_bounds__(kThreads) void adamw8_kernel(Step<TENSORS> s)
 {
     constexpr int V = 4, WAVES = kThreads / 64, N = kRun8 / (kScaleBlock * WAVES);
     const int k = entry_of(s, blockIdx.x), lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -251,15 +273,16 @@ __global__ __launch_bounds__(kThreads) void adamw8_kernel(Step s)
             if (j >= valid[n]) mm = vv = 0.0f;  // behind the tensor's end
             m[j] = mm;
             r[j] = sqrtf(vv);
-            out[j] = float(p[n][j]) * keep - mm / (r[j] * root + s.eps) * rate;
+            out[j] = float(p[n][j]) * keep - update(mm, r[j], root, s.eps, rate);
             po[j] = P(out[j]);
         }
         const float m_scale = scale_of(wave_top(m)), v_scale = scale_of(wave_top(r));
+        const float m_inv = 1.0f / m_scale, v_inv = 1.0f / v_scale;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             const bool some = r[j] > 0.0f;
-            m[j] = m[j] / m_scale;
-            r[j] = r[j] / v_scale;
+            m[j] = quotient(m[j], m_scale, m_inv);
+            r[j] = quotient(r[j], v_scale, v_inv);
             // a positive root never becomes 0: what is divided by it would grow without bound
             if (some && r[j] < kLeastCode) r[j] = kLeastCode;
         }
@@ -317,7 +340,7 @@ extern "C" ct_status adamw_nd(ct_dtype dtype, ct_dtype grad_dtype, int state_bit
             !ct::aligned_to(t.m_scale, 4) || !ct::aligned_to(t.v_scale, 4) || !ct::aligned_to(t.copy, 2))
             return fail(CT_EINVAL, "tensor pointers must be aligned to the element size" + at);
     }
-    Step s{};
+    Step<kEntries> s{};
     s.b1 = float(beta1), s.c1 = float(1.0 - beta1), s.b2 = float(beta2), s.c2 = float(1.0 - beta2);
     s.eps = float(eps), s.lr = float(lr), s.grad_scale = float(grad_scale);
     s.log_b1 = std::log(beta1), s.log_b2 = std::log(beta2);
@@ -334,12 +357,24 @@ extern "C" ct_status adamw_nd(ct_dtype dtype, ct_dtype grad_dtype, int state_bit
     auto launch = [&] {
         if (!s.entries) return;
         const unsigned blocks = s.first[s.entries];
-        ct::with_type(dt, [&](auto p) {
-            ct::with_type(gt, [&](auto g) {
-                if (state_bits == 32) adamw32_kernel<decltype(p), decltype(g)><<<blocks, kThreads, 0, hs>>>(s);
-                else adamw8_kernel<decltype(p), decltype(g)><<<blocks, kThreads, 0, hs>>>(s);
+        auto go = [&](const auto &args) {
+            constexpr int N = int(sizeof(args.e) / sizeof(args.e[0]));
+            ct::with_type(dt, [&](auto p) {
+                ct::with_type(gt, [&](auto g) {
+                    if (state_bits == 32) adamw32_kernel<decltype(p), decltype(g), N><<<blocks, kThreads, 0, hs>>>(args);
+                    else adamw8_kernel<decltype(p), decltype(g), N><<<blocks, kThreads, 0, hs>>>(args);
+                });
             });
-        });
+        };
+        if (s.entries <= kFewEntries) {
+            Step<kFewEntries> few;
+            static_cast<Hyper &>(few) = s;
+            std::copy(s.first, s.first + kFewEntries + 1, few.first);
+            std::copy(s.e, s.e + kFewEntries, few.e);
+            go(few);
+        } else {
+            go(s);
+        }
         s.entries = 0;
     };
     ct::mark_before(hs);

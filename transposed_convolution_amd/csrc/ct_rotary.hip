@@ -11,6 +11,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <cstring>
 #include <string>
 #include <type_traits>
 
@@ -20,8 +21,11 @@ namespace {
 
 using ct::Raw;
 
-constexpr int kThreads = 256, kMaxPairs = 256, kMaxAxes = 4;
+constexpr int kThreads = 256, kMaxPairs = 256, kFewPairs = 64, kMaxAxes = 4, AHEAD = 2;
 
+// The table of angles is an argument of the launch, whose time grows with its arguments: up to 64 pairs have
+// a kernel of their own.
+template <int PAIRS>
 struct Rotary {
     const void *x;
     void *y;
@@ -32,12 +36,12 @@ struct Rotary {
     int units;                   // threads along a head: runs of V pairs, then of 2 V elements that stay
     int inverse;
     int axis_end[kMaxAxes];      // pairs up to the end of an axis
-    uint64_t turn[kMaxPairs];
+    uint64_t turn[PAIRS];
 };
 
 // One thread keeps the sines and cosines of V pairs of one token and turns them in `head_run` heads.
-template <class T, class I, bool BY_TWOS>
-__global__ __launch_bounds__(kThreads) void rotary_kernel(Rotary a)
+template <class T, class I, bool BY_TWOS, int PAIRS>
+__global__ __launch_bounds__(kThreads) void rotary_kernel(Rotary<PAIRS> a)
 {
     constexpr int V = ct::kVec<T>;
     const int64_t id = int64_t(blockIdx.x) * kThreads + threadIdx.x;
@@ -78,6 +82,16 @@ __global__ __launch_bounds__(kThreads) void rotary_kernel(Rotary a)
         return;
     }
     const int p0 = unit * V, count = min(V, a.pairs - p0);
+    const int d0 = BY_TWOS ? 2 * p0 : p0, d1 = BY_TWOS ? 2 * p0 + V : p0 + a.pairs;
+    const int n0 = BY_TWOS ? 2 * count : count, n1 = BY_TWOS ? 2 * count - V : count;
+    // the first heads' loads go out before the sines and cosines are made, the next ones' before these are turned
+    Raw<T, V> u[AHEAD], w[AHEAD];
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i)
+        if (h0 + i < h1) {
+            u[i] = load(x + (h0 + i) * a.xh + d0, n0);
+            w[i] = load(x + (h0 + i) * a.xh + d1, n1);
+        }
     const I *position = static_cast<const I *>(a.positions) + n * a.pn + t * a.pt;
     float c[V], s[V];
 #pragma unroll
@@ -92,31 +106,41 @@ __global__ __launch_bounds__(kThreads) void rotary_kernel(Rotary a)
         sincospif(half_turns, &s[j], &c[j]);
         if (a.inverse) s[j] = -s[j];
     }
-    const int d0 = BY_TWOS ? 2 * p0 : p0, d1 = BY_TWOS ? 2 * p0 + V : p0 + a.pairs;
-    const int n0 = BY_TWOS ? 2 * count : count, n1 = BY_TWOS ? 2 * count - V : count;
-    for (int h = h0; h < h1; ++h) {
-        const Raw<T, V> u = load(x + h * a.xh + d0, n0), w = load(x + h * a.xh + d1, n1);
-        Raw<T, V> uo, wo;
-        if constexpr (BY_TWOS) {
+    for (int h = h0; h < h1; h += AHEAD) {
+        Raw<T, V> un[AHEAD], wn[AHEAD];
 #pragma unroll
-            for (int j = 0; j < V / 2; ++j) {
-                const float a0 = float(u[2 * j]), b0 = float(u[2 * j + 1]), a1 = float(w[2 * j]), b1 = float(w[2 * j + 1]);
-                const int k = V / 2 + j;
-                uo[2 * j] = T(a0 * c[j] - b0 * s[j]);
-                uo[2 * j + 1] = T(a0 * s[j] + b0 * c[j]);
-                wo[2 * j] = T(a1 * c[k] - b1 * s[k]);
-                wo[2 * j + 1] = T(a1 * s[k] + b1 * c[k]);
+        for (int i = 0; i < AHEAD; ++i)
+            if (h + AHEAD + i < h1) {
+                un[i] = load(x + (h + AHEAD + i) * a.xh + d0, n0);
+                wn[i] = load(x + (h + AHEAD + i) * a.xh + d1, n1);
             }
-        } else {
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const float a0 = float(u[j]), b0 = float(w[j]);
-                uo[j] = T(a0 * c[j] - b0 * s[j]);
-                wo[j] = T(a0 * s[j] + b0 * c[j]);
+        for (int i = 0; i < AHEAD; ++i) {
+            if (h + i >= h1) break;
+            Raw<T, V> uo, wo;
+            if constexpr (BY_TWOS) {
+#pragma unroll
+                for (int j = 0; j < V / 2; ++j) {
+                    const float a0 = float(u[i][2 * j]), b0 = float(u[i][2 * j + 1]), a1 = float(w[i][2 * j]), b1 = float(w[i][2 * j + 1]);
+                    const int k = V / 2 + j;
+                    uo[2 * j] = T(a0 * c[j] - b0 * s[j]);
+                    uo[2 * j + 1] = T(a0 * s[j] + b0 * c[j]);
+                    wo[2 * j] = T(a1 * c[k] - b1 * s[k]);
+                    wo[2 * j + 1] = T(a1 * s[k] + b1 * c[k]);
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    const float a0 = float(u[i][j]), b0 = float(w[i][j]);
+                    uo[j] = T(a0 * c[j] - b0 * s[j]);
+                    wo[j] = T(a0 * s[j] + b0 * c[j]);
+                }
             }
+            store(y + (h + i) * a.yh + d0, n0, uo);
+            store(y + (h + i) * a.yh + d1, n1, wo);
         }
-        store(y + h * a.yh + d0, n0, uo);
-        store(y + h * a.yh + d1, n1, wo);
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) u[i] = un[i], w[i] = wn[i];
     }
 }
 
@@ -156,7 +180,7 @@ extern "C" ct_status rotary_nd(ct_dtype dtype, const int64_t *shape, const void 
     if (!(base > 0.0 && base <= 1e300)) return fail(CT_EINVAL, "base must be positive and finite");
     if ((whole_ladder != 0 && whole_ladder != 1) || (interleaved != 0 && interleaved != 1) || (inverse != 0 && inverse != 1))
         return fail(CT_EINVAL, "whole_ladder, interleaved and inverse must be 0 or 1");
-    Rotary a{};
+    Rotary<kMaxPairs> a{};
     int64_t pairs = 0;
     for (int i = 0; i < axes; ++i) {
         if (sections[i] < 0 || sections[i] > kMaxPairs) return fail(CT_EINVAL, "a section must have 0 to 256 pairs");
@@ -202,16 +226,26 @@ extern "C" ct_status rotary_nd(ct_dtype dtype, const int64_t *shape, const void 
     a.units = int((pairs + V - 1) / V + (stay + 2 * V - 1) / (2 * V));
     // a thread turns several heads with the sines and cosines it has, as long as the threads fill the chip
     a.head_run = 1;
-    while (a.head_run < a.H && a.tokens * a.units * ((a.H + 2 * a.head_run - 1) / (2 * a.head_run)) >= 256 * 1024) a.head_run *= 2;
+    while (a.head_run < a.H && a.tokens * a.units * ((a.H + 2 * a.head_run - 1) / (2 * a.head_run)) >= 512 * 1024) a.head_run *= 2;
     const int64_t threads = a.tokens * a.units * ((a.H + a.head_run - 1) / a.head_run);
     if (threads >= int64_t(1) << 32) return fail(CT_EUNSUPPORTED, "too many tokens and heads for one launch");
     const hipStream_t hs = static_cast<hipStream_t>(stream);
     ct::mark_before(hs);
     ct::with_type(dt, [&](auto t) {
         using T = decltype(t);
+        auto launch = [&](auto i, auto twos, const auto &args) {
+            constexpr int P = int(sizeof(args.turn) / sizeof(args.turn[0]));
+            rotary_kernel<T, decltype(i), decltype(twos)::value, P>
+                <<<unsigned((threads + kThreads - 1) / kThreads), kThreads, 0, hs>>>(args);
+        };
         auto go = [&](auto i, auto twos) {
-            rotary_kernel<T, decltype(i), decltype(twos)::value>
-                <<<unsigned((threads + kThreads - 1) / kThreads), kThreads, 0, hs>>>(a);
+            if (a.pairs <= kFewPairs) {
+                Rotary<kFewPairs> few;
+                std::memcpy(static_cast<void *>(&few), &a, sizeof few);  // the table is the last member
+                launch(i, twos, few);
+            } else {
+                launch(i, twos, a);
+            }
         };
         if (pt == CT_INT32) interleaved ? go(int32_t{}, std::true_type{}) : go(int32_t{}, std::false_type{});
         else interleaved ? go(int64_t{}, std::true_type{}) : go(int64_t{}, std::false_type{});
