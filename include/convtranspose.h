@@ -527,12 +527,13 @@ ct_status embedding_workspace_size(int64_t tokens, int64_t rows, int64_t width, 
  *   out[n,i,h,:] = sum over its keys of exp(s_ij - lse) * v[n,j,:]
  * A token sees key j when j < lengths[n], and in a causal call j <= starts[n] + i.  A token that
  * sees nothing gives out = 0 and lse = -infinity.  Keys and values at or behind lengths[n] are never
- * looked at; there may be anything.  A value that is not finite in a key or value that one token
- * of a causal call sees may make the outputs of others of that image and key head NaN.
+ * looked at; there may be anything.  A key or value that is not finite reaches the tokens that see
+ * it alone.
  *   dtype          CT_FLOAT32, CT_FLOAT16 or CT_BFLOAT16: the type of q, k, v and out; sums,
  *                  scores and statistics are float32, the weights are rounded to dtype once
  *   q_shape        {N, Tq, H, D}; 1 <= D <= 256
- *   kv_tokens, kv_heads   k and v are (N, kv_tokens, kv_heads, D); kv_heads divides H
+ *   kv_tokens, kv_heads   k and v are (N, kv_tokens, kv_heads, D); kv_heads divides H.  Fewer than
+ *                  2^30 rows (tokens times heads) of either side, a token's stride at most 2^24
  *   *_strides      strides in elements of a tensor's image, token and head axes, in that order;
  *                  a head's D elements are dense.  So q, k and v may be parts of one
  *                  projection, a cache of more tokens than are seen, or repeated (stride 0)
@@ -559,7 +560,8 @@ ct_status attention_nd(ct_dtype dtype, const int64_t *q_shape, int64_t kv_tokens
  *   dv_j = sum of P_ij dout_i,  dk_j = sum of dS_ij q_i,  dq_i = sum of dS_ij k_j,
  * the sums for keys over the tokens and heads that see them.  P is computed again, nothing of
  * size Tq * kv_tokens is stored.  Keys at or behind lengths[n] get zeros, so do tokens that see
- * nothing (whatever dout and q hold there).
+ * nothing (whatever dout and q hold there).  One value that is not finite where something is seen may
+ * make all gradients of its image and key head NaN.
  *   dout, out      (N, Tq, H, D) with strides like q's; out and lse are what attention_nd wrote
  *   dq, dk, dv     dense (N, Tq, H, D), (N, kv_tokens, kv_heads, D) twice, of dtype, not
  *                  overlapping anything else

@@ -11,6 +11,8 @@ import numpy as np
 
 from layer_refs import EPS, HALF_ULP
 
+# An exponential below float32's normal range is 0: a probability is off by up to this beside its relative error.
+FLUSH = 2.0 ** -126
 ROUND = {"f32": 0.0, "f16": HALF_ULP["f16"], "bf16": HALF_ULP["bf16"]}  # of an operand in the second product
 
 
@@ -88,7 +90,7 @@ def attend_grad(do, q, k, v, out, lse, scale, seen, dtype):
     parts = np.matmul(np.abs(doh), np.abs(vh).swapaxes(2, 3)) + (np.abs(doh) * np.abs(oh)).sum(3, keepdims=True)
     norm = lambda t: np.sqrt((t * t).sum(3)).max(2, initial=0.0)[..., None, None]  # noqa: E731
     least = 2.0 ** -36 * scale * norm(doh) * norm(vh) if dtype == "f16" else 0.0  # below float16's normal range
-    ds_tol = np.abs(ds) * (ROUND[dtype] + rel + 8 * EPS) + scale * p * parts * (d + 16) * EPS + least * seen[:, None]
+    ds_tol = np.abs(ds) * (ROUND[dtype] + rel + 8 * EPS) + scale * (p * (d + 16) * EPS + FLUSH) * parts + least * seen[:, None]
     sum_heads = lambda t: t.reshape(n, hk, h // hk, tk, d).sum(2).transpose(0, 2, 1, 3)  # noqa: E731
     by_key = lambda a, b: sum_heads(np.matmul(a.swapaxes(2, 3), b))  # noqa: E731
     dq = np.matmul(ds, kh).transpose(0, 2, 1, 3)
@@ -96,7 +98,7 @@ def attend_grad(do, q, k, v, out, lse, scale, seen, dtype):
     n_q, n_k = (tk + 64) * EPS, (tq * h // hk + 64) * EPS
     dq_tol = np.matmul(ds_tol + n_q * np.abs(ds), np.abs(kh)).transpose(0, 2, 1, 3)
     dk_tol = by_key(ds_tol + n_k * np.abs(ds), np.abs(qh))
-    dv_tol = by_key(p * (ROUND[dtype] + rel + n_k) + 2.0 ** -40 * seen[:, None], np.abs(doh))
+    dv_tol = by_key(p * (ROUND[dtype] + rel + n_k) + (FLUSH + (2.0 ** -40 if dtype == "f16" else 0.0)) * seen[:, None], np.abs(doh))
     return (dq, dk, dv), (dq_tol, dk_tol, dv_tol)
 
 

@@ -340,6 +340,7 @@ extern "C" ct_status adamw_nd(ct_dtype dtype, ct_dtype grad_dtype, int state_bit
             !ct::aligned_to(t.m_scale, 4) || !ct::aligned_to(t.v_scale, 4) || !ct::aligned_to(t.copy, 2))
             return fail(CT_EINVAL, "tensor pointers must be aligned to the element size" + at);
     }
+    if (std::all_of(list, list + tensors, [](const ct_adamw_tensor &t) { return t.count == 0; })) return CT_OK;
     Step<kEntries> s{};
     s.b1 = float(beta1), s.c1 = float(1.0 - beta1), s.b2 = float(beta2), s.c2 = float(1.0 - beta2);
     s.eps = float(eps), s.lr = float(lr), s.grad_scale = float(grad_scale);

@@ -96,8 +96,8 @@ ct_status sizes(int dt, const int64_t *q_shape, int64_t tk, int64_t kv_heads, At
         return bad(CT_EINVAL, "there must be at least one key head, and the heads must be a multiple of the key heads");
     if (q_shape[3] < 1) return bad(CT_EINVAL, "a head needs at least one element");
     if (q_shape[3] > ct::kMaxHead) return bad(CT_EUNSUPPORTED, "heads of more than 256 elements are not served");
-    // 2^30 rows of either side: every count below fits 64 bits, every launch 2^32 threads
-    constexpr int64_t most = int64_t(1) << 30;
+    // rows of either side below 2^30: places and counts of them fit an int, sums of two too
+    constexpr int64_t most = (int64_t(1) << 30) - 1;
     auto product = [&](int64_t x, int64_t y, int64_t z) {
         if (x == 0 || y == 0 || z == 0) return int64_t(0);
         return x > most || y > most || z > most || x > most / y || x * y > most / z ? most + 1 : x * y * z;
@@ -105,7 +105,7 @@ ct_status sizes(int dt, const int64_t *q_shape, int64_t tk, int64_t kv_heads, At
     if (q_shape[0] > most || q_shape[1] > most || q_shape[2] > most || tk > most || product(q_shape[0], q_shape[1], q_shape[2]) > most ||
         product(q_shape[0], tk, kv_heads) > most || product(q_shape[0], kv_heads, 1) > (1 << 22) ||
         product(q_shape[1], q_shape[2], 1) > most)
-        return bad(CT_EUNSUPPORTED, "more than 2^30 rows of queries or keys, or 2^22 images times key heads");
+        return bad(CT_EUNSUPPORTED, "2^30 rows of queries or keys and more, or more than 2^22 images times key heads");
     a->N = int(q_shape[0]);
     a->Tq = int(q_shape[1]);
     a->H = int(q_shape[2]);
@@ -141,6 +141,14 @@ ct_status options(float scale, const int32_t *lengths, int causal, const int32_t
     a->lengths = lengths;
     a->starts = starts;
     return CT_OK;
+}
+
+// Blocks of a launch of 256 threads each, which holds fewer than 2^32 threads.
+ct_status launchable(int64_t blocks, std::string *err)
+{
+    if (blocks < (int64_t(1) << 24)) return CT_OK;
+    *err = "too many images, heads and tokens for one launch";
+    return CT_EUNSUPPORTED;
 }
 
 // A strided operand: (n, t, h) strides in elements, none negative.
@@ -196,6 +204,8 @@ extern "C" ct_status attention_nd(ct_dtype dtype, const int64_t *q_shape, int64_
     a.out = out;
     a.lse = lse;
     const ct::AttendPlan p = ct::attend_plan(a, dt);
+    st = launchable(int64_t(a.N) * a.Hkv * p.tiles * p.splits, &err);
+    if (st != CT_OK) return fail(st, err);
     const hipStream_t hs = static_cast<hipStream_t>(stream);
     ct::Scratch ws;
     st = ws.take(workspace, workspace_bytes, p.bytes, hs, &err);
@@ -240,6 +250,10 @@ extern "C" ct_status attention_backward_nd(ct_dtype dtype, const int64_t *q_shap
     a.dk = dk;
     a.dv = dv;
     const ct::AttendGradPlan p = ct::attend_grad_plan(a, dt);
+    const int64_t heads = int64_t(a.N) * a.Hkv;
+    const auto blocks = [](int64_t n, int64_t each) { return (n + each - 1) / each; };
+    st = launchable(heads * std::max({blocks(a.R, 64) + blocks(a.Tk, 64), blocks(a.Tk, p.key_span) * p.row_splits + blocks(a.R, p.row_span) * p.key_splits}), &err);
+    if (st != CT_OK) return fail(st, err);
     const hipStream_t hs = static_cast<hipStream_t>(stream);
     ct::Scratch ws;
     st = ws.take(workspace, workspace_bytes, p.bytes, hs, &err);

@@ -57,9 +57,13 @@ struct Attention {
     float *lse = nullptr;      // (N, H, Tq): written by the forward call, read by the gradient
     void *dq = nullptr, *dk = nullptr, *dv = nullptr;
 
-    __device__ __forceinline__ int length(int n) const { return lengths ? max(0, min(lengths[n], Tk)) : Tk; }
     // The place of an image's first query among the keys, within what makes a difference.
     __device__ __forceinline__ int start(int n) const { return starts ? max(-Tq, min(starts[n], Tk)) : Tk - Tq; }
+    // An image's keys: those that one of its tokens sees at all.
+    __device__ __forceinline__ int length(int n, int start) const
+    {
+        return Tq == 0 ? 0 : seen(lengths ? max(0, min(lengths[n], Tk)) : Tk, start, Tq - 1);
+    }
     // Keys that token t of an image sees: the first seen(...) ones.
     __device__ __forceinline__ int seen(int len, int start, int t) const
     {

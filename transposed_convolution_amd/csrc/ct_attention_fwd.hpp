@@ -106,10 +106,86 @@ __device__ __forceinline__ void finish(const Attention &a, float *part, int spli
     }
 }
 
+// A weight of 0 times a value that is not finite is NaN, so in a causal call such a value reaches rows of its
+// tile that do not see it.  Rows whose result is not finite are therefore made again, one after the other by
+// the whole wave, from the keys [from, seen) alone.  (A test of the values on the way costs the
+// loop its registers: 720 us became 1490 for 8191 tokens and heads of 128.)
+__device__ __forceinline__ bool finite(float x) { return fabsf(x) <= 3.402823466e38f; }
+template <class T>
+__device__ __forceinline__ void redo_row(const Attention &a, float *part, int splits, int split, int nh, int n, int hk, int row,
+                                         int from, int end, int lane)
+{
+    const int t = a.by_g.div(row), h = hk * a.G + row - t * a.G;
+    const T *q = static_cast<const T *>(a.q.p) + n * a.q.n + t * a.q.t + h * a.q.h;
+    const T *k = static_cast<const T *>(a.k.p) + n * a.k.n + hk * a.k.h, *v = static_cast<const T *>(a.v.p) + n * a.v.n + hk * a.v.h;
+    const float c = a.scale * kLog2e;
+    auto score = [&](int j) {
+        float s = 0.0f;
+        for (int d = 0; d < a.D; ++d) s = fmaf(float(q[d]), float(k[j * a.k.t + d]), s);
+        return s * c;
+    };
+    float m = -INFINITY, l = 0.0f, acc[kMaxHead / 64] = {};
+    for (int j = from + lane; j < end; j += 64) m = fmaxf(m, score(j));
+#pragma unroll
+    for (int x = 32; x; x >>= 1) m = fmaxf(m, __shfl_xor(m, x));
+    const float base = m == -INFINITY ? 0.0f : m;
+    for (int j0 = from; j0 < end; j0 += 64) {
+        const float p = j0 + lane < end ? exp2_fast(score(j0 + lane) - base) : 0.0f;
+        l += p;
+        for (int i = 0; i < min(64, end - j0); ++i) {
+            const float w = __shfl(p, i);
+#pragma unroll
+            for (int x = 0; x < kMaxHead / 64; ++x)
+                if (x * 64 + lane < a.D) acc[x] = fmaf(w, float(v[(j0 + i) * a.v.t + x * 64 + lane]), acc[x]);
+        }
+    }
+#pragma unroll
+    for (int x = 32; x; x >>= 1) l += __shfl_xor(l, x);
+    const Parts ps(part, a, splits);
+    const int64_t at = split * ps.rows + int64_t(nh) * a.R + row, place = (int64_t(n) * a.Tq + t) * a.H + h;
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll
+    for (int x = 0; x < kMaxHead / 64; ++x) {
+        const int d = x * 64 + lane;
+        if (d >= a.D) continue;
+        if (splits == 1) static_cast<T *>(a.out)[place * a.D + d] = T(acc[x] * inv);
+        else ps.out[at * a.D + d] = acc[x];
+    }
+    if (lane == 0) {
+        if (splits == 1) {
+            a.lse[(int64_t(n) * a.H + h) * a.Tq + t] = l == 0.0f ? -INFINITY : (m + __log2f(l)) * kLn2;
+        } else {
+            ps.stat[2 * at] = l == 0.0f ? -INFINITY : m;
+            ps.stat[2 * at + 1] = l;
+        }
+    }
+}
+// The results of a wave's 32 rows, of the keys [from, ..) of its split.
+template <class T, int DB>
+__device__ __forceinline__ void finish_rows(const Attention &a, float *part, int splits, int split, int nh, int n, int hk, int row0,
+                                            int lane, int from, int seen, float m, float l, const f32x16 (&o)[DB])
+{
+    const int row = row0 + (lane & 31);
+    bool odd = false;
+    if (a.causal) {
+        odd = !finite(l);
+#pragma unroll
+        for (int db = 0; db < DB; ++db)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) odd |= !finite(o[db][r]);
+        odd = row < a.R && half_max(odd ? 1.0f : 0.0f) > 0.0f;
+    }
+    if (row < a.R && !odd) finish<T, DB>(a, part, splits, split, nh, n, hk, row, lane >> 5, m, l, o);
+    for (uint64_t left = __ballot(odd) & 0xffffffffu; left; left &= left - 1) {
+        const int i = __builtin_ctzll(left);
+        redo_row<T>(a, part, splits, split, nh, n, hk, row0 + i, from, __builtin_amdgcn_readlane(seen, i), lane);
+    }
+}
+
 // A wave holds 32 rows, a block goes through the keys KT at a time; the next tile is on its way while one
 // is worked on.
 template <class T, int DP, int WAVES, int KT>
-__global__ __launch_bounds__(WAVES * 64, DP * sizeof(T) <= 256 ? 2 : 1) void attend_kernel(Attention a, float *part, int tiles, int splits, int chunk)
+__global__ __launch_bounds__(WAVES * 64, DP * sizeof(T) <= 128 ? 3 : DP * sizeof(T) <= 256 ? 2 : 1) void attend_kernel(Attention a, float *part, int tiles, int splits, int chunk)
 {
     using L = Tile<T, DP>;
     constexpr int KS = DP / 16, DB = DP / 32, KB = KT / 32, THREADS = WAVES * 64, ROWS = WAVES * 32;
@@ -122,7 +198,7 @@ __global__ __launch_bounds__(WAVES * 64, DP * sizeof(T) <= 256 ? 2 : 1) void att
     const int split = w % splits;
     w /= splits;
     const int tile = tiles - 1 - w % tiles, nh = w / tiles, n = nh / a.Hkv, hk = nh % a.Hkv;
-    const int len = a.length(n), start = a.start(n);
+    const int start = a.start(n), len = a.length(n, start);
     const int block_row = tile * ROWS, row0 = block_row + wave * 32;
 
     const int row = row0 + (lane & 31), t = a.by_g.div(row);
@@ -130,8 +206,9 @@ __global__ __launch_bounds__(WAVES * 64, DP * sizeof(T) <= 256 ? 2 : 1) void att
     const int seen = there ? a.seen(len, start, t) : 0;
     Frag<T> q[KS];
     const T *qp = static_cast<const T *>(a.q.p) + n * a.q.n + t * a.q.t + (hk * a.G + row - t * a.G) * a.q.h;
+    // a row that sees nothing is not read: without keys there may be no q
 #pragma unroll
-    for (int ks = 0; ks < KS; ++ks) q[ks] = load_frag<T>(qp, ks * 16 + half * 8, there ? a.D : 0);
+    for (int ks = 0; ks < KS; ++ks) q[ks] = load_frag<T>(qp, ks * 16 + half * 8, seen > 0 ? a.D : 0);
     // keys the block looks at, of this split's chunk
     const int want = min(a.seen(len, start, a.by_g.div(min(block_row + ROWS, a.R) - 1)), split * chunk + chunk);
     if (split > 0 && split * chunk >= want) return;  // the join passes over it
@@ -189,7 +266,7 @@ __global__ __launch_bounds__(WAVES * 64, DP * sizeof(T) <= 256 ? 2 : 1) void att
         if (kt + 1 < kt1) store(buf ^ 1);
     }
     const float l = half_sum(run.l);
-    if (there) finish<T, DB>(a, part, splits, split, nh, n, hk, row, half, run.m, l, o);
+    finish_rows<T, DB>(a, part, splits, split, nh, n, hk, row0, lane, split * chunk, min(seen, want), run.m, l, o);
 }
 
 // Up to 32 rows a key head (a token or a few over a cache): every wave takes 32 keys of its own at a
@@ -208,7 +285,7 @@ __global__ __launch_bounds__(WAVES * 64, DP * sizeof(T) <= 256 ? 2 : 1) void att
 
     int w = xcd_remap(blockIdx.x, gridDim.x);
     const int split = w % splits, nh = w / splits, n = nh / a.Hkv, hk = nh % a.Hkv;
-    const int len = a.length(n), start = a.start(n);
+    const int start = a.start(n), len = a.length(n, start);
     const int row = lane & 31, t = a.by_g.div(row), g = row - t * a.G;
     const bool there = row < a.R;
     const int seen = there ? a.seen(len, start, t) : 0;
@@ -228,7 +305,7 @@ __global__ __launch_bounds__(WAVES * 64, DP * sizeof(T) <= 256 ? 2 : 1) void att
     if (kt0 < kt1) mv.load(kp + int64_t(kt0) * 32 * a.k.t, a.k.t, len - kt0 * 32, a.D);
     const T *qp = static_cast<const T *>(a.q.p) + n * a.q.n + t * a.q.t + (hk * a.G + g) * a.q.h;
 #pragma unroll
-    for (int ks = 0; ks < KS; ++ks) q[ks] = load_frag<T>(qp, ks * 16 + half * 8, there ? a.D : 0);
+    for (int ks = 0; ks < KS; ++ks) q[ks] = load_frag<T>(qp, ks * 16 + half * 8, seen > 0 ? a.D : 0);
 
     f32x16 o[DB];
 #pragma unroll
@@ -300,7 +377,7 @@ __global__ __launch_bounds__(WAVES * 64, DP * sizeof(T) <= 256 ? 2 : 1) void att
             }
         m = top;
     }
-    if (there) finish<T, DB>(a, part, splits, split, nh, n, hk, row, half, m, l, o);
+    finish_rows<T, DB>(a, part, splits, split, nh, n, hk, 0, lane, split * chunk, min(seen, want), m, l, o);
 }
 
 // The splits of a row, a block a row: weights 2^(m - largest m).  A lane reads the statistics of one split; the
@@ -314,7 +391,7 @@ __global__ __launch_bounds__(WAVES * 64) void attend_join_kernel(Attention a, fl
     const int64_t id = blockIdx.x;
     const int nh = int(id / a.R), row = int(id - int64_t(nh) * a.R), n = nh / a.Hkv, t = a.by_g.div(row);
     const int h = (nh - n * a.Hkv) * a.G + row - t * a.G;
-    const int want = a.seen(a.length(n), a.start(n), a.by_g.div(min(row / span * span + span, a.R) - 1));
+    const int start = a.start(n), want = a.seen(a.length(n, start), start, a.by_g.div(min(row / span * span + span, a.R) - 1));
     const int count = max(1, (want + chunk - 1) / chunk);  // the first split always leaves its part
     // a plan has at most 64 splits: one a lane
     const bool mine = lane < count;

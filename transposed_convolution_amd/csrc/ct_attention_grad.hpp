@@ -39,7 +39,7 @@ __global__ __launch_bounds__(256) void stat_kernel(Attention a, RowStat *stat, f
     constexpr int V = kVec<T>;
     const int in = threadIdx.x & (LANES - 1), first = threadIdx.x / LANES;
     const int nh = blockIdx.x / blocks, b = blockIdx.x - nh * blocks, n = nh / a.Hkv, hk = nh - n * a.Hkv;
-    const int len = a.length(n), start = a.start(n), from = a.first_token(len, start);
+    const int start = a.start(n), len = a.length(n, start), from = a.first_token(len, start);
     float most = 0.0f;
     const bool rows = b < row_blocks;
     const int base = (rows ? b : b - row_blocks) * kStatRows;
@@ -173,7 +173,7 @@ __device__ static __forceinline__ void run(const Attention &a, const GradShared 
     const int split = w % splits;
     w /= splits;
     const int tile = w % tiles, nh = w / tiles, n = nh / a.Hkv, hk = nh - n * a.Hkv;
-    const int len = a.length(n), start = a.start(n), from_token = a.first_token(len, start);
+    const int start = a.start(n), len = a.length(n, start), from_token = a.first_token(len, start);
     const int group = wave / PARTS * 32 + (lane & 31), column = wave % PARTS * DB;  // the lane's key, the wave's first 32 columns
     const int block_key = tile * KEYS, key0 = block_key + wave / PARTS * 32, key = block_key + group;
     // rows from the first that sees the block's first key on, of this split's chunk
@@ -334,7 +334,7 @@ __device__ static __forceinline__ void run(const Attention &a, const GradShared 
     const int split = w % splits;
     w /= splits;
     const int tile = tiles - 1 - w % tiles, nh = w / tiles, n = nh / a.Hkv, hk = nh - n * a.Hkv;
-    const int len = a.length(n), start = a.start(n), from_token = a.first_token(len, start);
+    const int start = a.start(n), len = a.length(n, start), from_token = a.first_token(len, start);
     const int block_row = tile * ROWS, row0 = block_row + wave * 32;
     // keys the block looks at, of this split's chunk
     const int want = min(a.seen(len, start, a.by_g.div(min(block_row + ROWS, a.R) - 1)), split * chunk + chunk);
@@ -435,7 +435,7 @@ __global__ __launch_bounds__(WAVES * 64, DP * sizeof(T) <= 256 ? 2 : 1) void key
     K::run(a, shared, part, sh, blockIdx.x, gridDim.x, *reinterpret_cast<typename K::Lds *>(lds));
 }
 template <class T, int DP, int WAVES, int KT>
-__global__ __launch_bounds__(WAVES * 64, DP * sizeof(T) <= 256 ? 2 : 1) void row_grad_kernel(Attention a, GradShared shared, float *part, Share sh)
+__global__ __launch_bounds__(WAVES * 64, DP * sizeof(T) <= 128 ? 3 : DP * sizeof(T) <= 256 ? 2 : 1) void row_grad_kernel(Attention a, GradShared shared, float *part, Share sh)
 {
     using K = RowGrad<T, DP, WAVES, KT>;
     __shared__ __attribute__((aligned(16))) char lds[sizeof(typename K::Lds)];
@@ -463,7 +463,7 @@ __global__ __launch_bounds__(256) void grad_join_kernel(Attention a, AttendGradP
     int token = blockIdx.x;
     if (token < key_tokens) {
         const int n = token / a.Tk, block_key = (token - n * a.Tk) / p.key_span * p.key_span;
-        const int len = a.length(n), start = a.start(n);
+        const int start = a.start(n), len = a.length(n, start);
         const int from = a.causal ? max(0, min(block_key - start, a.Tq)) * a.G : 0;
         const int s0 = from / p.row_chunk, s1 = block_key < len ? p.row_splits : 0;
         const int count = a.Hkv * a.D;
@@ -477,7 +477,7 @@ __global__ __launch_bounds__(256) void grad_join_kernel(Attention a, AttendGradP
         }
     } else {
         token -= key_tokens;
-        const int n = token / a.Tq, t = token - n * a.Tq, len = a.length(n), start = a.start(n);
+        const int n = token / a.Tq, t = token - n * a.Tq, start = a.start(n), len = a.length(n, start);
         const int count = a.H * a.D;
         const int64_t all = int64_t(a.N) * a.Tq * count, base = int64_t(token) * count;
         for (int i = threadIdx.x; i < count; i += 256) {
