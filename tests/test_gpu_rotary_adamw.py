@@ -180,3 +180,119 @@ def test_adamw_8_bit_codes_of_every_magnitude(T):
     want, scale = coded(np.sqrt(x * x), True)
     assert torch.equal(v.cpu().view(torch.uint8), want.view(torch.uint8))
     assert int((v.cpu().float() == 0).sum()) == int((x == 0).sum())
+
+
+@pytest.mark.parametrize("count", [1, 8, 9, 40, 41, 131])
+def test_adamw_many_tensors(T, count):
+    """More tensors than a launch's arguments describe; each is updated once."""
+    rng = np.random.default_rng(count)
+    sizes = rng.integers(1, 1500, size=count)
+    sizes[0] = 40000
+    p0 = [rng.normal(size=s).astype(np.float32) for s in sizes]
+    g0 = [rng.normal(size=s).astype(np.float32) for s in sizes]
+    p, g = ([torch.from_numpy(a).cuda() for a in part] for part in (p0, g0))
+    m, v = ([torch.zeros_like(t) for t in p] for _ in range(2))
+    T.adamw_nd(p, g, m, v, step=1, weight_decay=0.0, **HYPER)
+    torch.cuda.synchronize()
+    for k in range(count):
+        want, wm, wv = A.adamw(p0[k].astype(np.float64), g0[k].astype(np.float64), 0.0, 0.0, HYPER["lr"], *HYPER["betas"], HYPER["eps"],
+                               1, 0.0, 1.0)
+        R.assert_close(host(p[k]), want, param_bound(want, p0[k], want - p0[k]), "f32", f"param {k}")
+        R.assert_close(host(m[k]), wm, 4 * R.EPS * np.abs(wm), "f32", f"m {k}")
+        R.assert_close(host(v[k]), wv, 6 * R.EPS * np.abs(wv), "f32", f"v {k}")
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_adamw_and_rotary_captured_follow_device_values(T, bits):
+    """A graph of a turn and a step: replays with new step numbers, rates, gradients and positions equal eager calls."""
+    state = torch.float32 if bits == 32 else torch.float8_e4m3fn
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    x = torch.randn((2, 6, 4, 32), generator=gen, device="cuda")
+    pos = torch.zeros((2, 6, 2), dtype=torch.int64, device="cuda")
+    make = lambda: dict(p=[torch.ones(n, device="cuda") for n in (700, 2 * 6 * 4 * 32)],  # noqa: E731
+                        m=[torch.zeros(n, dtype=state, device="cuda") for n in (700, 1536)],
+                        v=[torch.zeros(n, dtype=state, device="cuda") for n in (700, 1536)],
+                        ms=[torch.zeros(n, device="cuda") for n in (3, 6)], vs=[torch.zeros(n, device="cuda") for n in (3, 6)])
+    grad = torch.zeros(700, device="cuda")
+    lr, step, scale = torch.zeros(1, device="cuda"), torch.zeros(1, dtype=torch.int64, device="cuda"), torch.zeros(1, device="cuda")
+    turned = torch.empty_like(x)
+
+    def arguments(s, **options):
+        if bits == 8:
+            options.update(m_scales=s["ms"], v_scales=s["vs"])
+        return (s["p"], [grad, turned.reshape(-1)], s["m"], s["v"]), options
+
+    kept, eager = make(), make()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        turn = T.PreparedCall(T.rotary_nd, x, pos, (6, 10), out=turned)
+        args, options = arguments(kept, lr=lr, step=step, grad_scale=scale, weight_decay=[0.1, 0.0])
+        update = T.PreparedCall(T.adamw_nd, *args, **options)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        turn()
+        update()
+    for k in range(1, 5):
+        grad.copy_(torch.randn(700, generator=gen, device="cuda"))
+        pos.copy_(torch.randint(0, 1 << 30, pos.shape, generator=gen, device="cuda"))
+        lr.fill_(0.01 * k), step.fill_(k), scale.fill_(1.0 / k)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(turned, T.rotary_nd(x, pos, (6, 10)))
+        args, options = arguments(eager, lr=lr, step=step, grad_scale=scale, weight_decay=[0.1, 0.0])
+        T.adamw_nd(*args, **options)
+        torch.cuda.synchronize()
+        bits_of = lambda t: t.view(torch.uint8) if t.dtype == torch.float8_e4m3fn else t  # noqa: E731
+        for name in ("p", "m", "v") + (("ms", "vs") if bits == 8 else ()):
+            assert all(torch.equal(bits_of(a), bits_of(b)) for a, b in zip(kept[name], eager[name])), (k, name)
+        assert not torch.equal(kept["p"][0], torch.ones(700, device="cuda"))
+
+
+def test_adamw_values_that_are_not_finite_stay_in_their_block(T):
+    for bad in (float("nan"), float("inf")):
+        p, g = torch.ones(1000, device="cuda"), torch.ones(1000, device="cuda")
+        g[300] = bad
+        m, v = (torch.zeros(1000, dtype=torch.float8_e4m3fn, device="cuda") for _ in range(2))
+        ms, vs = torch.zeros(4, device="cuda"), torch.zeros(4, device="cuda")
+        T.adamw_nd([p], [g], [m], [v], lr=0.1, step=1, m_scales=[ms], v_scales=[vs])
+        torch.cuda.synchronize()
+        held, root = m.float() * ms.repeat_interleave(256)[:1000], v.float() * vs.repeat_interleave(256)[:1000]
+        block = torch.zeros(1000, dtype=torch.bool, device="cuda")
+        block[256:512] = True
+        assert not torch.isfinite(held[block]).any() and not torch.isfinite(root[block]).any(), bad
+        assert torch.isfinite(held[~block]).all() and torch.isfinite(root[~block]).all() and not torch.isfinite(p[300])
+        others = torch.cat((p[:300], p[301:]))  # the step itself takes the states before they are held in 8 bits
+        assert torch.isfinite(others).all()
+
+
+def test_adamw_zero_states_and_refusals(T):
+    p = torch.ones(300, device="cuda")
+    zero = lambda: torch.zeros(300, dtype=torch.float8_e4m3fn, device="cuda")  # noqa: E731
+    m, v, ms, vs = zero(), zero(), torch.zeros(2, device="cuda"), torch.zeros(2, device="cuda")
+    T.adamw_nd([p], [torch.zeros(300, device="cuda")], [m], [v], lr=0.5, step=1, weight_decay=0.5, m_scales=[ms], v_scales=[vs])
+    torch.cuda.synchronize()
+    assert torch.equal(p, torch.full((300,), 0.75, device="cuda")) and not m.float().any() and not v.float().any()
+    f = lambda: torch.zeros(300, device="cuda")  # noqa: E731
+    for what, call in {
+        "twice": lambda: T.adamw_nd([p, p], [f(), f()], [f(), f()], [f(), f()], lr=0.1, step=1),
+        "dense": lambda: T.adamw_nd([p[::2]], [f()[:150]], [f()[:150]], [f()[:150]], lr=0.1, step=1),
+        "dense with 300": lambda: T.adamw_nd([p], [f()], [f()[:10]], [f()], lr=0.1, step=1),
+        "scales": lambda: T.adamw_nd([p], [f()], [zero()], [zero()], lr=0.1, step=1),
+        "float8": lambda: T.adamw_nd([p], [f()], [f().half()], [f().half()], lr=0.1, step=1),
+        "copies must": lambda: T.adamw_nd([p], [f()], [f()], [f()], lr=0.1, step=1, copies=[f()]),
+        "one value": lambda: T.adamw_nd([p], [f()], [f()], [f()], lr=f(), step=1),
+        "counts from 1": lambda: T.adamw_nd([p], [f()], [f()], [f()], lr=0.1, step=0),
+    }.items():
+        with pytest.raises(T.ConvTransposeError, match=what):
+            call()
+    x, pos = torch.zeros((2, 3, 4, 16), device="cuda"), torch.zeros((2, 3, 1), dtype=torch.int32, device="cuda")
+    for what, call in {
+        "half a head": lambda: T.rotary_nd(x, pos, (9,)),
+        "one section an axis": lambda: T.rotary_nd(x, pos, (2, 2)),
+        "int32 or int64": lambda: T.rotary_nd(x, pos.float(), (4,)),
+        "dense": lambda: T.rotary_nd(x.transpose(2, 3), pos, (1,)),
+        "x's strides": lambda: T.rotary_nd(x, pos, (4,), out=x.as_strided((2, 3, 4, 16), (16, 32, 96, 1))),
+    }.items():
+        with pytest.raises(T.ConvTransposeError, match=what):
+            call()
