@@ -45,11 +45,15 @@ AttendGradPlan attend_grad_plan(const Attention &a, int dtype)
     p.waves = fills || bytes > kOneWaveBytes ? 4 : 1;
     p.key_span = p.waves == 1 ? 32 : padded_head(a.D) == 256 && dtype != CT_FLOAT32 ? 64 : 128;
     p.row_span = p.waves == 1 ? 32 : 128;
+    // 512 blocks of 4 waves (2 a compute unit) or 2048 of one fill the chip.  In a causal call half of the (tile, chunk) pairs
+    // have nothing to do and the others differ, so three times as many are given out: at 4097 tokens, 16 heads
+    // over 4 of 128, key blocks with 6, 8, 12 and 16 parts took 479, 400, 316 and 356 us, row blocks with 2, 3, 4
+    // and 6 took 325, 204, 257 and 219.
     auto chunk = [&](int64_t blocks, int64_t length) {
         const int64_t wanted = p.waves == 1 ? 2048 : a.causal ? 1536 : 512, least = fills ? 512 : 64, step = 64;
         if (blocks == 0 || length == 0 || blocks >= wanted) return std::max<int64_t>(1, length);
         const int64_t splits = std::max<int64_t>(1, std::min({ceil_div(wanted, blocks), ceil_div(length, least), int64_t(kMostSplits)}));
-        return ceil_div(ceil_div(length, splits), step) * step;
+        return splits == 1 ? length : ceil_div(ceil_div(length, splits), step) * step;
     };
     p.row_chunk = int(chunk(heads * ceil_div(a.Tk, p.key_span), a.R));
     p.key_chunk = int(chunk(heads * ceil_div(a.R, p.row_span), a.Tk));

@@ -76,6 +76,15 @@ struct Attention {
     }
 };
 
+// The i-th tile of rows that an image's key head gives out.  In a causal call later rows see more keys: the longest
+// go first.  Where the heads do not come out even over the 8 XCDs, some of which then take parts of a head, long and
+// short ones take turns, so that every part is a fair one (4 heads of 129 tiles in whole order
+// gave one XCD three times the work of the next).
+__device__ __forceinline__ int long_first(int i, int tiles, int heads)
+{
+    return heads & 7 ? (i & 1 ? i >> 1 : tiles - 1 - (i >> 1)) : tiles - 1 - i;
+}
+
 using f32x16 = float __attribute__((ext_vector_type(16)));
 using f32x4 = float __attribute__((ext_vector_type(4)));
 
@@ -259,6 +268,33 @@ struct Tile {
         }
         return f;
     }
+};
+
+// N operands read from LDS, each for a matrix instruction, P of them ahead of their use.  Left to itself the compiler
+// asks for an operand right before its instruction when registers are short, and every instruction
+// then waits for LDS; here reads and matrix instructions keep the order they are written in.
+template <class T, int N, int P>
+struct Ahead {
+    Frag<T> f[P];
+    template <class L>
+    __device__ __forceinline__ void prime(L &&load)
+    {
+#pragma unroll
+        for (int i = 0; i < P && i < N; ++i) f[i] = load(i);
+        keep_order();
+    }
+    template <class L, class U>
+    __device__ __forceinline__ void run(L &&load, U &&use)
+    {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            use(i, f[i % P]);
+            if (i + P < N) f[i % P] = load(i + P);
+            keep_order();
+        }
+    }
+    // vector, scalar and transcendental instructions and global loads may pass
+    __device__ static __forceinline__ void keep_order() { __builtin_amdgcn_sched_barrier(0x416); }
 };
 
 // ROWS rows on their way from memory to a tile, 16 bytes a thread and piece; the threads of a row are a

@@ -189,15 +189,15 @@ __global__ __launch_bounds__(WAVES * 64, DP * sizeof(T) <= 128 ? 3 : DP * sizeof
 {
     using L = Tile<T, DP>;
     constexpr int KS = DP / 16, DB = DP / 32, KB = KT / 32, THREADS = WAVES * 64, ROWS = WAVES * 32;
+    constexpr int P1 = 4, P2 = 4;  // operands asked for ahead
     __shared__ __attribute__((aligned(16))) T lds[2][2][KT * DP];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), half = lane >> 5;
 
-    // an XCD takes a contiguous run of blocks: those of one image and key head share its L2; a
-    // causal call's long tiles go first
+    // an XCD takes a contiguous run of blocks: those of one image and key head share its L2
     int w = xcd_remap(blockIdx.x, gridDim.x);
     const int split = w % splits;
     w /= splits;
-    const int tile = tiles - 1 - w % tiles, nh = w / tiles, n = nh / a.Hkv, hk = nh % a.Hkv;
+    const int nh = w / tiles, tile = long_first(w - nh * tiles, tiles, a.N * a.Hkv), n = nh / a.Hkv, hk = nh % a.Hkv;
     const int start = a.start(n), len = a.length(n, start);
     const int block_row = tile * ROWS, row0 = block_row + wave * 32;
 
@@ -248,20 +248,22 @@ __global__ __launch_bounds__(WAVES * 64, DP * sizeof(T) <= 128 ? 3 : DP * sizeof
             const T *kl = lds[buf][0], *vl = lds[buf][1];
             f32x16 s[KB];
 #pragma unroll
-            for (int kb = 0; kb < KB; ++kb) {
-                s[kb] = f32x16{};
-#pragma unroll
-                for (int ks = 0; ks < KS; ++ks) s[kb] = mma(L::by_rows(kl, kb * 32 + (lane & 31), ks, half), q[ks], s[kb]);
-            }
+            for (int kb = 0; kb < KB; ++kb) s[kb] = f32x16{};
+            Ahead<T, KB * KS, P1> keys;
+            auto key = [&](int i) { return L::by_rows(kl, i / KS * 32 + (lane & 31), i % KS, half); };
+            keys.prime(key);
+            keys.run(key, [&](int i, const Frag<T> &f) { s[i / KS] = mma(f, q[i % KS], s[i / KS]); });
+            Ahead<T, KT / 16 * DB, P2> values;
+            auto value = [&](int i) { return L::by_columns(vl, i / DB * 16, i % DB, lane); };
+            values.prime(value);
             if (kt >= whole) hide(s, seen - kt * KT, half);
             run.look(s, o, c);
             run.template weigh<T>(s, c);
-#pragma unroll
-            for (int st = 0; st < KT / 16; ++st) {
-                const Frag<T> p = operand<T>(s[st / 2], st % 2);
-#pragma unroll
-                for (int db = 0; db < DB; ++db) o[db] = mma(L::by_columns(vl, st * 16, db, lane), p, o[db]);
-            }
+            Frag<T> p;
+            values.run(value, [&](int i, const Frag<T> &f) {
+                if (i % DB == 0) p = operand<T>(s[i / DB / 2], i / DB % 2);
+                o[i % DB] = mma(f, p, o[i % DB]);
+            });
         }
         if (kt + 1 < kt1) store(buf ^ 1);
     }

@@ -165,14 +165,14 @@ struct Lds {
 __device__ static __forceinline__ void run(const Attention &a, const GradShared &shared, float *part, Share sh, int block, int count, Lds &lds)
 {
     using L = Tile<T, DP>;
-    constexpr int KS = DP / 16, DB = DP / 32 / PARTS, RB = RT / 32, THREADS = WAVES * 64;
+    constexpr int KS = DP / 16, DB = DP / 32 / PARTS, RB = RT / 32, THREADS = WAVES * 64, P = DP * sizeof(T) > 128 ? 2 : 4;  // operands asked for ahead: registers are short in long heads
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), half = lane >> 5;
     const int tiles = sh.tiles, splits = sh.splits, chunk = sh.chunk;
 
     int w = xcd_remap(block, count);
     const int split = w % splits;
     w /= splits;
-    const int tile = w % tiles, nh = w / tiles, n = nh / a.Hkv, hk = nh - n * a.Hkv;
+    const int nh = w / tiles, tile = tiles - 1 - long_first(w - nh * tiles, tiles, a.N * a.Hkv), n = nh / a.Hkv, hk = nh - n * a.Hkv;
     const int start = a.start(n), len = a.length(n, start), from_token = a.first_token(len, start);
     const int group = wave / PARTS * 32 + (lane & 31), column = wave % PARTS * DB;  // the lane's key, the wave's first 32 columns
     const int block_key = tile * KEYS, key0 = block_key + wave / PARTS * 32, key = block_key + group;
@@ -256,18 +256,21 @@ __device__ static __forceinline__ void run(const Attention &a, const GradShared 
 #pragma unroll
         for (int rb = 0; rb < RB; ++rb) {
             f32x16 s = {}, g = {};
-#pragma unroll
-            for (int ks = 0; ks < KS; ++ks) {
-                const Frag<T> qf = L::by_rows(ql, rb * 32 + (lane & 31), ks, half);
-                if constexpr (LDSK) s = mma(qf, L::by_rows(lds.keys, group, ks, half), s);
-                else s = mma(qf, k[ks], s);
-            }
-#pragma unroll
-            for (int ks = 0; ks < KS; ++ks) {
-                const Frag<T> df = L::by_rows(dl, rb * 32 + (lane & 31), ks, half);
-                if constexpr (LDSV) g = mma(df, L::by_rows(lds.values, group, ks, half), g);
-                else g = mma(df, v[ks], g);
-            }
+            Ahead<T, 2 * KS, P> rows;
+            auto row = [&](int i) { return L::by_rows(i < KS ? ql : dl, rb * 32 + (lane & 31), i % KS, half); };
+            rows.prime(row);
+            rows.run(row, [&](int i, const Frag<T> &f) {
+                if (i < KS) {
+                    if constexpr (LDSK) s = mma(f, L::by_rows(lds.keys, group, i, half), s);
+                    else s = mma(f, k[i], s);
+                } else {
+                    if constexpr (LDSV) g = mma(f, L::by_rows(lds.values, group, i - KS, half), g);
+                    else g = mma(f, v[i - KS], g);
+                }
+            });
+            Ahead<T, 4 * DB, P> columns;
+            auto col = [&](int i) { return L::by_columns(i & 1 ? ql : dl, rb * 32 + i / (2 * DB) * 16, column + i / 2 % DB, lane); };
+            columns.prime(col);
 #pragma unroll
             for (int r4 = 0; r4 < 4; ++r4) {
                 const int at = rb * 32 + 8 * r4 + 4 * half;
@@ -288,15 +291,12 @@ __device__ static __forceinline__ void run(const Attention &a, const GradShared 
                     g[r] = sees ? g[r] : 0.0f;
                 }
             }
-#pragma unroll
-            for (int st = 0; st < 2; ++st) {
-                const Frag<T> pf = operand<T>(s, st), gf = operand<T>(g, st);
-#pragma unroll
-                for (int db = 0; db < DB; ++db) {
-                    dv[db] = mma(L::by_columns(dl, rb * 32 + st * 16, column + db, lane), pf, dv[db]);
-                    dk[db] = mma(L::by_columns(ql, rb * 32 + st * 16, column + db, lane), gf, dk[db]);
-                }
-            }
+            Frag<T> pf, gf;
+            columns.run(col, [&](int i, const Frag<T> &f) {
+                if (i % (2 * DB) == 0) pf = operand<T>(s, i / (2 * DB)), gf = operand<T>(g, i / (2 * DB));
+                if (i & 1) dk[i / 2 % DB] = mma(f, gf, dk[i / 2 % DB]);
+                else dv[i / 2 % DB] = mma(f, pf, dv[i / 2 % DB]);
+            });
         }
         if (BUFS == 2 && rt + 1 < rt1) store(buf ^ 1);
     }
@@ -326,14 +326,14 @@ struct Lds {
 __device__ static __forceinline__ void run(const Attention &a, const GradShared &shared, float *part, Share sh, int block, int count, Lds &lds)
 {
     using L = Tile<T, DP>;
-    constexpr int KS = DP / 16, DB = DP / 32, KB = KT / 32, THREADS = WAVES * 64, ROWS = WAVES * 32;
+    constexpr int KS = DP / 16, DB = DP / 32, KB = KT / 32, THREADS = WAVES * 64, ROWS = WAVES * 32, P = DP * sizeof(T) > 128 ? 2 : 4;  // operands asked for ahead: registers are short in long heads
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), half = lane >> 5;
     const int tiles = sh.tiles, splits = sh.splits, chunk = sh.chunk;
 
     int w = xcd_remap(block, count);
     const int split = w % splits;
     w /= splits;
-    const int tile = tiles - 1 - w % tiles, nh = w / tiles, n = nh / a.Hkv, hk = nh - n * a.Hkv;
+    const int nh = w / tiles, tile = long_first(w - nh * tiles, tiles, a.N * a.Hkv), n = nh / a.Hkv, hk = nh - n * a.Hkv;
     const int start = a.start(n), len = a.length(n, start), from_token = a.first_token(len, start);
     const int block_row = tile * ROWS, row0 = block_row + wave * 32;
     // keys the block looks at, of this split's chunk
@@ -394,10 +394,16 @@ __device__ static __forceinline__ void run(const Attention &a, const GradShared 
 #pragma unroll
             for (int kb = 0; kb < KB; ++kb) {
                 f32x16 s = {}, g = {};
-#pragma unroll
-                for (int ks = 0; ks < KS; ++ks) s = mma(L::by_rows(kl, kb * 32 + (lane & 31), ks, half), q[ks], s);
-#pragma unroll
-                for (int ks = 0; ks < KS; ++ks) g = mma(L::by_rows(vl, kb * 32 + (lane & 31), ks, half), d_o[ks], g);
+                Ahead<T, 2 * KS, P> rows;
+                auto row = [&](int i) { return L::by_rows(i < KS ? kl : vl, kb * 32 + (lane & 31), i % KS, half); };
+                rows.prime(row);
+                rows.run(row, [&](int i, const Frag<T> &f) {
+                    if (i < KS) s = mma(f, q[i], s);
+                    else g = mma(f, d_o[i - KS], g);
+                });
+                Ahead<T, 2 * DB, P> columns;
+                auto col = [&](int i) { return L::by_columns(kl, kb * 32 + i / DB * 16, i % DB, lane); };
+                columns.prime(col);
 #pragma unroll
                 for (int r = 0; r < 16; ++r) {
                     const float p = exp2_fast(fmaf(s[r], c, -lse2));
@@ -408,12 +414,11 @@ __device__ static __forceinline__ void run(const Attention &a, const GradShared 
 #pragma unroll
                     for (int r = 0; r < 16; ++r) g[r] = kb * 32 + c_row(r, half) < end ? g[r] : 0.0f;
                 }
-#pragma unroll
-                for (int st = 0; st < 2; ++st) {
-                    const Frag<T> gf = operand<T>(g, st);
-#pragma unroll
-                    for (int db = 0; db < DB; ++db) dq[db] = mma(L::by_columns(kl, kb * 32 + st * 16, db, lane), gf, dq[db]);
-                }
+                Frag<T> gf;
+                columns.run(col, [&](int i, const Frag<T> &f) {
+                    if (i % DB == 0) gf = operand<T>(g, i / DB);
+                    dq[i % DB] = mma(f, gf, dq[i % DB]);
+                });
             }
         }
         if (BUFS == 2 && kt + 1 < kt1) store(buf ^ 1);
