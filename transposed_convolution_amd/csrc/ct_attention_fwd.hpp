@@ -189,7 +189,7 @@ __global__ __launch_bounds__(WAVES * 64, DP * sizeof(T) <= 128 ? 3 : DP * sizeof
 {
     using L = Tile<T, DP>;
     constexpr int KS = DP / 16, DB = DP / 32, KB = KT / 32, THREADS = WAVES * 64, ROWS = WAVES * 32;
-    constexpr int P1 = 4, P2 = 4;  // operands asked for ahead
+    constexpr int P = 4;  // operands asked for ahead
     __shared__ __attribute__((aligned(16))) T lds[2][2][KT * DP];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), half = lane >> 5;
 
@@ -249,11 +249,11 @@ __global__ __launch_bounds__(WAVES * 64, DP * sizeof(T) <= 128 ? 3 : DP * sizeof
             f32x16 s[KB];
 #pragma unroll
             for (int kb = 0; kb < KB; ++kb) s[kb] = f32x16{};
-            Ahead<T, KB * KS, P1> keys;
+            Ahead<T, KB * KS, P> keys;
             auto key = [&](int i) { return L::by_rows(kl, i / KS * 32 + (lane & 31), i % KS, half); };
             keys.prime(key);
             keys.run(key, [&](int i, const Frag<T> &f) { s[i / KS] = mma(f, q[i % KS], s[i / KS]); });
-            Ahead<T, KT / 16 * DB, P2> values;
+            Ahead<T, KT / 16 * DB, P> values;
             auto value = [&](int i) { return L::by_columns(vl, i / DB * 16, i % DB, lane); };
             values.prime(value);
             if (kt >= whole) hide(s, seen - kt * KT, half);
