@@ -43,20 +43,20 @@ AttendGradPlan attend_grad_plan(const Attention &a, int dtype)
     const int64_t most = std::max(a.Tk, a.R);
     const bool fills = heads * ceil_div(most, 128) * std::max<int64_t>(1, std::min<int64_t>(a.Tk, a.R) / 512) >= 256;
     p.waves = fills || bytes > kOneWaveBytes ? 4 : 1;
-    p.key_span = p.waves == 1 ? 32 : padded_head(a.D) == 256 && dtype != CT_FLOAT32 ? 64 : 128;
+    p.key_span = p.waves == 1 ? 32 : wide_keys(bytes) ? 256 : padded_head(a.D) == 256 && dtype != CT_FLOAT32 ? 64 : 128;
     p.row_span = p.waves == 1 ? 32 : 128;
-    // 512 blocks of 4 waves (2 a compute unit) or 2048 of one fill the chip.  In a causal call half of the (tile, chunk) pairs
-    // have nothing to do and the others differ, so three times as many are given out: at 4097 tokens, 16 heads
-    // over 4 of 128, key blocks with 6, 8, 12 and 16 parts took 479, 400, 316 and 356 us, row blocks with 2, 3, 4
-    // and 6 took 325, 204, 257 and 219.
-    auto chunk = [&](int64_t blocks, int64_t length) {
-        const int64_t wanted = p.waves == 1 ? 2048 : a.causal ? 1536 : 512, least = fills ? 512 : 64, step = 64;
+    // 2048 waves (2 a SIMD) fill the chip.  In a causal call half of the (tile, chunk) pairs have nothing to do and
+    // the others differ, so three times as many are given out: the gradient of 4097 tokens, 16 heads over 4 of 128, took
+    // 511, 470, 446 and 494 us with 8, 10, 12 and 16 parts for its key blocks (8 waves each); its row blocks (4
+    // waves) alone 325, 204, 257 and 219 with 2, 3, 4 and 6.
+    auto chunk = [&](int64_t blocks, int64_t length, int waves) {
+        const int64_t wanted = (waves > 1 && a.causal ? 6144 : 2048) / waves, least = fills ? 512 : 64, step = 64;
         if (blocks == 0 || length == 0 || blocks >= wanted) return std::max<int64_t>(1, length);
         const int64_t splits = std::max<int64_t>(1, std::min({ceil_div(wanted, blocks), ceil_div(length, least), int64_t(kMostSplits)}));
         return splits == 1 ? length : ceil_div(ceil_div(length, splits), step) * step;
     };
-    p.row_chunk = int(chunk(heads * ceil_div(a.Tk, p.key_span), a.R));
-    p.key_chunk = int(chunk(heads * ceil_div(a.R, p.row_span), a.Tk));
+    p.row_chunk = int(chunk(heads * ceil_div(a.Tk, p.key_span), a.R, p.waves > 1 && wide_keys(bytes) ? 8 : p.waves));
+    p.key_chunk = int(chunk(heads * ceil_div(a.R, p.row_span), a.Tk, p.waves));
     p.row_splits = int(std::max<int64_t>(1, ceil_div(a.R, p.row_chunk)));
     p.key_splits = int(std::max<int64_t>(1, ceil_div(a.Tk, p.key_chunk)));
     size_t at = 0;
@@ -256,7 +256,9 @@ extern "C" ct_status attention_backward_nd(ct_dtype dtype, const int64_t *q_shap
     const ct::AttendGradPlan p = ct::attend_grad_plan(a, dt);
     const int64_t heads = int64_t(a.N) * a.Hkv;
     const auto blocks = [](int64_t n, int64_t each) { return (n + each - 1) / each; };
-    st = launchable(heads * std::max({blocks(a.R, 64) + blocks(a.Tk, 64), blocks(a.Tk, p.key_span) * p.row_splits + blocks(a.R, p.row_span) * p.key_splits}), &err);
+    // (a block of 8 waves counts twice)
+    st = launchable(heads * std::max(blocks(a.R, 64) + blocks(a.Tk, 64), blocks(a.Tk, std::min(p.key_span, 128)) * p.row_splits +
+                                                                             blocks(a.R, p.row_span) * p.key_splits), &err);
     if (st != CT_OK) return fail(st, err);
     const hipStream_t hs = static_cast<hipStream_t>(stream);
     ct::Scratch ws;

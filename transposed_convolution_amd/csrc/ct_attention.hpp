@@ -320,15 +320,24 @@ struct Mover {
         const char *p = reinterpret_cast<const char *>(base);
         const int64_t step = kStep * stride * int64_t(sizeof(T));
         if (valid >= ROWS && D % L::kChunk == 0) {
-            // threads behind the row's end keep the zeros they began with
-            if (column < D) {
-#pragma unroll
-                for (int i = 0; i < kPieces; ++i) r[i] = *reinterpret_cast<const Chunk *>(p + i * step + at);
-            }
+            whole(D, [&](int i) { return p + i * step + at; });
         } else {
 #pragma unroll
             for (int i = 0; i < kPieces; ++i)
                 r[i] = load_chunk<T>(reinterpret_cast<const T *>(p + i * step + at), row0 + i * kStep < valid ? D - column : 0, D % L::kChunk);
+        }
+    }
+    // Pieces that all exist, of rows of whole chunks, from at(i).
+    template <class F>
+    __device__ __forceinline__ void whole(int D, F &&at)
+    {
+        if (L::kChunks == kLanes && D == DP) {
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i) r[i] = *reinterpret_cast<const Chunk *>(at(i));
+        } else if (column < D) {
+            // threads behind the row's end keep the zeros they began with
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i) r[i] = *reinterpret_cast<const Chunk *>(at(i));
         }
     }
     // Rows row(i), null for zeros.
@@ -409,6 +418,10 @@ struct AttendGradPlan {
     size_t stat = 0, top = 0, key_part = 0, row_part = 0, bytes = 0;  // offsets in the workspace, and its size
 };
 constexpr size_t kOneWaveBytes = 256;  // longer heads do not fit the registers of the one-wave kernel
+
+// Heads (padded) of 129 to 256 bytes: a block of the key gradient has 8 waves, one block a compute unit, so that its
+// keys and values fit LDS.
+constexpr bool wide_keys(size_t bytes) { return bytes > 128 && bytes <= 256; }
 AttendGradPlan attend_grad_plan(const Attention &a, int dtype);
 template <class T>
 void launch_attend_grad(const Attention &a, const AttendGradPlan &p, char *ws, hipStream_t st);

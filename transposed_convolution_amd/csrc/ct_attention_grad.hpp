@@ -29,6 +29,11 @@ struct RowStat {
     float lse2, delta;
 };
 
+// Operands asked for ahead.  Gradient with heads of 64 / 128 / 256 (float16, 4096 tokens), 2: 1242 / 1204 / 1280 us,
+// 3: 1240 / 1140 / 1424, 4: 1230 / 1180 / 1305; registers are short in long heads.
+template <class T, int DP>
+constexpr int kAhead = DP * sizeof(T) > 256 ? 2 : DP * sizeof(T) > 128 ? 3 : 4;
+
 constexpr int kStatRows = 64;  // rows or keys a block of stat_kernel looks at
 
 // RowStat of the rows, and for float16 the largest norm of 64 rows' do, or of 64 keys' values, for each
@@ -137,298 +142,307 @@ struct Share {
 };
 
 // How long heads are held: the two accumulators of a wave's 32 keys take a register for each element of the
-// head, and its keys' and values' operands a quarter of one a byte.  Up to 128 bytes a head all of it
-// fits beside the scores at two waves a SIMD; beyond, the values' operands are read from LDS each time; at
-// 256 elements of 16 bits the keys' too, and two waves share the 32 keys, each with half of the columns (both make
-// all scores: 6 products for 4, where one wave kept 900 bytes in scratch and took 2.3 times as long).
+// head, and its keys' and values' operands an eighth of one a byte.  Up to 128 bytes a head all of it fits beside
+// the scores at two waves a SIMD.  Beyond, the values' operands are read from LDS each time, at 256 bytes the keys'
+// too: 8 waves share the rows' tile then, so that one block of 16-bit heads of 128 has 147 KB (4096 tokens, 4 x 8
+// heads, float16: 1410 us with 4 waves and the keys in registers, some of them in scratch, 1325 with 8, 1204 with the keys
+// in LDS).  At 256 elements of 16 bits two waves share the 32 keys, each with half of the columns: both make all
+// scores, 6 products for 4, but one wave kept 900 bytes in scratch (2 x 4096 tokens, 4 heads, float16: 3927 us, now 1290).
 template <class T, int DP>
 struct KeyPlan {
     static constexpr int kBytes = DP * int(sizeof(T));
     static constexpr int kParts = DP == 256 && sizeof(T) == 2 ? 2 : 1;
-    static constexpr bool kValues = kBytes > 128 && kBytes <= 512, kKeys = kParts == 2;  // in LDS
-    static constexpr int kSpan = 128 / kParts;                                           // keys of a block of 4 waves
+    static constexpr bool kValues = kBytes > 128 && kBytes <= 512, kKeys = kParts == 2 || kBytes == 256;  // in LDS
+    static constexpr int kWaves = wide_keys(kBytes) ? 8 : 4;
 };
 
 // dk and dv of a block of keys from RT rows at a time.
 template <class T, int DP, int WAVES, int RT>
 struct KeyGrad {
-using Plan = KeyPlan<T, DP>;
-static constexpr int PARTS = WAVES == 1 ? 1 : Plan::kParts, KEYS = WAVES / PARTS * 32;
-static constexpr bool LDSV = Plan::kValues, LDSK = Plan::kKeys;
-// two buffers where other waves are to be waited for and registers are not short
-static constexpr int BUFS = WAVES == 1 || Plan::kBytes > 128 ? 1 : 2;
-struct Lds {
-    T tile[BUFS][2][RT * DP], values[LDSV ? KEYS * DP : 8], keys[LDSK ? KEYS * DP : 8];
-    float lse2[BUFS][RT], delta[BUFS][RT];
-    int ends[BUFS][RT];
-};
-__device__ static __forceinline__ void run(const Attention &a, const GradShared &shared, float *part, Share sh, int block, int count, Lds &lds)
-{
-    using L = Tile<T, DP>;
-    constexpr int KS = DP / 16, DB = DP / 32 / PARTS, RB = RT / 32, THREADS = WAVES * 64, P = DP * sizeof(T) > 128 ? 2 : 4;  // operands asked for ahead: registers are short in long heads
-    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), half = lane >> 5;
-    const int tiles = sh.tiles, splits = sh.splits, chunk = sh.chunk;
-
-    int w = xcd_remap(block, count);
-    const int split = w % splits;
-    w /= splits;
-    const int nh = w / tiles, tile = tiles - 1 - long_first(w - nh * tiles, tiles, a.N * a.Hkv), n = nh / a.Hkv, hk = nh - n * a.Hkv;
-    const int start = a.start(n), len = a.length(n, start), from_token = a.first_token(len, start);
-    const int group = wave / PARTS * 32 + (lane & 31), column = wave % PARTS * DB;  // the lane's key, the wave's first 32 columns
-    const int block_key = tile * KEYS, key0 = block_key + wave / PARTS * 32, key = block_key + group;
-    // rows from the first that sees the block's first key on, of this split's chunk
-    const int from = a.causal ? max(0, min(block_key - start, a.Tq)) * a.G : 0;
-    const int rt0 = max(from, split * chunk) / RT, rt1 = block_key < len ? (min(a.R, split * chunk + chunk) + RT - 1) / RT : 0;
-    if (splits > 1 && rt0 >= rt1) return;  // the join passes over it
-
-    Frag<T> k[LDSK ? 1 : KS], v[LDSV ? 1 : KS];
-    const T *kp = static_cast<const T *>(a.k.p) + n * a.k.n + key * a.k.t + hk * a.k.h;
-    const T *vp = static_cast<const T *>(a.v.p) + n * a.v.n + key * a.v.t + hk * a.v.h;
-#pragma unroll
-    for (int ks = 0; ks < KS; ++ks) {
-        // a lane reads from LDS what it put there (or the other wave of its keys, behind the loop's first barrier)
-        const Frag<T> f = load_frag<T>(kp, ks * 16 + half * 8, key < len ? a.D : 0);
-        if constexpr (LDSK) L::put(lds.keys, group, ks, half, f);
-        else k[ks] = f;
-        const Frag<T> g = load_frag<T>(vp, ks * 16 + half * 8, key < len ? a.D : 0);
-        if constexpr (LDSV) L::put(lds.values, group, ks, half, g);
-        else v[ks] = g;
-    }
-    f32x16 dk[DB], dv[DB];
-#pragma unroll
-    for (int db = 0; db < DB; ++db) dk[db] = dv[db] = f32x16{};
-
-    const int shift = grad_shift<T, THREADS>(a, shared.top, nh, shared.row_blocks, shared.blocks);
-    const float bias = kHalf<T> ? float(kHalfBias) : 0.0f, c = a.scale * kLog2e;
-    const float factor = a.scale * exp2f(float(shift) - bias);
-
-    const T *qp = static_cast<const T *>(a.q.p) + n * a.q.n + hk * a.G * a.q.h;
-    const T *dp = static_cast<const T *>(a.d_o.p) + n * a.d_o.n + hk * a.G * a.d_o.h;
-    const RowStat *sp = shared.stat + int64_t(nh) * a.R;
-    Mover<T, DP, RT, THREADS> qm(tid), dm(tid);
-    RowStat mine{INFINITY, 0.0f};
-    int end = 0;
-    auto load = [&](int rt) {
-        if (a.G == 1 && rt * RT >= from_token) {
-            qm.load(qp + int64_t(rt) * RT * a.q.t, a.q.t, a.R - rt * RT, a.D);
-            dm.load(dp + int64_t(rt) * RT * a.d_o.t, a.d_o.t, a.R - rt * RT, a.D);
-        } else {
-            // rows that see nothing are zeros: what stands there takes no part
-            auto place = [&](int r, const T *p, const Strided &s) -> const T * {
-                const int row = rt * RT + r, t = a.by_g.div(row);
-                return row < a.R && t >= from_token ? p + t * s.t + (row - t * a.G) * s.h : nullptr;
-            };
-            qm.load(a.D, [&](int r) { return place(r, qp, a.q); });
-            dm.load(a.D, [&](int r) { return place(r, dp, a.d_o); });
-        }
-        if (tid < RT) {
-            const int row = rt * RT + tid;
-            mine = row < a.R ? sp[row] : RowStat{INFINITY, 0.0f};
-            // how many of the keys from the block's first on the row sees
-            end = row < a.R ? a.seen(len, start, a.by_g.div(row)) - block_key : 0;
-        }
+    using Plan = KeyPlan<T, DP>;
+    static constexpr int PARTS = WAVES == 1 ? 1 : Plan::kParts, KEYS = WAVES / PARTS * 32;
+    static constexpr bool LDSV = Plan::kValues, LDSK = Plan::kKeys;
+    // two buffers where other waves are to be waited for and registers are not short
+    static constexpr int BUFS = WAVES == 1 || Plan::kBytes > 128 ? 1 : 2;
+    struct Lds {
+        T tile[BUFS][2][RT * DP], values[LDSV ? KEYS * DP : 8], keys[LDSK ? KEYS * DP : 8];
+        float lse2[BUFS][RT], delta[BUFS][RT];
+        int ends[BUFS][RT];
     };
-    auto store = [&](int buf) {
-        qm.store(lds.tile[buf][0]);
-        dm.store(lds.tile[buf][1]);
-        if (tid < RT) {
-            lds.lse2[buf][tid] = mine.lse2 - bias;
-            lds.delta[buf][tid] = mine.delta * factor;
-            lds.ends[buf][tid] = end;
-        }
-    };
+    __device__ static __forceinline__ void run(const Attention &a, const GradShared &shared, float *part, Share sh, int block, int count, Lds &lds)
+    {
+        using L = Tile<T, DP>;
+        constexpr int KS = DP / 16, DB = DP / 32 / PARTS, RB = RT / 32, THREADS = WAVES * 64;
+        constexpr int P = kAhead<T, DP>;
+        const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), half = lane >> 5;
+        const int tiles = sh.tiles, splits = sh.splits, chunk = sh.chunk;
 
-    if (rt0 < rt1) {
-        load(rt0);
-        if (BUFS == 2) store(0);
-    }
-    for (int rt = rt0; rt < rt1; ++rt) {
-        __syncthreads();
-        const int buf = BUFS == 2 ? (rt - rt0) & 1 : 0;
-        if (BUFS == 1) {
-            store(0);
+        int w = xcd_remap(block, count);
+        const int split = w % splits;
+        w /= splits;
+        const int nh = w / tiles, tile = tiles - 1 - long_first(w - nh * tiles, tiles, a.N * a.Hkv), n = nh / a.Hkv, hk = nh - n * a.Hkv;
+        const int start = a.start(n), len = a.length(n, start), from_token = a.first_token(len, start);
+        const int group = wave / PARTS * 32 + (lane & 31), column = wave % PARTS * DB;  // the lane's key, the wave's first 32 columns
+        const int block_key = tile * KEYS, key0 = block_key + wave / PARTS * 32, key = block_key + group;
+        // rows from the first that sees the block's first key on, of this split's chunk
+        const int from = a.causal ? max(0, min(block_key - start, a.Tq)) * a.G : 0;
+        const int rt0 = max(from, split * chunk) / RT, rt1 = block_key < len ? (min(a.R, split * chunk + chunk) + RT - 1) / RT : 0;
+        if (splits > 1 && rt0 >= rt1) return;  // the join passes over it
+
+        Frag<T> k[LDSK ? 1 : KS], v[LDSV ? 1 : KS];
+        const T *kp = static_cast<const T *>(a.k.p) + n * a.k.n + key * a.k.t + hk * a.k.h;
+        const T *vp = static_cast<const T *>(a.v.p) + n * a.v.n + key * a.v.t + hk * a.v.h;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+            // a lane reads from LDS what it put there (or the other wave of its keys, behind the loop's first barrier)
+            const Frag<T> f = load_frag<T>(kp, ks * 16 + half * 8, key < len ? a.D : 0);
+            if constexpr (LDSK) L::put(lds.keys, group, ks, half, f);
+            else k[ks] = f;
+            const Frag<T> g = load_frag<T>(vp, ks * 16 + half * 8, key < len ? a.D : 0);
+            if constexpr (LDSV) L::put(lds.values, group, ks, half, g);
+            else v[ks] = g;
+        }
+        f32x16 dk[DB], dv[DB];
+#pragma unroll
+        for (int db = 0; db < DB; ++db) dk[db] = dv[db] = f32x16{};
+
+        const int shift = grad_shift<T, THREADS>(a, shared.top, nh, shared.row_blocks, shared.blocks);
+        const float bias = kHalf<T> ? float(kHalfBias) : 0.0f, c = a.scale * kLog2e;
+        const float factor = a.scale * exp2f(float(shift) - bias);
+
+        const T *qp = static_cast<const T *>(a.q.p) + n * a.q.n + hk * a.G * a.q.h;
+        const T *dp = static_cast<const T *>(a.d_o.p) + n * a.d_o.n + hk * a.G * a.d_o.h;
+        const RowStat *sp = shared.stat + int64_t(nh) * a.R;
+        Mover<T, DP, RT, THREADS> qm(tid), dm(tid);
+        RowStat mine{INFINITY, 0.0f};
+        int end = 0;
+        auto load = [&](int rt) {
+            if (a.G == 1 && rt * RT >= from_token) {
+                qm.load(qp + int64_t(rt) * RT * a.q.t, a.q.t, a.R - rt * RT, a.D);
+                dm.load(dp + int64_t(rt) * RT * a.d_o.t, a.d_o.t, a.R - rt * RT, a.D);
+            } else {
+                // rows that see nothing are zeros: what stands there takes no part
+                auto place = [&](int r, const T *p, const Strided &s) -> const T * {
+                    const int row = rt * RT + r, t = a.by_g.div(row);
+                    return row < a.R && t >= from_token ? p + t * s.t + (row - t * a.G) * s.h : nullptr;
+                };
+                qm.load(a.D, [&](int r) { return place(r, qp, a.q); });
+                dm.load(a.D, [&](int r) { return place(r, dp, a.d_o); });
+            }
+            if (tid < RT) {
+                const int row = rt * RT + tid;
+                mine = row < a.R ? sp[row] : RowStat{INFINITY, 0.0f};
+                // how many of the keys from the block's first on the row sees
+                end = row < a.R ? a.seen(len, start, a.by_g.div(row)) - block_key : 0;
+            }
+        };
+        auto store = [&](int buf) {
+            qm.store(lds.tile[buf][0]);
+            dm.store(lds.tile[buf][1]);
+            if (tid < RT) {
+                lds.lse2[buf][tid] = mine.lse2 - bias;
+                lds.delta[buf][tid] = mine.delta * factor;
+                lds.ends[buf][tid] = end;
+            }
+        };
+
+        if (rt0 < rt1) {
+            load(rt0);
+            if (BUFS == 2) store(0);
+        }
+        for (int rt = rt0; rt < rt1; ++rt) {
             __syncthreads();
-        }
-        if (rt + 1 < rt1) load(rt + 1);
-        const T *ql = lds.tile[buf][0], *dl = lds.tile[buf][1];
-        // the tile's first row sees fewest keys; rows that do not exist have P = 0
-        const bool whole = key0 + 32 <= a.seen(len, start, a.by_g.div(rt * RT));
-#pragma unroll
-        for (int rb = 0; rb < RB; ++rb) {
-            f32x16 s = {}, g = {};
-            Ahead<T, 2 * KS, P> rows;
-            auto row = [&](int i) { return L::by_rows(i < KS ? ql : dl, rb * 32 + (lane & 31), i % KS, half); };
-            rows.prime(row);
-            rows.run(row, [&](int i, const Frag<T> &f) {
-                if (i < KS) {
-                    if constexpr (LDSK) s = mma(f, L::by_rows(lds.keys, group, i, half), s);
-                    else s = mma(f, k[i], s);
-                } else {
-                    if constexpr (LDSV) g = mma(f, L::by_rows(lds.values, group, i - KS, half), g);
-                    else g = mma(f, v[i - KS], g);
-                }
-            });
-            Ahead<T, 4 * DB, P> columns;
-            auto col = [&](int i) { return L::by_columns(i & 1 ? ql : dl, rb * 32 + i / (2 * DB) * 16, column + i / 2 % DB, lane); };
-            columns.prime(col);
-#pragma unroll
-            for (int r4 = 0; r4 < 4; ++r4) {
-                const int at = rb * 32 + 8 * r4 + 4 * half;
-                const f32x4 le = *reinterpret_cast<const f32x4 *>(lds.lse2[buf] + at), de = *reinterpret_cast<const f32x4 *>(lds.delta[buf] + at);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int r = 4 * r4 + j;
-                    const float p = exp2_fast(fmaf(s[r], c, -le[j]));
-                    s[r] = p;
-                    g[r] = p * fmaf(g[r], factor, -de[j]);
-                }
+            const int buf = BUFS == 2 ? (rt - rt0) & 1 : 0;
+            if (BUFS == 1) {
+                store(0);
+                __syncthreads();
             }
-            if (!whole) {
-#pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    const bool sees = key - block_key < lds.ends[buf][rb * 32 + c_row(r, half)];
-                    s[r] = sees ? s[r] : 0.0f;
-                    g[r] = sees ? g[r] : 0.0f;
-                }
+            if (rt + 1 < rt1) load(rt + 1);
+            const T *ql = lds.tile[buf][0], *dl = lds.tile[buf][1];
+            if (WAVES > 4 && a.causal && a.seen(len, start, a.by_g.div(min(rt * RT + RT, a.R) - 1)) <= key0) {
+                // nothing of this wave's (the test costs shorter blocks more than it saves)
+                if (BUFS == 2 && rt + 1 < rt1) store(buf ^ 1);
+                continue;
             }
-            Frag<T> pf, gf;
-            columns.run(col, [&](int i, const Frag<T> &f) {
-                if (i % (2 * DB) == 0) pf = operand<T>(s, i / (2 * DB)), gf = operand<T>(g, i / (2 * DB));
-                if (i & 1) dk[i / 2 % DB] = mma(f, gf, dk[i / 2 % DB]);
-                else dv[i / 2 % DB] = mma(f, pf, dv[i / 2 % DB]);
-            });
+            // the tile's first row sees fewest keys; rows that do not exist have P = 0
+            const bool whole = key0 + 32 <= a.seen(len, start, a.by_g.div(rt * RT));
+#pragma unroll
+            for (int rb = 0; rb < RB; ++rb) {
+                f32x16 s = {}, g = {};
+                Ahead<T, 2 * KS, P> rows;
+                auto row = [&](int i) { return L::by_rows(i < KS ? ql : dl, rb * 32 + (lane & 31), i % KS, half); };
+                rows.prime(row);
+                rows.run(row, [&](int i, const Frag<T> &f) {
+                    if (i < KS) {
+                        if constexpr (LDSK) s = mma(f, L::by_rows(lds.keys, group, i, half), s);
+                        else s = mma(f, k[i], s);
+                    } else {
+                        if constexpr (LDSV) g = mma(f, L::by_rows(lds.values, group, i - KS, half), g);
+                        else g = mma(f, v[i - KS], g);
+                    }
+                });
+                Ahead<T, 4 * DB, P> columns;
+                auto col = [&](int i) { return L::by_columns(i & 1 ? ql : dl, rb * 32 + i / (2 * DB) * 16, column + i / 2 % DB, lane); };
+                columns.prime(col);
+#pragma unroll
+                for (int r4 = 0; r4 < 4; ++r4) {
+                    const int at = rb * 32 + 8 * r4 + 4 * half;
+                    const f32x4 le = *reinterpret_cast<const f32x4 *>(lds.lse2[buf] + at), de = *reinterpret_cast<const f32x4 *>(lds.delta[buf] + at);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int r = 4 * r4 + j;
+                        const float p = exp2_fast(fmaf(s[r], c, -le[j]));
+                        s[r] = p;
+                        g[r] = p * fmaf(g[r], factor, -de[j]);
+                    }
+                }
+                if (!whole) {
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) {
+                        const bool sees = key - block_key < lds.ends[buf][rb * 32 + c_row(r, half)];
+                        s[r] = sees ? s[r] : 0.0f;
+                        g[r] = sees ? g[r] : 0.0f;
+                    }
+                }
+                Frag<T> pf, gf;
+                columns.run(col, [&](int i, const Frag<T> &f) {
+                    if (i % (2 * DB) == 0) pf = operand<T>(s, i / (2 * DB)), gf = operand<T>(g, i / (2 * DB));
+                    if (i & 1) dk[i / 2 % DB] = mma(f, gf, dk[i / 2 % DB]);
+                    else dv[i / 2 % DB] = mma(f, pf, dv[i / 2 % DB]);
+                });
+            }
+            if (BUFS == 2 && rt + 1 < rt1) store(buf ^ 1);
         }
-        if (BUFS == 2 && rt + 1 < rt1) store(buf ^ 1);
+        if (key >= a.Tk) return;
+        const float undo_k = exp2f(-float(shift)), undo_v = exp2f(-bias);
+        const int64_t at = ((int64_t(n) * a.Tk + key) * a.Hkv + hk) * a.D + column * 32;
+        const int D = a.D - column * 32;
+        if (splits == 1) {
+            store_columns<T, DB>(static_cast<T *>(a.dk) + at, dk, undo_k, D, half);
+            store_columns<T, DB>(static_cast<T *>(a.dv) + at, dv, undo_v, D, half);
+        } else {
+            const int64_t all = int64_t(a.N) * a.Tk * a.Hkv * a.D;
+            float *to = part + int64_t(split) * 2 * all + at;
+            store_columns<float, DB>(to, dk, undo_k, D, half);
+            store_columns<float, DB>(to + all, dv, undo_v, D, half);
+        }
     }
-    if (key >= a.Tk) return;
-    const float undo_k = exp2f(-float(shift)), undo_v = exp2f(-bias);
-    const int64_t at = ((int64_t(n) * a.Tk + key) * a.Hkv + hk) * a.D + column * 32;
-    const int D = a.D - column * 32;
-    if (splits == 1) {
-        store_columns<T, DB>(static_cast<T *>(a.dk) + at, dk, undo_k, D, half);
-        store_columns<T, DB>(static_cast<T *>(a.dv) + at, dv, undo_v, D, half);
-    } else {
-        const int64_t all = int64_t(a.N) * a.Tk * a.Hkv * a.D;
-        float *to = part + int64_t(split) * 2 * all + at;
-        store_columns<float, DB>(to, dk, undo_k, D, half);
-        store_columns<float, DB>(to + all, dv, undo_v, D, half);
-    }
-}
 };
 
 // dq of a block of rows, a wave 32 of them, from KT keys at a time.
 template <class T, int DP, int WAVES, int KT>
 struct RowGrad {
-static constexpr int BUFS = WAVES == 1 ? 1 : 2;
-struct Lds {
-    T tile[BUFS][2][KT * DP];
-};
-__device__ static __forceinline__ void run(const Attention &a, const GradShared &shared, float *part, Share sh, int block, int count, Lds &lds)
-{
-    using L = Tile<T, DP>;
-    constexpr int KS = DP / 16, DB = DP / 32, KB = KT / 32, THREADS = WAVES * 64, ROWS = WAVES * 32, P = DP * sizeof(T) > 128 ? 2 : 4;  // operands asked for ahead: registers are short in long heads
-    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), half = lane >> 5;
-    const int tiles = sh.tiles, splits = sh.splits, chunk = sh.chunk;
-
-    int w = xcd_remap(block, count);
-    const int split = w % splits;
-    w /= splits;
-    const int nh = w / tiles, tile = long_first(w - nh * tiles, tiles, a.N * a.Hkv), n = nh / a.Hkv, hk = nh - n * a.Hkv;
-    const int start = a.start(n), len = a.length(n, start), from_token = a.first_token(len, start);
-    const int block_row = tile * ROWS, row0 = block_row + wave * 32;
-    // keys the block looks at, of this split's chunk
-    const int want = min(a.seen(len, start, a.by_g.div(min(block_row + ROWS, a.R) - 1)), split * chunk + chunk);
-    const int kt0 = split * chunk / KT, kt1 = (want + KT - 1) / KT;
-    if (splits > 1 && kt0 >= kt1) return;  // the join passes over it
-
-    const int shift = grad_shift<T, THREADS>(a, shared.top, nh, shared.row_blocks, shared.blocks);
-    const float bias = kHalf<T> ? float(kHalfBias) : 0.0f, c = a.scale * kLog2e;
-    const float factor = a.scale * exp2f(float(shift) - bias);
-
-    const int row = row0 + (lane & 31), t = a.by_g.div(row), h = hk * a.G + row - t * a.G;
-    const bool sees = row < a.R && t >= from_token;
-    const int seen = sees ? a.seen(len, start, t) : 0;
-    const RowStat mine = row < a.R ? shared.stat[int64_t(nh) * a.R + row] : RowStat{INFINITY, 0.0f};
-    const float lse2 = mine.lse2 - bias, delta = mine.delta * factor;
-    Frag<T> q[KS], d_o[KS];
-    const T *qp = static_cast<const T *>(a.q.p) + n * a.q.n + t * a.q.t + h * a.q.h;
-    const T *dp = static_cast<const T *>(a.d_o.p) + n * a.d_o.n + t * a.d_o.t + h * a.d_o.h;
-#pragma unroll
-    for (int ks = 0; ks < KS; ++ks) {
-        q[ks] = load_frag<T>(qp, ks * 16 + half * 8, sees ? a.D : 0);
-        d_o[ks] = load_frag<T>(dp, ks * 16 + half * 8, sees ? a.D : 0);
-    }
-    const bool rows = row0 < a.R;
-    const int whole = rows ? a.seen(len, start, a.by_g.div(row0)) / KT : 0;
-    const int none = rows ? (a.seen(len, start, a.by_g.div(min(row0 + 32, a.R) - 1)) + KT - 1) / KT : 0;
-
-    const T *kp = static_cast<const T *>(a.k.p) + n * a.k.n + hk * a.k.h;
-    const T *vp = static_cast<const T *>(a.v.p) + n * a.v.n + hk * a.v.h;
-    Mover<T, DP, KT, THREADS> km(tid), vm(tid);
-    auto load = [&](int kt) {
-        km.load(kp + int64_t(kt) * KT * a.k.t, a.k.t, len - kt * KT, a.D);
-        vm.load(vp + int64_t(kt) * KT * a.v.t, a.v.t, len - kt * KT, a.D);
+    static constexpr int BUFS = WAVES == 1 ? 1 : 2;
+    struct Lds {
+        T tile[BUFS][2][KT * DP];
     };
-    f32x16 dq[DB];
-#pragma unroll
-    for (int db = 0; db < DB; ++db) dq[db] = f32x16{};
+    __device__ static __forceinline__ void run(const Attention &a, const GradShared &shared, float *part, Share sh, int block, int count, Lds &lds)
+    {
+        using L = Tile<T, DP>;
+        constexpr int KS = DP / 16, DB = DP / 32, KB = KT / 32, THREADS = WAVES * 64, ROWS = WAVES * 32;
+        constexpr int P = kAhead<T, DP>;
+        const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), half = lane >> 5;
+        const int tiles = sh.tiles, splits = sh.splits, chunk = sh.chunk;
 
-    auto store = [&](int buf) {
-        km.store(lds.tile[buf][0]);
-        vm.store(lds.tile[buf][1]);
-    };
-    if (kt0 < kt1) {
-        load(kt0);
-        if (BUFS == 2) store(0);
-    }
-    for (int kt = kt0; kt < kt1; ++kt) {
-        __syncthreads();
-        const int buf = BUFS == 2 ? (kt - kt0) & 1 : 0;
-        if (BUFS == 1) {
-            store(0);
+        int w = xcd_remap(block, count);
+        const int split = w % splits;
+        w /= splits;
+        const int nh = w / tiles, tile = long_first(w - nh * tiles, tiles, a.N * a.Hkv), n = nh / a.Hkv, hk = nh - n * a.Hkv;
+        const int start = a.start(n), len = a.length(n, start), from_token = a.first_token(len, start);
+        const int block_row = tile * ROWS, row0 = block_row + wave * 32;
+        // keys the block looks at, of this split's chunk
+        const int want = min(a.seen(len, start, a.by_g.div(min(block_row + ROWS, a.R) - 1)), split * chunk + chunk);
+        const int kt0 = split * chunk / KT, kt1 = (want + KT - 1) / KT;
+        if (splits > 1 && kt0 >= kt1) return;  // the join passes over it
+
+        const int shift = grad_shift<T, THREADS>(a, shared.top, nh, shared.row_blocks, shared.blocks);
+        const float bias = kHalf<T> ? float(kHalfBias) : 0.0f, c = a.scale * kLog2e;
+        const float factor = a.scale * exp2f(float(shift) - bias);
+
+        const int row = row0 + (lane & 31), t = a.by_g.div(row), h = hk * a.G + row - t * a.G;
+        const bool sees = row < a.R && t >= from_token;
+        const int seen = sees ? a.seen(len, start, t) : 0;
+        const RowStat mine = row < a.R ? shared.stat[int64_t(nh) * a.R + row] : RowStat{INFINITY, 0.0f};
+        const float lse2 = mine.lse2 - bias, delta = mine.delta * factor;
+        Frag<T> q[KS], d_o[KS];
+        const T *qp = static_cast<const T *>(a.q.p) + n * a.q.n + t * a.q.t + h * a.q.h;
+        const T *dp = static_cast<const T *>(a.d_o.p) + n * a.d_o.n + t * a.d_o.t + h * a.d_o.h;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+            q[ks] = load_frag<T>(qp, ks * 16 + half * 8, sees ? a.D : 0);
+            d_o[ks] = load_frag<T>(dp, ks * 16 + half * 8, sees ? a.D : 0);
+        }
+        const bool rows = row0 < a.R;
+        const int whole = rows ? a.seen(len, start, a.by_g.div(row0)) / KT : 0;
+        const int none = rows ? (a.seen(len, start, a.by_g.div(min(row0 + 32, a.R) - 1)) + KT - 1) / KT : 0;
+
+        const T *kp = static_cast<const T *>(a.k.p) + n * a.k.n + hk * a.k.h;
+        const T *vp = static_cast<const T *>(a.v.p) + n * a.v.n + hk * a.v.h;
+        Mover<T, DP, KT, THREADS> km(tid), vm(tid);
+        auto load = [&](int kt) {
+            km.load(kp + int64_t(kt) * KT * a.k.t, a.k.t, len - kt * KT, a.D);
+            vm.load(vp + int64_t(kt) * KT * a.v.t, a.v.t, len - kt * KT, a.D);
+        };
+        f32x16 dq[DB];
+#pragma unroll
+        for (int db = 0; db < DB; ++db) dq[db] = f32x16{};
+
+        auto store = [&](int buf) {
+            km.store(lds.tile[buf][0]);
+            vm.store(lds.tile[buf][1]);
+        };
+        if (kt0 < kt1) {
+            load(kt0);
+            if (BUFS == 2) store(0);
+        }
+        for (int kt = kt0; kt < kt1; ++kt) {
             __syncthreads();
-        }
-        if (kt + 1 < kt1) load(kt + 1);
-        if (kt < none) {
-            const T *kl = lds.tile[buf][0], *vl = lds.tile[buf][1];
-#pragma unroll
-            for (int kb = 0; kb < KB; ++kb) {
-                f32x16 s = {}, g = {};
-                Ahead<T, 2 * KS, P> rows;
-                auto row = [&](int i) { return L::by_rows(i < KS ? kl : vl, kb * 32 + (lane & 31), i % KS, half); };
-                rows.prime(row);
-                rows.run(row, [&](int i, const Frag<T> &f) {
-                    if (i < KS) s = mma(f, q[i], s);
-                    else g = mma(f, d_o[i - KS], g);
-                });
-                Ahead<T, 2 * DB, P> columns;
-                auto col = [&](int i) { return L::by_columns(kl, kb * 32 + i / DB * 16, i % DB, lane); };
-                columns.prime(col);
-#pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    const float p = exp2_fast(fmaf(s[r], c, -lse2));
-                    g[r] = p * fmaf(g[r], factor, -delta);
-                }
-                if (kt >= whole) {
-                    const int end = seen - kt * KT;
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) g[r] = kb * 32 + c_row(r, half) < end ? g[r] : 0.0f;
-                }
-                Frag<T> gf;
-                columns.run(col, [&](int i, const Frag<T> &f) {
-                    if (i % DB == 0) gf = operand<T>(g, i / DB);
-                    dq[i % DB] = mma(f, gf, dq[i % DB]);
-                });
+            const int buf = BUFS == 2 ? (kt - kt0) & 1 : 0;
+            if (BUFS == 1) {
+                store(0);
+                __syncthreads();
             }
+            if (kt + 1 < kt1) load(kt + 1);
+            if (kt < none) {
+                const T *kl = lds.tile[buf][0], *vl = lds.tile[buf][1];
+#pragma unroll
+                for (int kb = 0; kb < KB; ++kb) {
+                    f32x16 s = {}, g = {};
+                    Ahead<T, 2 * KS, P> rows;
+                    auto row = [&](int i) { return L::by_rows(i < KS ? kl : vl, kb * 32 + (lane & 31), i % KS, half); };
+                    rows.prime(row);
+                    rows.run(row, [&](int i, const Frag<T> &f) {
+                        if (i < KS) s = mma(f, q[i], s);
+                        else g = mma(f, d_o[i - KS], g);
+                    });
+                    Ahead<T, 2 * DB, P> columns;
+                    auto col = [&](int i) { return L::by_columns(kl, kb * 32 + i / DB * 16, i % DB, lane); };
+                    columns.prime(col);
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) {
+                        const float p = exp2_fast(fmaf(s[r], c, -lse2));
+                        g[r] = p * fmaf(g[r], factor, -delta);
+                    }
+                    if (kt >= whole) {
+                        const int end = seen - kt * KT;
+#pragma unroll
+                        for (int r = 0; r < 16; ++r) g[r] = kb * 32 + c_row(r, half) < end ? g[r] : 0.0f;
+                    }
+                    Frag<T> gf;
+                    columns.run(col, [&](int i, const Frag<T> &f) {
+                        if (i % DB == 0) gf = operand<T>(g, i / DB);
+                        dq[i % DB] = mma(f, gf, dq[i % DB]);
+                    });
+                }
+            }
+            if (BUFS == 2 && kt + 1 < kt1) store(buf ^ 1);
         }
-        if (BUFS == 2 && kt + 1 < kt1) store(buf ^ 1);
+        if (row >= a.R) return;
+        const float undo = exp2f(-float(shift));
+        const int64_t at = ((int64_t(n) * a.Tq + t) * a.H + h) * a.D;
+        if (splits == 1) store_columns<T, DB>(static_cast<T *>(a.dq) + at, dq, undo, a.D, half);
+        else store_columns<float, DB>(part + int64_t(split) * a.N * a.Tq * a.H * a.D + at, dq, undo, a.D, half);
     }
-    if (row >= a.R) return;
-    const float undo = exp2f(-float(shift));
-    const int64_t at = ((int64_t(n) * a.Tq + t) * a.H + h) * a.D;
-    if (splits == 1) store_columns<T, DB>(static_cast<T *>(a.dq) + at, dq, undo, a.D, half);
-    else store_columns<float, DB>(part + int64_t(split) * a.N * a.Tq * a.H * a.D + at, dq, undo, a.D, half);
-}
 };
 
 // The kernels: each kind of block by itself, or, for small calls, both in one launch.
@@ -521,7 +535,7 @@ void launch_attend_grad(const Attention &a, const AttendGradPlan &p, char *ws, h
                 return;
             }
         }
-        if (key_count) key_grad_kernel<T, DP, 4, TILE><<<unsigned(key_count), 256, 0, st>>>(a, shared, key_part, keys);
+        if (key_count) key_grad_kernel<T, DP, KeyPlan<T, DP>::kWaves, TILE><<<unsigned(key_count), KeyPlan<T, DP>::kWaves * 64, 0, st>>>(a, shared, key_part, keys);
         if (row_count) row_grad_kernel<T, DP, 4, TILE><<<unsigned(row_count), 256, 0, st>>>(a, shared, row_part, rows);
     });
     const int key_tokens = p.row_splits > 1 ? a.N * a.Tk : 0, row_tokens = p.key_splits > 1 ? a.N * a.Tq : 0;
