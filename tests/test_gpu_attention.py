@@ -109,6 +109,23 @@ def test_backward(T, shape, dtype):
     check_backward(T, dtype, tensors, arrays, seen, None, str(shape), causal=causal, lengths=ints(lengths), starts=ints(starts))
 
 
+# calls that fill the chip: blocks of several waves, in one piece and split over rows and keys
+LARGE = [
+    (8, 150, 140, 16, 16, 64, True, (140, 3, 0, 77, 140, 64, 65, 139), None),
+    (3, 530, 540, 22, 11, 128, True, None, (10, 300, -40)),
+    (2, 300, 700, 48, 24, 96, False, (700, 401), None),
+    (16, 257, 129, 8, 8, 33, True, None, None),          # the first 128 tokens see nothing
+    (1, 260, 520, 66, 66, 120, True, None, None),
+]
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("shape", LARGE, ids=[str(s[:6]) for s in LARGE])
+def test_large(T, shape, dtype):
+    test_forward(T, shape, dtype)
+    test_backward(T, shape, dtype)
+
+
 def test_layouts(T):
     """Parts of one projection, heads in front of tokens, and repeated keys."""
     n, t, h, hk, d = 2, 90, 4, 2, 40
