@@ -537,14 +537,15 @@ ct_status embedding_workspace_size(int64_t tokens, int64_t rows, int64_t width, 
  *   *_strides      strides in elements of a tensor's image, token and head axes, in that order;
  *                  a head's D elements are dense.  So q, k and v may be parts of one
  *                  projection, a cache of more tokens than are seen, or repeated (stride 0)
- *   scale          positive and finite
+ *   scale          positive, at most 1e38
  *   causal         0 or 1
  *   lengths        device array of N int32, or NULL (kv_tokens); taken as 0 below 0 and as
  *                  kv_tokens above it
  *   starts         device array of N int32: the place of the first query among the keys; NULL:
  *                  kv_tokens - Tq.  For causal calls only.  A serving step gives lengths (with the
  *                  new tokens) and starts = lengths - Tq
- *   out, lse       dense (N, Tq, H, D) of dtype and (N, H, Tq) of float32
+ *   out, lse       dense (N, Tq, H, D) of dtype and (N, H, Tq) of float32, not overlapping
+ *                  anything else
  *   workspace      as for group_norm_nd (attention_workspace_size bytes)
  * Validation comes first: on any error nothing is launched and the outputs are untouched.  With
  * no tokens at all nothing is written.  The same inputs give the same bits.
@@ -595,7 +596,8 @@ ct_status attention_workspace_size(ct_dtype dtype, const int64_t *q_shape, int64
  *   axes           1..4; R <= 256, 2 R <= D
  *   base           positive and finite
  *   interleaved    0: pair p is (p, p + R); 1: (2 p, 2 p + 1)
- * Angles are exact to 2^-32 of a turn at positions up to 2^31 in magnitude.
+ * Angles are right to 2^-24 of a turn for bases of 1 and more and positions up to 2^31 in
+ * magnitude.
  */
 ct_status rotary_nd(ct_dtype dtype, const int64_t *shape, const void *x, const int64_t *x_strides, ct_dtype position_dtype,
                     int axes, const void *positions, const int64_t *position_strides, const int64_t *sections, double base,
@@ -617,7 +619,8 @@ ct_status rotary_nd(ct_dtype dtype, const int64_t *shape, const void *x, const i
  *   copy_dtype     type of the copies: CT_FLOAT16 or CT_BFLOAT16 (any value without copies)
  *   lr, grad_scale, step   host values; lr_device, grad_scale_device (one float32) and step_device (one int64)
  *                  are read when the kernels run and take their place, or NULL.  step counts from 1
- *   beta1, beta2   in [0, 1); eps finite, not negative
+ *   lr, grad_scale finite as float32
+ *   beta1, beta2   in [0, 1); eps 0, or 1e-30 .. 1e30
  * Tensors are dense and must not overlap; one of count 0 is passed over.  The list may be freed
  * after the call: a captured graph keeps its own copy.
  */

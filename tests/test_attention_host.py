@@ -86,6 +86,14 @@ def _rotary(T, dtype=1, shape=(2, 3, 4, 16), x=P, xs=(192, 64, 16), ptype=5, axe
                                       i(ys), None)
 
 
+def test_scales_and_rates_that_leave_float32(T):
+    # 2e38 log2(e), and the reciprocal of a denormal eps, are infinite
+    assert _forward(T, scale=2e38) == 1 and _backward(T, scale=2e38) == 1
+    for kw in (dict(eps=1e-40), dict(eps=1e31), dict(lr=1e39), dict(lr=-1e39), dict(scale=1e39)):
+        assert _adamw(T, **kw) == 1, kw
+    assert _adamw(T, eps=0.0, entry=dict(count=0)) == 0 and _adamw(T, eps=1e-30, entry=dict(count=0)) == 0
+
+
 def test_rotary_refusals(T):
     bad = [(dict(dtype=2), 3), (dict(dtype=7), 3), (dict(ptype=0), 3), (dict(shape=None), 1), (dict(sections=None), 1), (dict(xs=None), 1),
            (dict(axes=0), 1), (dict(axes=5, sections=(1,) * 5), 1), (dict(shape=(2, 3, 4, -1)), 1), (dict(sections=(3, -1)), 1),

@@ -906,8 +906,8 @@ def _attention_args(q, k, v, scale, causal, lengths, starts):
     if k.shape[2] < 1 or q.shape[2] < 1 or q.shape[2] % k.shape[2]:
         raise ConvTransposeError(1, "q's heads must be a multiple of k's")
     scale = q.shape[3] ** -0.5 if scale is None and q.shape[3] else scale
-    if scale is None or not 0.0 < float(scale) < 3e38:
-        raise ConvTransposeError(1, "scale must be positive and finite")
+    if scale is None or not 0.0 < float(scale) <= 1e38:
+        raise ConvTransposeError(1, "scale must lie in (0, 1e38]")
     if starts is not None and not causal:
         raise ConvTransposeError(1, "starts are for causal calls")
     for name, t in (("lengths", lengths), ("starts", starts)):
@@ -956,6 +956,8 @@ def attention_nd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, scale: Op
     sizes, operands, mask = _attention_args(q, k, v, scale, causal, lengths, starts)
     nbytes = _attention_workspace(sizes, False) if _prepare_only else 0
     with _on(stream):
+        if out is not None and out.numel() and out.data_ptr() in (q.data_ptr(), k.data_ptr(), v.data_ptr()):
+            raise ConvTransposeError(1, "out must not be one of the inputs")
         out = _dense_like("out", out, q)
         lse = torch.empty((q.shape[0], q.shape[2], q.shape[1]), dtype=torch.float32, device=q.device)
         ws, wsb = _scratch(nbytes, q.device, _prepare_only)
@@ -1120,8 +1122,9 @@ def adamw_nd(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], ms: 
 class PreparedCall:
     """One call of ``convolution_nd``, ``qlinear_convtranspose_nd``, ``group_norm_nd``,
     ``group_norm_backward_nd``, ``dropout_nd``, ``embedding_nd``, ``embedding_backward_nd``,
-    ``attention_nd``, ``attention_backward_nd``, ``rotary_nd`` or ``adamw_nd`` with its arguments validated and marshalled once (and its
-    workspace, where it takes one, allocated): ``PreparedCall(convolution_nd, x, w, ...)``
+    ``attention_nd``, ``attention_backward_nd``, ``rotary_nd`` or ``adamw_nd`` with its
+    arguments validated and marshalled once (and its workspace, where it takes one,
+    allocated): ``PreparedCall(convolution_nd, x, w, ...)``
     takes the function's own arguments; each call then enqueues the operation with a single
     C call, writing the same output tensors (``.out``).  Repeated calls must be ordered on
     one stream; the tensors must outlive the object."""

@@ -317,9 +317,10 @@ extern "C" ct_status adamw_nd(ct_dtype dtype, ct_dtype grad_dtype, int state_bit
     if (state_bits != 8 && state_bits != 32) return fail(CT_EUNSUPPORTED, "state_bits must be 8 or 32");
     if (tensors < 0) return fail(CT_EINVAL, "the number of tensors must not be negative");
     if (tensors && !list) return fail(CT_EINVAL, "the list of tensors is NULL");
-    if (!std::isfinite(lr) || !std::isfinite(grad_scale)) return fail(CT_EINVAL, "lr and grad_scale must be finite");
+    if (!std::isfinite(float(lr)) || !std::isfinite(float(grad_scale))) return fail(CT_EINVAL, "lr and grad_scale must be finite");
     if (!(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0)) return fail(CT_EINVAL, "the betas must lie in [0, 1)");
-    if (!(eps >= 0.0) || !std::isfinite(eps)) return fail(CT_EINVAL, "eps must be finite and not negative");
+    // (the update's reciprocal takes no denormal number)
+    if (!(eps == 0.0 || (eps >= 1e-30 && eps <= 1e30))) return fail(CT_EINVAL, "eps must be 0 or lie in 1e-30 .. 1e30");
     if (!step_device && step < 1) return fail(CT_EINVAL, "step counts from 1");
     if (!ct::aligned_to(step_device, 8) || !ct::aligned_to(lr_device, 4) || !ct::aligned_to(grad_scale_device, 4))
         return fail(CT_EINVAL, "device scalars must be aligned to their size");

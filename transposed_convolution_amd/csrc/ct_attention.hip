@@ -124,8 +124,8 @@ ct_status sizes(int dt, const int64_t *q_shape, int64_t tk, int64_t kv_heads, At
 
 ct_status options(float scale, const int32_t *lengths, int causal, const int32_t *starts, Attention *a, std::string *err)
 {
-    if (!(scale > 0.0f && scale <= 3.0e38f)) {
-        *err = "scale must be positive and finite";
+    if (!(scale > 0.0f && scale <= 1.0e38f)) {  // times log2(e) it still is a float32
+        *err = "scale must lie in (0, 1e38]";
         return CT_EINVAL;
     }
     if (causal != 0 && causal != 1) {
