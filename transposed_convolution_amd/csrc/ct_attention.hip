@@ -19,12 +19,15 @@ AttendPlan attend_plan(const Attention &a, int dtype)
     const int64_t heads = int64_t(a.N) * a.Hkv;
     p.few = a.R <= 32;
     p.tiles = p.few ? 1 : int(ceil_div(a.R, 128));
-    // Blocks wanted before a call's work is split over its keys (and joined by a second kernel), and
-    // the keys a split should have: float32 products take 16 times as long.
+    // Blocks wanted before a call's work is split over its keys (and joined by a second kernel: 4 us), and the keys a
+    // split should have.  Few rows, 8 heads over 4 of 64: 200 keys took 7.2 us in one block a head and 9.5 split, 4096
+    // keys 10.9 in splits of 128 and 13.7 in splits of 512.  Many rows: a chunk is to outweigh its part of the output, and
+    // float32 products take 8 times as long (5 heads of 40, 77 rows, 1001 keys, float32: 28.6 us whole, 15 in 9 parts).
     const int64_t base = heads * p.tiles, wanted = p.few && padded_head(a.D) * float_size(dtype) > 256 ? 256 : 512,
                   least = p.few ? 128 : dtype == CT_FLOAT32 ? 64 : 256;
     int64_t splits = 1;
-    if (base > 0 && base < wanted && !(p.few && a.Tk <= 512)) splits = std::max<int64_t>(1, std::min({ceil_div(wanted, base), ceil_div(a.Tk, least), int64_t(kMostSplits)}));
+    if (base > 0 && base < wanted && !(p.few && a.Tk <= 512))
+        splits = std::max<int64_t>(1, std::min({ceil_div(wanted, base), ceil_div(a.Tk, least), int64_t(kMostSplits)}));
     // chunks are whole steps of a block
     const int64_t step = p.few ? 128 : 64;
     p.chunk = int(splits > 1 ? ceil_div(ceil_div(a.Tk, splits), step) * step : std::max(1, a.Tk));
@@ -37,8 +40,9 @@ AttendGradPlan attend_grad_plan(const Attention &a, int dtype)
 {
     AttendGradPlan p;
     const int64_t heads = int64_t(a.N) * a.Hkv;
-    // Blocks of 4 waves share what they read, blocks of one wave make more of a small call: those
-    // are taken where 4-wave blocks, split as far as is sensible, would not fill the chip.
+    // Blocks of several waves share what they read, blocks of one wave make more of a small call: those
+    // are taken where the former, split as far as is sensible, would not fill the chip (4 x 257 tokens, 3 heads of 36,
+    // float32: 116 us with 4 waves, 44.6 with one).
     const size_t bytes = padded_head(a.D) * float_size(dtype);
     const int64_t most = std::max(a.Tk, a.R);
     const bool fills = heads * ceil_div(most, 128) * std::max<int64_t>(1, std::min<int64_t>(a.Tk, a.R) / 512) >= 256;

@@ -183,13 +183,22 @@ __device__ __forceinline__ void finish_rows(const Attention &a, float *part, int
 }
 
 // A wave holds 32 rows, a block goes through the keys KT at a time; the next tile is on its way while one
-// is worked on.
+// is worked on.  8 x 4096 tokens, 8 heads of 64, float16: 405 us, 680 TFLOP/s; 2 x 8191 causal tokens, 16 heads over 4
+// of 128, bfloat16: 685 us, 800 TFLOP/s; heads of 256, 2 x 4096 tokens, 4 heads, float16: 350 us, 390 TFLOP/s (one
+// wave a SIMD).  Bound by the vector unit beside the matrix unit: a score takes 6 vector instructions, one of them the
+// exponential at a half of their rate, and heads of 64 only 16 cycles of a matrix instruction a row of 32; the two are busy
+// 58 and 30 % of the time (heads of 128: 45 and 34 %), and waves wait for each other's results in between.
+// Other cuts, us for the first and the second call (438 and 695 then): 64 rows a wave 408 and 1112, 32 keys a tile 452 and
+// 835, 128 keys 427 and 1144, 8 waves a block 500 and 738, three buffers 469 and 1140.  Three waves a SIMD
+// (168 registers) took heads of 64 from 521 to 441.
 template <class T, int DP, int WAVES, int KT>
-__global__ __launch_bounds__(WAVES * 64, DP * sizeof(T) <= 128 ? 3 : DP * sizeof(T) <= 256 ? 2 : 1) void attend_kernel(Attention a, float *part, int tiles, int splits, int chunk)
+__global__ __launch_bounds__(WAVES * 64, DP * sizeof(T) <= 128 ? 3 : DP * sizeof(T) <= 256 ? 2 : 1) void attend_kernel(
+    Attention a, float *part, int tiles, int splits, int chunk)
 {
     using L = Tile<T, DP>;
     constexpr int KS = DP / 16, DB = DP / 32, KB = KT / 32, THREADS = WAVES * 64, ROWS = WAVES * 32;
-    constexpr int P = 4;  // operands asked for ahead
+    // Operands asked for ahead: heads of 128 took 727 us without, 699, 692, 687 and 690 with 2, 3, 4 and 6.
+    constexpr int P = 4;
     __shared__ __attribute__((aligned(16))) T lds[2][2][KT * DP];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), half = lane >> 5;
 
@@ -272,8 +281,10 @@ __global__ __launch_bounds__(WAVES * 64, DP * sizeof(T) <= 128 ? 3 : DP * sizeof
 }
 
 // Up to 32 rows a key head (a token or a few over a cache): every wave takes 32 keys of its own at a
-// time, through LDS of its own, and the block's waves are joined at the end.  Bound by memory and its
-// latency: nothing waits for another wave on the way.
+// time, through LDS of its own, and the block's waves are joined at the end.  Nothing waits for another wave
+// on the way.  One token, 4 images of up to 32768 keys, 16 heads over 4 of 128, bfloat16: 45 us with the join,
+// 2.9 TB/s of the keys and values that are seen.  Bound by latency in short calls: 8 images of up to 4096 keys,
+// 8 heads over 2 of 64, take 7.4 us for the chain length, keys, scores, values, join of waves, and 4 for the join of splits.
 template <class T, int DP, int WAVES>
 __global__ __launch_bounds__(WAVES * 64, DP * sizeof(T) <= 256 ? 2 : 1) void attend_few_kernel(Attention a, float *part, int splits, int chunk)
 {
@@ -383,8 +394,9 @@ __global__ __launch_bounds__(WAVES * 64, DP * sizeof(T) <= 256 ? 2 : 1) void att
 }
 
 // The splits of a row, a block a row: weights 2^(m - largest m).  A lane reads the statistics of one split; the
-// waves (one for a few splits, four for many) take the parts in turn, 8 asked for at a time.  Chunks that a block of `span` rows had nothing of
-// are passed over.
+// waves (one for a few splits, four for many) take the parts in turn, 8 asked for at a time.  Chunks that a block of
+// `span` rows had nothing of are passed over.  A launch and two dependent reads: 4 us for 64 rows of 32 parts, 5 for 1155
+// rows of 9.
 template <class T, int C, int WAVES>
 __global__ __launch_bounds__(WAVES * 64) void attend_join_kernel(Attention a, float *part, int splits, int chunk, int span)
 {
@@ -454,10 +466,11 @@ void launch_attend(const Attention &a, const AttendPlan &p, float *part, hipStre
     with_head(a.D, [&](auto head) {
         constexpr int DP = decltype(head)::value, KT = DP * sizeof(T) > 256 ? 32 : 64, C = (DP + 63) / 64;
         constexpr int FW = DP * sizeof(T) > 512 ? 2 : 4;  // their tiles fit LDS
+        const int span = p.few ? 32 : 128;
         if (p.few) attend_few_kernel<T, DP, FW><<<unsigned(heads * p.splits), FW * 64, 0, st>>>(a, part, p.splits, p.chunk);
         else attend_kernel<T, DP, 4, KT><<<unsigned(heads * p.tiles * p.splits), 256, 0, st>>>(a, part, p.tiles, p.splits, p.chunk);
-        if (p.splits > 16) attend_join_kernel<T, C, 4><<<unsigned(heads * a.R), 256, 0, st>>>(a, part, p.splits, p.chunk, p.few ? 32 : 128);
-        else if (p.splits > 1) attend_join_kernel<T, C, 1><<<unsigned(heads * a.R), 64, 0, st>>>(a, part, p.splits, p.chunk, p.few ? 32 : 128);
+        if (p.splits > 16) attend_join_kernel<T, C, 4><<<unsigned(heads * a.R), 256, 0, st>>>(a, part, p.splits, p.chunk, span);
+        else if (p.splits > 1) attend_join_kernel<T, C, 1><<<unsigned(heads * a.R), 64, 0, st>>>(a, part, p.splits, p.chunk, span);
     });
 }
 

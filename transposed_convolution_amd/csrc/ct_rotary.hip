@@ -39,7 +39,11 @@ struct Rotary {
     uint64_t turn[PAIRS];
 };
 
-// One thread keeps the sines and cosines of V pairs of one token and turns them in `head_run` heads.
+// One thread keeps the sines and cosines of V pairs of one token and turns them in `head_run` heads.  Bound by memory
+// where there is much: 2 x 16384 tokens, 20 heads of 128, bfloat16, 336 MB in 75 us, 4.5 TB/s, where a copy of as many
+// bytes runs at 5.4; a token of 8 sequences, 10 heads of 64: 5.4 us, a launch whose arguments hold the table (4.4 for
+// one without) and a chain of position, sine and store.  One head a thread makes the sines
+// again for each.
 template <class T, class I, bool BY_TWOS, int PAIRS>
 __global__ __launch_bounds__(kThreads) void rotary_kernel(Rotary<PAIRS> a)
 {
