@@ -286,6 +286,21 @@ def test_empty_sides(T):
     assert out.shape == none.shape and not dk.any() and not dv.any()
 
 
+def test_out_is_not_an_input(T):
+    x = torch.ones((2, 3, 4, 8), device="cuda")
+    for k, out in (((x + 1), x), (x, x)):
+        with pytest.raises(T.ConvTransposeError, match="one of the inputs"):
+            T.attention_nd(x, k, k, out=out)
+    with pytest.raises(T.ConvTransposeError, match="one of the inputs"):
+        T.attention_nd(x + 1, x, x + 2, out=x)
+    with pytest.raises(T.ConvTransposeError, match="scale"):
+        T.attention_nd(x, x, x, scale=2e38)
+    # the largest scale keeps the formula: scores of 0 weigh alike (lse: 8 roundings of log 3 are 5.3e-7)
+    out, lse = T.attention_nd(torch.zeros_like(x), x, x, scale=1e38)
+    torch.cuda.synchronize()
+    assert torch.equal(out, x) and bool((lse - np.log(3.0)).abs().max() < 5.3e-7)
+
+
 def test_long_cache(T):
     """Keys more than 2^31 elements from the first: two million tokens of 8 heads of 128."""
     tk, hk, d = (1 << 21) + 70, 8, 128

@@ -186,8 +186,9 @@ __device__ __forceinline__ void finish_rows(const Attention &a, float *part, int
 // is worked on.  8 x 4096 tokens, 8 heads of 64, float16: 405 us, 680 TFLOP/s; 2 x 8191 causal tokens, 16 heads over 4
 // of 128, bfloat16: 685 us, 800 TFLOP/s; heads of 256, 2 x 4096 tokens, 4 heads, float16: 350 us, 390 TFLOP/s (one
 // wave a SIMD).  Bound by the vector unit beside the matrix unit: a score takes 6 vector instructions, one of them the
-// exponential at a half of their rate, and heads of 64 only 16 cycles of a matrix instruction a row of 32; the two are busy
-// 58 and 30 % of the time (heads of 128: 45 and 34 %), and waves wait for each other's results in between.
+// exponential at a half of their rate, so that 32 x 32 scores take 500 cycles of them and, with heads of 64, 256 of matrix
+// instructions; the two are busy 60 and 30 % of the time (heads of 128: 44 and 34 %), the rest is steps that wait for
+// the one before.
 // Other cuts, us for the first and the second call (438 and 695 then): 64 rows a wave 408 and 1112, 32 keys a tile 452 and
 // 835, 128 keys 427 and 1144, 8 waves a block 500 and 738, three buffers 469 and 1140.  Three waves a SIMD
 // (168 registers) took heads of 64 from 521 to 441.
