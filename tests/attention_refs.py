@@ -72,8 +72,10 @@ def attend(q, k, v, scale, seen, dtype):
     return (out.transpose(0, 2, 1, 3), lse), (tol.transpose(0, 2, 1, 3), lse_tol)
 
 
-def attend_grad(do, q, k, v, out, lse, scale, seen, dtype):
-    """The gradient from out and lse as they are given.  Returns (dq, dk, dv) and a bound on each's error."""
+def attend_grad(do, q, k, v, out, lse, scale, seen, dtype, least=None):
+    """The gradient from out and lse as they are given.  Returns (dq, dk, dv) and a bound on each's error.  `least`:
+    what float16 score gradients below its normal range may be off by, in the sums for dq and for dk, where the
+    largest of all rows says too little."""
     n, tq, h, d = q.shape
     tk, hk = k.shape[1], k.shape[2]
     k, v = _where(seen, k, v)
@@ -89,15 +91,17 @@ def attend_grad(do, q, k, v, out, lse, scale, seen, dtype):
     ds = scale * p * (dp - delta)
     parts = np.matmul(np.abs(doh), np.abs(vh).swapaxes(2, 3)) + (np.abs(doh) * np.abs(oh)).sum(3, keepdims=True)
     norm = lambda t: np.sqrt((t * t).sum(3)).max(2, initial=0.0)[..., None, None]  # noqa: E731
-    least = 2.0 ** -36 * scale * norm(doh) * norm(vh) if dtype == "f16" else 0.0  # below float16's normal range
-    ds_tol = np.abs(ds) * (ROUND[dtype] + rel + 8 * EPS) + scale * (p * (d + 16) * EPS + FLUSH) * parts + least * seen[:, None]
+    if least is None:
+        least = [2.0 ** -36 * scale * norm(doh) * norm(vh) if dtype == "f16" else 0.0] * 2  # below float16's normal range
+    ds_tol = np.abs(ds) * (ROUND[dtype] + rel + 8 * EPS) + scale * (p * (d + 16) * EPS + FLUSH) * parts
+    dq_ds_tol, dk_ds_tol = (ds_tol + t * seen[:, None] for t in least)
     sum_heads = lambda t: t.reshape(n, hk, h // hk, tk, d).sum(2).transpose(0, 2, 1, 3)  # noqa: E731
     by_key = lambda a, b: sum_heads(np.matmul(a.swapaxes(2, 3), b))  # noqa: E731
     dq = np.matmul(ds, kh).transpose(0, 2, 1, 3)
     dk, dv = by_key(ds, qh), by_key(p, doh)
     n_q, n_k = (tk + 64) * EPS, (tq * h // hk + 64) * EPS
-    dq_tol = np.matmul(ds_tol + n_q * np.abs(ds), np.abs(kh)).transpose(0, 2, 1, 3)
-    dk_tol = by_key(ds_tol + n_k * np.abs(ds), np.abs(qh))
+    dq_tol = np.matmul(dq_ds_tol + n_q * np.abs(ds), np.abs(kh)).transpose(0, 2, 1, 3)
+    dk_tol = by_key(dk_ds_tol + n_k * np.abs(ds), np.abs(qh))
     dv_tol = by_key(p * (ROUND[dtype] + rel + n_k) + (FLUSH + (2.0 ** -40 if dtype == "f16" else 0.0)) * seen[:, None], np.abs(doh))
     return (dq, dk, dv), (dq_tol, dk_tol, dv_tol)
 

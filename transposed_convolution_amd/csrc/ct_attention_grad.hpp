@@ -13,9 +13,10 @@
 // of the 7.  Both kernels are bound as the forward one is, by the vector instructions of a score (8 here) and
 // by waiting between dependent steps at two or three waves a SIMD.
 //
-// float16 has few exponents, and P is about 1 / Tk: P is held 2^15 times larger, and dS by the power
-// of two that takes its largest possible value, scale * 2 max|do| max|v|, to 2^15.  Both are divided
-// out of the float32 sums at the end.
+// float16 has few exponents, and P is about 1 / Tk: P is held 2^15 times larger, and dS by a power of two
+// that takes its largest possible value, scale * 2 |do| max|v|, to 2^15: of its row in the sum for dq, of its tile of
+// rows in the sum for dk, which is scaled where that power changes.  So a row's gradient keeps its digits whatever
+// size that of other rows has.  Both powers are taken out of the float32 sums at the end.
 #pragma once
 
 #include "ct_attention.hpp"
@@ -39,7 +40,7 @@ constexpr int kAhead = DP * sizeof(T) > 256 ? 2 : DP * sizeof(T) > 128 ? 3 : 4;
 
 constexpr int kStatRows = 64;  // rows or keys a block of stat_kernel looks at
 
-// RowStat of the rows, and for float16 the largest norm of 64 rows' do, or of 64 keys' values, for each
+// RowStat of the rows, and for float16 log2 of the largest norm of 64 rows' do, or of 64 keys' values, for each
 // image and key head.  LANES lanes a row, 16 bytes a lane; one pass over o, do and v, 4.6 TB/s of 100 MB.
 template <class T, int LANES>
 __global__ __launch_bounds__(256) void stat_kernel(Attention a, RowStat *stat, float *top, int row_blocks, int blocks)
@@ -95,42 +96,50 @@ __global__ __launch_bounds__(256) void stat_kernel(Attention a, RowStat *stat, f
         if (threadIdx.x == 0) {
 #pragma unroll
             for (int i = 1; i < 256 / LANES; ++i) most = fmaxf(most, shared[i]);
-            top[blockIdx.x] = sqrtf(most);
+            top[blockIdx.x] = 0.5f * log2f(most);
         }
     }
 }
 
-// The power of two dS of an image and key head is held by; the same in both kernels.
+// log2 of the largest norm of the values of an image and key head, of its first `count` blocks of 64 keys.
 template <class T, int THREADS>
-__device__ __forceinline__ int grad_shift(const Attention &a, const float *top, int nh, int row_blocks, int blocks)
+__device__ __forceinline__ float value_top(const float *top, int count)
 {
     if constexpr (!kHalf<T>) {
-        return 0;
+        return 0.0f;
     } else {
-        __shared__ float shared[2][THREADS / 64];
-        float most[2] = {0.0f, 0.0f};
-        const float *p = top + int64_t(nh) * blocks;
-        for (int b = threadIdx.x; b < blocks; b += THREADS) {
-            const float v = p[b];
-            most[0] = fmaxf(most[0], b < row_blocks ? v : 0.0f);
-            most[1] = fmaxf(most[1], b < row_blocks ? 0.0f : v);
-        }
+        __shared__ float shared[THREADS / 64];
+        float most = -INFINITY;
+        for (int b = threadIdx.x; b < count; b += THREADS) most = fmaxf(most, top[b]);
 #pragma unroll
-        for (int of = 0; of < 2; ++of) {
-#pragma unroll
-            for (int s = 32; s; s >>= 1) most[of] = fmaxf(most[of], __shfl_xor(most[of], s));
-            if ((threadIdx.x & 63) == 0) shared[of][threadIdx.x >> 6] = most[of];
-        }
+        for (int s = 32; s; s >>= 1) most = fmaxf(most, __shfl_xor(most, s));
+        if ((threadIdx.x & 63) == 0) shared[threadIdx.x >> 6] = most;
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < THREADS / 64; ++i) {
-            most[0] = fmaxf(most[0], shared[0][i]);
-            most[1] = fmaxf(most[1], shared[1][i]);
-        }
-        // logarithms, not products: the norms' product may leave float32
-        const float bound = log2f(most[0]) + log2f(most[1]) + log2f(a.scale) + 1.0f;
-        // (nothing but zeros, or a value that is not finite: any shift will do)
-        return bound > -100.0f && bound < 100.0f ? kHalfBias - int(ceilf(bound)) : 0;
+        for (int i = 0; i < THREADS / 64; ++i) most = fmaxf(most, shared[i]);
+        return most;
+    }
+}
+// A value that a wave's lanes share, in a scalar register.
+__device__ __forceinline__ float uniform(float x)
+{
+    return __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, x)));
+}
+// The power of two by which dS is held whose magnitude has log2 below `bound`.  2^60 is enough for any: what is below
+// 2^-25 there is 2^-85 and nothing in float16, however many are summed.  (Values that are not finite end at 200.)
+__device__ __forceinline__ int grad_shift(float bound)
+{
+    return kHalfBias - int(ceilf(fminf(fmaxf(bound, float(kHalfBias - 60)), 200.0f)));
+}
+// c / 2^shift
+template <class T, int DB>
+__device__ __forceinline__ void unshift(f32x16 (&c)[DB], int shift)
+{
+    if constexpr (kHalf<T>) {
+#pragma unroll
+        for (int db = 0; db < DB; ++db)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) c[db][r] = ldexpf(c[db][r], -shift);
     }
 }
 
@@ -210,9 +219,12 @@ struct KeyGrad {
 #pragma unroll
         for (int db = 0; db < DB; ++db) dk[db] = dv[db] = f32x16{};
 
-        const int shift = grad_shift<T, THREADS>(a, shared.top, nh, shared.row_blocks, shared.blocks);
         const float bias = kHalf<T> ? float(kHalfBias) : 0.0f, c = a.scale * kLog2e;
-        const float factor = a.scale * exp2f(float(shift) - bias);
+        // float16: the power of the sums so far, that of the tile in LDS, log2 of what goes with a row's norm in dS
+        const float *top = shared.top + int64_t(nh) * shared.blocks;
+        const float rest = uniform(1.0f + log2f(a.scale) + value_top<T, THREADS>(top + shared.row_blocks, shared.blocks - shared.row_blocks));
+        int shift = 0, next = 60;
+        float factor = a.scale, norm = 0.0f;
 
         const T *qp = static_cast<const T *>(a.q.p) + n * a.q.n + hk * a.G * a.q.h;
         const T *dp = static_cast<const T *>(a.d_o.p) + n * a.d_o.n + hk * a.G * a.d_o.h;
@@ -221,6 +233,7 @@ struct KeyGrad {
         RowStat mine{INFINITY, 0.0f};
         int end = 0;
         auto load = [&](int rt) {
+            if constexpr (kHalf<T>) norm = top[rt * RT / kStatRows];
             if (a.G == 1 && rt * RT >= from_token) {
                 qm.load(qp + int64_t(rt) * RT * a.q.t, a.q.t, a.R - rt * RT, a.D);
                 dm.load(dp + int64_t(rt) * RT * a.d_o.t, a.d_o.t, a.R - rt * RT, a.D);
@@ -243,9 +256,16 @@ struct KeyGrad {
         auto store = [&](int buf) {
             qm.store(lds.tile[buf][0]);
             dm.store(lds.tile[buf][1]);
+            float by = a.scale;
+            if constexpr (kHalf<T>) {
+                // it stays while it is at most 2 below what the tile allows: norms of like size change nothing
+                const int allowed = __builtin_amdgcn_readfirstlane(grad_shift(norm + rest));
+                if (next > allowed || (next < allowed - 2 && norm > -INFINITY)) next = allowed;
+                by = ldexpf(a.scale, next - kHalfBias);
+            }
             if (tid < RT) {
                 lds.lse2[buf][tid] = mine.lse2 - bias;
-                lds.delta[buf][tid] = mine.delta * factor;
+                lds.delta[buf][tid] = mine.delta * by;
                 lds.ends[buf][tid] = end;
             }
         };
@@ -261,12 +281,18 @@ struct KeyGrad {
                 store(0);
                 __syncthreads();
             }
+            const int held = next;  // this tile's
             if (rt + 1 < rt1) load(rt + 1);
             const T *ql = lds.tile[buf][0], *dl = lds.tile[buf][1];
             if (WAVES > 4 && a.causal && a.seen(len, start, a.by_g.div(min(rt * RT + RT, a.R) - 1)) <= key0) {
                 // nothing of this wave's (the test costs shorter blocks more than it saves)
                 if (BUFS == 2 && rt + 1 < rt1) store(buf ^ 1);
                 continue;
+            }
+            if (kHalf<T> && shift != held) {
+                unshift<T, DB>(dk, shift - held);
+                shift = held;
+                factor = uniform(ldexpf(a.scale, shift - kHalfBias));
             }
             // the tile's first row sees fewest keys; rows that do not exist have P = 0
             const bool whole = key0 + 32 <= a.seen(len, start, a.by_g.div(rt * RT));
@@ -318,16 +344,17 @@ struct KeyGrad {
             if (BUFS == 2 && rt + 1 < rt1) store(buf ^ 1);
         }
         if (key >= a.Tk) return;
-        const float undo_k = exp2f(-float(shift)), undo_v = exp2f(-bias);
+        unshift<T, DB>(dk, shift);
+        const float undo_v = exp2f(-bias);
         const int64_t at = ((int64_t(n) * a.Tk + key) * a.Hkv + hk) * a.D + column * 32;
         const int D = a.D - column * 32;
         if (splits == 1) {
-            store_columns<T, DB>(static_cast<T *>(a.dk) + at, dk, undo_k, D, half);
+            store_columns<T, DB>(static_cast<T *>(a.dk) + at, dk, 1.0f, D, half);
             store_columns<T, DB>(static_cast<T *>(a.dv) + at, dv, undo_v, D, half);
         } else {
             const int64_t all = int64_t(a.N) * a.Tk * a.Hkv * a.D;
             float *to = part + int64_t(split) * 2 * all + at;
-            store_columns<float, DB>(to, dk, undo_k, D, half);
+            store_columns<float, DB>(to, dk, 1.0f, D, half);
             store_columns<float, DB>(to + all, dv, undo_v, D, half);
         }
     }
@@ -356,19 +383,18 @@ struct RowGrad {
         const int start = a.start(n), len = a.length(n, start), from_token = a.first_token(len, start);
         const int block_row = tile * ROWS, row0 = block_row + wave * 32;
         // keys the block looks at, of this split's chunk
-        const int want = min(a.seen(len, start, a.by_g.div(min(block_row + ROWS, a.R) - 1)), split * chunk + chunk);
+        const int most_seen = a.seen(len, start, a.by_g.div(min(block_row + ROWS, a.R) - 1)), want = min(most_seen, split * chunk + chunk);
         const int kt0 = split * chunk / KT, kt1 = (want + KT - 1) / KT;
         if (splits > 1 && kt0 >= kt1) return;  // the join passes over it
 
-        const int shift = grad_shift<T, THREADS>(a, shared.top, nh, shared.row_blocks, shared.blocks);
         const float bias = kHalf<T> ? float(kHalfBias) : 0.0f, c = a.scale * kLog2e;
-        const float factor = a.scale * exp2f(float(shift) - bias);
+        // of the keys that the block's rows see, whatever this split has of them: delta is of all
+        const float most = value_top<T, THREADS>(shared.top + int64_t(nh) * shared.blocks + shared.row_blocks, (most_seen + kStatRows - 1) / kStatRows);
 
         const int row = row0 + (lane & 31), t = a.by_g.div(row), h = hk * a.G + row - t * a.G;
         const bool sees = row < a.R && t >= from_token;
         const int seen = sees ? a.seen(len, start, t) : 0;
         const RowStat mine = row < a.R ? shared.stat[int64_t(nh) * a.R + row] : RowStat{INFINITY, 0.0f};
-        const float lse2 = mine.lse2 - bias, delta = mine.delta * factor;
         Frag<T> q[KS], d_o[KS];
         const T *qp = static_cast<const T *>(a.q.p) + n * a.q.n + t * a.q.t + h * a.q.h;
         const T *dp = static_cast<const T *>(a.d_o.p) + n * a.d_o.n + t * a.d_o.t + h * a.d_o.h;
@@ -377,6 +403,18 @@ struct RowGrad {
             q[ks] = load_frag<T>(qp, ks * 16 + half * 8, sees ? a.D : 0);
             d_o[ks] = load_frag<T>(dp, ks * 16 + half * 8, sees ? a.D : 0);
         }
+        int shift = 0;
+        float factor = a.scale;
+        if constexpr (kHalf<T>) {  // a row is a lane's and the lane's 32 above
+            float square = 0.0f;
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) square = fmaf(float(d_o[ks][j]), float(d_o[ks][j]), square);
+            shift = grad_shift(1.0f + log2f(a.scale) + most + 0.5f * log2f(half_sum(square)));
+            factor = ldexpf(a.scale, shift - kHalfBias);
+        }
+        const float lse2 = mine.lse2 - bias, delta = mine.delta * factor;
         const bool rows = row0 < a.R;
         const int whole = rows ? a.seen(len, start, a.by_g.div(row0)) / KT : 0;
         const int none = rows ? (a.seen(len, start, a.by_g.div(min(row0 + 32, a.R) - 1)) + KT - 1) / KT : 0;
@@ -443,10 +481,10 @@ struct RowGrad {
             if (BUFS == 2 && kt + 1 < kt1) store(buf ^ 1);
         }
         if (row >= a.R) return;
-        const float undo = exp2f(-float(shift));
+        unshift<T, DB>(dq, shift);
         const int64_t at = ((int64_t(n) * a.Tq + t) * a.H + h) * a.D;
-        if (splits == 1) store_columns<T, DB>(static_cast<T *>(a.dq) + at, dq, undo, a.D, half);
-        else store_columns<float, DB>(part + int64_t(split) * a.N * a.Tq * a.H * a.D + at, dq, undo, a.D, half);
+        if (splits == 1) store_columns<T, DB>(static_cast<T *>(a.dq) + at, dq, 1.0f, a.D, half);
+        else store_columns<float, DB>(part + int64_t(split) * a.N * a.Tq * a.H * a.D + at, dq, 1.0f, a.D, half);
     }
 };
 
