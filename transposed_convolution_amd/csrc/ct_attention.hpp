@@ -350,6 +350,23 @@ struct Mover {
             r[i] = load_chunk<T>(p + column, p ? D - column : 0, D % L::kChunk);
         }
     }
+    // Values that are not finite become zeros; were there any?
+    __device__ __forceinline__ bool drop_not_finite()
+    {
+        using U = std::conditional_t<sizeof(T) == 2, unsigned short, unsigned>;
+        constexpr U ONES = std::is_same_v<T, _Float16> ? 0x7c00 : sizeof(T) == 2 ? 0x7f80 : U(0x7f800000);  // the exponent's
+        bool found = false;
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i)
+#pragma unroll
+            for (int j = 0; j < L::kChunk; ++j) {
+                const T x = r[i][j];
+                const bool odd = (__builtin_bit_cast(U, x) & ONES) == ONES;
+                r[i][j] = odd ? T(0.0f) : x;
+                found |= odd;
+            }
+        return found;
+    }
     __device__ __forceinline__ void store(T *tile) const
     {
         if (L::kChunks == kLanes || column < DP) {

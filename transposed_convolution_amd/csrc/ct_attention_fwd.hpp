@@ -84,6 +84,8 @@ struct Parts {
     }
 };
 
+__device__ __forceinline__ bool finite(float x) { return fabsf(x) <= 3.402823466e38f; }
+
 // The result of a row: stored, or left as a part.
 template <class T, int DB>
 __device__ __forceinline__ void finish(const Attention &a, float *part, int splits, int split, int nh, int n, int hk, int row,
@@ -106,79 +108,57 @@ __device__ __forceinline__ void finish(const Attention &a, float *part, int spli
     }
 }
 
-// A weight of 0 times a value that is not finite is NaN, so in a causal call such a value reaches rows of its
-// tile that do not see it.  Rows whose result is not finite are therefore made again, one after the other by
-// the whole wave, from the keys [from, seen) alone.  (A test of the values on the way costs the
-// loop its registers: 720 us became 1490 for 8191 tokens and heads of 128.)
-__device__ __forceinline__ bool finite(float x) { return fabsf(x) <= 3.402823466e38f; }
-template <class T>
-__device__ __forceinline__ void redo_row(const Attention &a, float *part, int splits, int split, int nh, int n, int hk, int row,
-                                         int from, int end, int lane)
-{
-    const int t = a.by_g.div(row), h = hk * a.G + row - t * a.G;
-    const T *q = static_cast<const T *>(a.q.p) + n * a.q.n + t * a.q.t + h * a.q.h;
-    const T *k = static_cast<const T *>(a.k.p) + n * a.k.n + hk * a.k.h, *v = static_cast<const T *>(a.v.p) + n * a.v.n + hk * a.v.h;
-    const float c = a.scale * kLog2e;
-    auto score = [&](int j) {
-        float s = 0.0f;
-        for (int d = 0; d < a.D; ++d) s = fmaf(float(q[d]), float(k[j * a.k.t + d]), s);
-        return s * c;
-    };
-    float m = -INFINITY, l = 0.0f, acc[kMaxHead / 64] = {};
-    for (int j = from + lane; j < end; j += 64) m = fmaxf(m, score(j));
-#pragma unroll
-    for (int x = 32; x; x >>= 1) m = fmaxf(m, __shfl_xor(m, x));
-    const float base = m == -INFINITY ? 0.0f : m;
-    for (int j0 = from; j0 < end; j0 += 64) {
-        const float p = j0 + lane < end ? exp2_fast(score(j0 + lane) - base) : 0.0f;
-        l += p;
-        for (int i = 0; i < min(64, end - j0); ++i) {
-            const float w = __shfl(p, i);
-#pragma unroll
-            for (int x = 0; x < kMaxHead / 64; ++x)
-                if (x * 64 + lane < a.D) acc[x] = fmaf(w, float(v[(j0 + i) * a.v.t + x * 64 + lane]), acc[x]);
-        }
-    }
-#pragma unroll
-    for (int x = 32; x; x >>= 1) l += __shfl_xor(l, x);
-    const Parts ps(part, a, splits);
-    const int64_t at = split * ps.rows + int64_t(nh) * a.R + row, place = (int64_t(n) * a.Tq + t) * a.H + h;
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-#pragma unroll
-    for (int x = 0; x < kMaxHead / 64; ++x) {
-        const int d = x * 64 + lane;
-        if (d >= a.D) continue;
-        if (splits == 1) static_cast<T *>(a.out)[place * a.D + d] = T(acc[x] * inv);
-        else ps.out[at * a.D + d] = acc[x];
-    }
-    if (lane == 0) {
-        if (splits == 1) {
-            a.lse[(int64_t(n) * a.H + h) * a.Tq + t] = l == 0.0f ? -INFINITY : (m + __log2f(l)) * kLn2;
-        } else {
-            ps.stat[2 * at] = l == 0.0f ? -INFINITY : m;
-            ps.stat[2 * at + 1] = l;
-        }
-    }
-}
-// The results of a wave's 32 rows, of the keys [from, ..) of its split.
+// A weight of 0 times a value that is not finite is NaN, so in a causal call such a value would reach rows that do not
+// see it.  The tiles that some rows see in part (two or three a block) therefore have zeros in such places, and what
+// stood there is added at the end to the rows that see it: a weight leaves neither an infinity nor a NaN
+// otherwise.  In tiles that every row sees it takes part as it is.
+//
+// This happens only where such a value was found: a lane looks at one of 64 keys, then those that have any are taken
+// from memory, several at a time where heads are short.  `end`: how many of the keys the lane's row sees.
 template <class T, int DB>
-__device__ __forceinline__ void finish_rows(const Attention &a, float *part, int splits, int split, int nh, int n, int hk, int row0,
-                                            int lane, int from, int seen, float m, float l, const f32x16 (&o)[DB])
+__device__ __forceinline__ void add_not_finite(f32x16 (&o)[DB], const T *v, int64_t stride, int keys, int end, int D, int lane)
 {
-    const int row = row0 + (lane & 31);
-    bool odd = false;
-    if (a.causal) {
-        odd = !finite(l);
+    constexpr int K = DB == 1 ? 8 : DB == 2 ? 4 : DB <= 4 ? 2 : 1;
+    const int half = lane >> 5;
+    for (int j0 = 0; j0 < keys; j0 += 64) {
+        bool odd = false;
+        if (j0 + lane < keys)
+            for (int d = 0; d < D; d += kVec<T>) {
+                const Raw<T, kVec<T>> r = load_chunk<T>(v + (j0 + lane) * stride + d, D - d, D % kVec<T>);
 #pragma unroll
-        for (int db = 0; db < DB; ++db)
+                for (int i = 0; i < kVec<T>; ++i) odd |= !finite(float(r[i]));
+            }
+        for (uint64_t left = __ballot(odd); left;) {
+            const int first = __builtin_ctzll(left) / K * K, j = j0 + first;
+            left &= ~(((uint64_t(1) << K) - 1) << first);
 #pragma unroll
-            for (int r = 0; r < 16; ++r) odd |= !finite(o[db][r]);
-        odd = row < a.R && half_max(odd ? 1.0f : 0.0f) > 0.0f;
-    }
-    if (row < a.R && !odd) finish<T, DB>(a, part, splits, split, nh, n, hk, row, lane >> 5, m, l, o);
-    for (uint64_t left = __ballot(odd) & 0xffffffffu; left; left &= left - 1) {
-        const int i = __builtin_ctzll(left);
-        redo_row<T>(a, part, splits, split, nh, n, hk, row0 + i, from, __builtin_amdgcn_readlane(seen, i), lane);
+            for (int db = 0; db < DB; ++db) {
+                Raw<T, 4> x[K][4];
+#pragma unroll
+                for (int key = 0; key < K; ++key)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int d = db * 32 + 8 * k + 4 * half;
+                        const T *p = v + (j + key) * stride + d;
+                        x[key][k] = Raw<T, 4>{};
+                        if (j + key < end && d + 4 <= D) {
+                            x[key][k] = *reinterpret_cast<const Raw<T, 4> *>(p);
+                        } else if (j + key < end) {
+#pragma unroll
+                            for (int i = 0; i < 3; ++i)
+                                if (d + i < D) x[key][k][i] = p[i];
+                        }
+                    }
+#pragma unroll
+                for (int key = 0; key < K; ++key)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) {
+                        const float f = float(x[key][r / 4][r % 4]);
+                        o[db][r] += finite(f) ? 0.0f : f;
+                    }
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
     }
 }
 
@@ -201,6 +181,7 @@ __global__ __launch_bounds__(WAVES * 64, DP * sizeof(T) <= 128 ? 3 : DP * sizeof
     // Operands asked for ahead: heads of 128 took 727 us without, 699, 692, 687 and 690 with 2, 3, 4 and 6.
     constexpr int P = 4;
     __shared__ __attribute__((aligned(16))) T lds[2][2][KT * DP];
+    __shared__ int odd[WAVES];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), half = lane >> 5;
 
     // an XCD takes a contiguous run of blocks: those of one image and key head share its L2
@@ -227,6 +208,8 @@ __global__ __launch_bounds__(WAVES * 64, DP * sizeof(T) <= 128 ? 3 : DP * sizeof
     const bool rows = row0 < a.R;
     const int whole = rows ? a.seen(len, start, a.by_g.div(row0)) / KT : 0;
     const int none = rows ? (a.seen(len, start, a.by_g.div(min(row0 + 32, a.R) - 1)) + KT - 1) / KT : 0;
+    // tiles from here on some rows of the block see in part, but for those behind the length
+    const int mixed = a.causal ? a.seen(len, start, a.by_g.div(block_row)) / KT : kt1;
 
     const T *kp = static_cast<const T *>(a.k.p) + n * a.k.n + hk * a.k.h;
     const T *vp = static_cast<const T *>(a.v.p) + n * a.v.n + hk * a.v.h;
@@ -236,7 +219,9 @@ __global__ __launch_bounds__(WAVES * 64, DP * sizeof(T) <= 128 ? 3 : DP * sizeof
         km.load(kp + int64_t(kt) * KT * a.k.t, a.k.t, len - kt * KT, a.D);
         vm.load(vp + int64_t(kt) * KT * a.v.t, a.v.t, len - kt * KT, a.D);
     };
-    auto store = [&](int buf) {
+    int found = 0;  // did this wave bring values that are not finite in such tiles
+    auto store = [&](int buf, int kt) {
+        if (kt >= mixed) found |= __any(vm.drop_not_finite());
         km.store(lds[buf][0]);
         vm.store(lds[buf][1]);
     };
@@ -248,7 +233,7 @@ __global__ __launch_bounds__(WAVES * 64, DP * sizeof(T) <= 128 ? 3 : DP * sizeof
     const float c = a.scale * kLog2e;
     if (kt0 < kt1) {
         load(kt0);
-        store(0);
+        store(0, kt0);
     }
     for (int kt = kt0; kt < kt1; ++kt) {
         __syncthreads();
@@ -275,10 +260,19 @@ __global__ __launch_bounds__(WAVES * 64, DP * sizeof(T) <= 128 ? 3 : DP * sizeof
                 o[i % DB] = mma(f, p, o[i % DB]);
             });
         }
-        if (kt + 1 < kt1) store(buf ^ 1);
+        if (kt + 1 < kt1) store(buf ^ 1, kt + 1);
+    }
+    const int odd0 = max(mixed, kt0);
+    if (odd0 < kt1) {
+        if (lane == 0) odd[wave] = found;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < WAVES; ++i) found |= odd[i];
+        if (__builtin_amdgcn_readfirstlane(found))
+            add_not_finite<T, DB>(o, vp + int64_t(odd0) * KT * a.v.t, a.v.t, min(kt1 * KT, len) - odd0 * KT, seen - odd0 * KT, a.D, lane);
     }
     const float l = half_sum(run.l);
-    finish_rows<T, DB>(a, part, splits, split, nh, n, hk, row0, lane, split * chunk, min(seen, want), run.m, l, o);
+    if (there) finish<T, DB>(a, part, splits, split, nh, n, hk, row, half, run.m, l, o);
 }
 
 // Up to 32 rows a key head (a token or a few over a cache): every wave takes 32 keys of its own at a
@@ -308,7 +302,7 @@ __global__ __launch_bounds__(WAVES * 64, DP * sizeof(T) <= 256 ? 2 : 1) void att
     const int want = min(a.seen(len, start, a.Tq - 1), split * chunk + chunk);
     if (split > 0 && split * chunk >= want) return;  // the join passes over it
     const int kt0 = split * chunk / 32 + wave, kt1 = (want + 31) / 32;
-    const int whole = a.seen(len, start, 0) / 32;
+    const int whole = a.seen(len, start, 0) / 32, mixed = a.causal ? whole : kt1;
     const T *kp = static_cast<const T *>(a.k.p) + n * a.k.n + hk * a.k.h;
     const T *vp = static_cast<const T *>(a.v.p) + n * a.v.n + hk * a.v.h;
 
@@ -326,6 +320,7 @@ __global__ __launch_bounds__(WAVES * 64, DP * sizeof(T) <= 256 ? 2 : 1) void att
     for (int db = 0; db < DB; ++db) o[db] = f32x16{};
     Running run;
     const float c = a.scale * kLog2e;
+    bool odd = false;
     for (int kt = kt0; kt < kt1; kt += WAVES) {
         // the wave's own tiles: what it stores and reads there stays in order
         mv.store(kl);
@@ -336,6 +331,7 @@ __global__ __launch_bounds__(WAVES * 64, DP * sizeof(T) <= 256 ? 2 : 1) void att
         if (kt >= whole) hide(s, seen - kt * 32, half);
         run.look(s, o, c);
         run.weigh<T>(s, c);
+        if (kt >= mixed) odd |= __any(mv.drop_not_finite());
         mv.store(vl);
         const int next = kt + WAVES;
         if (next < kt1) mv.load(kp + int64_t(next) * 32 * a.k.t, a.k.t, len - next * 32, a.D);
@@ -346,6 +342,9 @@ __global__ __launch_bounds__(WAVES * 64, DP * sizeof(T) <= 256 ? 2 : 1) void att
             for (int db = 0; db < DB; ++db) o[db] = mma(L::by_columns(vl, st * 16, db, lane), p, o[db]);
         }
     }
+    if (odd)
+        for (int kt = kt0; kt < kt1; kt += WAVES)
+            if (kt >= mixed) add_not_finite<T, DB>(o, vp + int64_t(kt) * 32 * a.v.t, a.v.t, min(32, len - kt * 32), seen - kt * 32, a.D, lane);
     float l = half_sum(run.l), m = run.m;
     if constexpr (WAVES > 1) {
         if (half == 0) {
@@ -391,7 +390,7 @@ __global__ __launch_bounds__(WAVES * 64, DP * sizeof(T) <= 256 ? 2 : 1) void att
             }
         m = top;
     }
-    finish_rows<T, DB>(a, part, splits, split, nh, n, hk, 0, lane, split * chunk, min(seen, want), m, l, o);
+    if (there) finish<T, DB>(a, part, splits, split, nh, n, hk, row, half, m, l, o);
 }
 
 // The splits of a row, a block a row: weights 2^(m - largest m).  A lane reads the statistics of one split; the
