@@ -275,6 +275,13 @@ __global__ __launch_bounds__(WAVES * 64, DP * sizeof(T) <= 128 ? 3 : DP * sizeof
     if (there) finish<T, DB>(a, part, splits, split, nh, n, hk, row, half, run.m, l, o);
 }
 
+// Memory accesses of a wave's lanes on both sides stay there: what one lane stored before, another reads after.
+__device__ __forceinline__ void in_order()
+{
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
 // Up to 32 rows a key head (a token or a few over a cache): every wave takes 32 keys of its own at a
 // time, through LDS of its own, and the block's waves are joined at the end.  Nothing waits for another wave
 // on the way.  One token, 4 images of up to 32768 keys, 16 heads over 4 of 128, bfloat16: 45 us with the join,
@@ -322,9 +329,11 @@ __global__ __launch_bounds__(WAVES * 64, DP * sizeof(T) <= 256 ? 2 : 1) void att
     const float c = a.scale * kLog2e;
     bool odd = false;
     for (int kt = kt0; kt < kt1; kt += WAVES) {
-        // the wave's own tiles: what it stores and reads there stays in order
+        // The tiles are the wave's own, whose LDS accesses are done in order; in_order keeps the compiler from changing
+        // it, here and for the next tiles' stores: each tile's reads lie before the other's.
         mv.store(kl);
         mv.load(vp + int64_t(kt) * 32 * a.v.t, a.v.t, len - kt * 32, a.D);
+        in_order();
         f32x16 s[1] = {f32x16{}};
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) s[0] = mma(L::by_rows(kl, lane & 31, ks, half), q[ks], s[0]);
@@ -335,6 +344,7 @@ __global__ __launch_bounds__(WAVES * 64, DP * sizeof(T) <= 256 ? 2 : 1) void att
         mv.store(vl);
         const int next = kt + WAVES;
         if (next < kt1) mv.load(kp + int64_t(next) * 32 * a.k.t, a.k.t, len - next * 32, a.D);
+        in_order();
 #pragma unroll
         for (int st = 0; st < 2; ++st) {
             const Frag<T> p = operand<T>(s[0], st);
