@@ -1,11 +1,12 @@
-"""Attention's gradient where rows are of very different sizes, against the plain 64-bit form."""
+"""Attention where scores are far from zero and its gradient where rows are of very different sizes, against the plain
+64-bit form."""
 import numpy as np
 import pytest
 import torch
 
 import attention_refs as A
 import layer_refs as R
-from test_gpu_attention import T, dev, host, inputs  # noqa: F401  (T: the fixture)
+from test_gpu_attention import DT, T, dev, host, inputs  # noqa: F401  (T: the fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -80,3 +81,37 @@ def test_float16_score_gradients_beyond_any_power(T, shape):  # noqa: F811
     assert not dq.any() and not dk.any()
     want, tol = A.attend_grad(arrays[3], *arrays[:3], o, l, 1.0, seen, "f16")  # dv has no scale where scores are 0
     R.assert_close(host(dv), want[2], tol[2], "f16", "dv")
+
+
+# tq, tk, h, hk, causal: whole blocks, a few rows, split over the keys
+FAR = [(150, 150, 2, 1, True), (3, 90, 8, 2, True), (2, 2000, 4, 2, True), (130, 1400, 1, 1, False)]
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("power", [9, 14, 17, 24, 60])
+@pytest.mark.parametrize("call", FAR, ids=str)
+def test_scores_far_from_zero(T, dtype, power, call):  # noqa: F811
+    """Scores that are multiples of 2^power, up to 127 of them either way: the largest take all, in equal parts.  Every
+    third token's scores are zeros, beside the others in its wave."""
+    tq, tk, h, hk, causal = call
+    rng = np.random.default_rng(85)
+    q, k = np.zeros((1, tq, h, 64)), rng.normal(size=(1, tk, hk, 64))
+    q[:, :, :, 0] = np.where(np.arange(tq) % 3 == 0, 0.0, 16.0)[None, :, None]
+    k[..., 0] = rng.integers(-127, 128, size=(1, tk, hk))
+    (tq_, qv), (tk_, kv), (tv_, vv) = (dev(a, dtype) for a in (q, k, rng.normal(size=k.shape)))
+    scale = 2.0 ** (power - 4)
+    seen = A.visible(1, tq, tk, causal, None, None)
+    (o, l), _ = A.attend(qv, kv, vv, scale, seen, dtype)
+    out, lse = T.attention_nd(tq_, tk_, tv_, scale=scale, causal=causal)
+    torch.cuda.synchronize()
+    # weights are 1 and 0 (2^-700 and less), but for the zero scores' rows in float16, which are 2^7: out is a float32
+    # sum of up to tk values, their count's reciprocal and a product
+    tol = (tk + 4) * R.EPS * np.abs(vv).max()
+    if power < 24:
+        # references below 2^20 were rounded, by up to 2^-5, and the scores' products with c are not: a weight is then
+        # 2^(+-2^-5) of a power of two, the same for equal scores, and is rounded to dtype beside the products but not in
+        # the sum of weights
+        tol += A.ROUND[dtype] * np.abs(vv).max()
+    R.assert_close(host(out), o, tol, dtype, f"{call} 2^{power} out")
+    # scale log2(e), its product with the score, the sum with the count's logarithm, the way back: 6 roundings
+    R.assert_close(host(lse), l, 6 * R.EPS * np.abs(l) + 8 * R.EPS, "f32", f"{call} 2^{power} lse")

@@ -19,12 +19,18 @@ constexpr float kSlack = 8.0f;
 template <class T>
 constexpr float kWeightBias = std::is_same_v<T, _Float16> ? 7.0f : 0.0f;
 
-// The softmax of a row so far: reference m (in powers of two), sum l of 2^(s c - m + bias), this lane's
-// half of it.
+// References from here on (in powers of two) are those of scores whose product with c is rounded by itself.  One fused
+// step, s c - m, keeps what the reference's own rounding left out, half a unit: 2^-5 here, which does no harm, but
+// from 2^24 on it takes float16 weights beyond their range and from 2^31 on any: the largest score's is not 1 then
+// but infinite or nothing.
+constexpr float kFar = 0x1p20f;
+
+// The softmax of a row so far: reference m (in powers of two, the bias taken off where it is not far), sum l of 2^(s c - m), this
+// lane's half of it.
 struct Running {
     float m = -INFINITY, l = 0.0f;
     // Moves the reference for a tile's scores, and scales the output where it does.
-    template <int KB, int DB>
+    template <class T, int KB, int DB>
     __device__ __forceinline__ void look(const f32x16 (&s)[KB], f32x16 (&o)[DB], float c)
     {
         float top = s[0][0];
@@ -33,9 +39,9 @@ struct Running {
 #pragma unroll
             for (int r = 0; r < 16; ++r) top = fmaxf(top, s[kb][r]);
         top = half_max(top) * c;
-        const bool moves = top > m + kSlack || (m == -INFINITY && top > -INFINITY);
+        const bool moves = top - m > kSlack + kWeightBias<T>;  // exact where they are near each other
         if (__any(moves)) {
-            const float to = moves ? top : m;
+            const float to = moves ? fabsf(top) < kFar ? top - kWeightBias<T> : top : m;
             const float f = moves ? exp2_fast(m - to) : 1.0f;
             m = to;
             l *= f;
@@ -45,17 +51,31 @@ struct Running {
                 for (int r = 0; r < 16; ++r) o[db][r] *= f;
         }
     }
+    // Scores times c, rounded: the product of the largest is the reference itself.
+    template <int KB>
+    __device__ __forceinline__ static void far(f32x16 (&s)[KB], float c)
+    {
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) s[kb][r] *= c;
+    }
     // Scores become weights.
     template <class T, int KB>
     __device__ __forceinline__ void weigh(f32x16 (&s)[KB], float c)
     {
-        const float base = m == -INFINITY ? 0.0f : m - kWeightBias<T>;
+        const float base = m == -INFINITY ? 0.0f : m;
+        float by = c;
+        if (__any(fabsf(base) >= kFar)) {
+            far(s, c);
+            by = 1.0f;
+        }
         float sum[2] = {0.0f, 0.0f};
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
-                const float e = exp2_fast(fmaf(s[kb][r], c, -base));
+                const float e = exp2_fast(fmaf(s[kb][r], by, -base));
                 s[kb][r] = e;
                 sum[r & 1] += e;
             }
@@ -92,16 +112,15 @@ __device__ __forceinline__ void finish(const Attention &a, float *part, int spli
                                        int half, float m, float l, const f32x16 (&o)[DB])
 {
     const int t = a.by_g.div(row), h = hk * a.G + row - t * a.G;
-    const float to = m - kWeightBias<T>;
     if (splits == 1) {
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
         store_columns<T, DB>(static_cast<T *>(a.out) + ((int64_t(n) * a.Tq + t) * a.H + h) * a.D, o, inv, a.D, half);
-        if (half == 0) a.lse[(int64_t(n) * a.H + h) * a.Tq + t] = l == 0.0f ? -INFINITY : (to + __log2f(l)) * kLn2;
+        if (half == 0) a.lse[(int64_t(n) * a.H + h) * a.Tq + t] = l == 0.0f ? -INFINITY : (m + __log2f(l)) * kLn2;
     } else {
         const Parts ps(part, a, splits);
         const int64_t at = split * ps.rows + int64_t(nh) * a.R + row;
         if (half == 0) {
-            ps.stat[2 * at] = l == 0.0f ? -INFINITY : to;
+            ps.stat[2 * at] = l == 0.0f ? -INFINITY : m;
             ps.stat[2 * at + 1] = l;
         }
         store_columns<float, DB>(ps.out + at * a.D, o, 1.0f, a.D, half);
@@ -171,9 +190,10 @@ __device__ __forceinline__ void add_not_finite(f32x16 (&o)[DB], const T *v, int6
 // the one before.
 // Other cuts, us for the first and the second call (438 and 695 then): 64 rows a wave 408 and 1112, 32 keys a tile 452 and
 // 835, 128 keys 427 and 1144, 8 waves a block 500 and 738, three buffers 469 and 1140.  Three waves a SIMD
-// (168 registers) took heads of 64 from 521 to 441.
+// (168 registers) took heads of 64 from 521 to 441.  Heads of 32 have four (128 registers): 4 x 4096 tokens, 8 heads, float16, 131 us, 155
+// with three; causal bfloat16 122, 96 with three.
 template <class T, int DP, int WAVES, int KT>
-__global__ __launch_bounds__(WAVES * 64, DP * sizeof(T) <= 128 ? 3 : DP * sizeof(T) <= 256 ? 2 : 1) void attend_kernel(
+__global__ __launch_bounds__(WAVES * 64, DP * sizeof(T) <= 64 ? 4 : DP * sizeof(T) <= 128 ? 3 : DP * sizeof(T) <= 256 ? 2 : 1) void attend_kernel(
     Attention a, float *part, int tiles, int splits, int chunk)
 {
     using L = Tile<T, DP>;
@@ -252,7 +272,7 @@ __global__ __launch_bounds__(WAVES * 64, DP * sizeof(T) <= 128 ? 3 : DP * sizeof
             auto value = [&](int i) { return L::by_columns(vl, i / DB * 16, i % DB, lane); };
             values.prime(value);
             if (kt >= whole) hide(s, seen - kt * KT, half);
-            run.look(s, o, c);
+            run.template look<T>(s, o, c);
             run.template weigh<T>(s, c);
             Frag<T> p;
             values.run(value, [&](int i, const Frag<T> &f) {
@@ -338,7 +358,7 @@ __global__ __launch_bounds__(WAVES * 64, DP * sizeof(T) <= 256 ? 2 : 1) void att
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) s[0] = mma(L::by_rows(kl, lane & 31, ks, half), q[ks], s[0]);
         if (kt >= whole) hide(s, seen - kt * 32, half);
-        run.look(s, o, c);
+        run.template look<T>(s, o, c);
         run.weigh<T>(s, c);
         if (kt >= mixed) odd |= __any(mv.drop_not_finite());
         mv.store(vl);
