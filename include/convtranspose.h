@@ -590,7 +590,8 @@ ct_status attention_workspace_size(ct_dtype dtype, const int64_t *q_shape, int64
  * with inverse on the gradient of y.
  *   dtype          CT_FLOAT32, CT_FLOAT16 or CT_BFLOAT16; one rounding
  *   shape          {N, T, H, D}, strides of x and y as for attention_nd; y may be x itself (with
- *                  x's strides) and must not overlap it otherwise
+ *                  x's strides) and must not overlap it otherwise.  Fewer than 2^31 tokens and elements of
+ *                  a token, at most 2^30 heads
  *   position_dtype CT_INT32 or CT_INT64; positions is (N, T, axes), its axes dense,
  *                  position_strides those of N and T (0: the same for all images or tokens)
  *   axes           1..4; R <= 256, 2 R <= D

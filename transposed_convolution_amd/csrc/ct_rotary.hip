@@ -175,6 +175,8 @@ extern "C" ct_status rotary_nd(ct_dtype dtype, const int64_t *shape, const void 
         (shape[1] && shape[0] >= most / shape[1]) ||
         (shape[3] && (shape[2] >= most / shape[3])))
         return fail(CT_EUNSUPPORTED, "more than 2^31 tokens or elements of a token");
+    // (the sum of two counts of heads is an int)
+    if (shape[2] > most / 2) return fail(CT_EUNSUPPORTED, "more than 2^30 heads are not served");
     for (int i = 0; i < 3; ++i)
         if (x_strides[i] < 0 || y_strides[i] < 0 || x_strides[i] > (int64_t(1) << 40) || y_strides[i] > (int64_t(1) << 40))
             return fail(CT_EINVAL, "strides must lie in 0 .. 2^40");
