@@ -43,6 +43,7 @@ class AttentionDecoder:
         scales = lambda: [torch.zeros((p.numel() + 255) // 256, device=device) for p in self.parameters()]  # noqa: E731
         self.m, self.v = make(), make()
         self.scales = {} if state_bits == 32 else dict(m_scales=scales(), v_scales=scales())
+        self.betas = (0.9, 0.999 if state_bits == 32 else 0.95)  # what 8 bits can follow
         self.steps = torch.zeros(1, dtype=torch.int64, device=device)
 
     def parameters(self):
@@ -94,7 +95,7 @@ class AttentionDecoder:
 
     def update(self, grads, lr):
         self.steps += 1
-        T.adamw_nd(self.parameters(), grads, self.m, self.v, lr=lr, step=self.steps, weight_decay=(0.01, 0.0, 0.0),
+        T.adamw_nd(self.parameters(), grads, self.m, self.v, lr=lr, step=self.steps, betas=self.betas, weight_decay=(0.01, 0.0, 0.0),
                    copies=(self.lookup, None, None), **self.scales)
 
 

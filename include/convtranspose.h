@@ -616,7 +616,12 @@ ct_status rotary_nd(ct_dtype dtype, const int64_t *shape, const void *x, const i
  *                  magnitude / 448, at least 2^-126; a code is the quotient rounded to nearest, but
  *                  a positive sqrt(v) has at least the smallest code, 2^-9.  Zeros everywhere
  *                  (scales too) are the states before the first step.  One value that is not
- *                  finite makes its block's states NaN.  The step itself uses m and v unrounded
+ *                  finite makes its block's states NaN.  The step itself uses m and v unrounded.
+ *                  Nearest codes lie 6 to 12 % apart, so a change of sqrt(v) by less than half of that, beside
+ *                  the largest of its 256, is lost at each step: a step without gradients brings
+ *                  1 - sqrt(beta2), which is enough up to beta2 = 0.89.  With noisy gradients v follows a
+ *                  fall up to beta2 = 0.95 (to 0.88..1.14 of sqrt(v) in 32 bits), at 0.98 in part, and at 0.99 and
+ *                  0.999 it stays several times too large, so steps stay small: take 32 bits there
  *   copy_dtype     type of the copies: CT_FLOAT16 or CT_BFLOAT16 (any value without copies)
  *   lr, grad_scale, step   host values; lr_device, grad_scale_device (one float32) and step_device (one int64)
  *                  are read when the kernels run and take their place, or NULL.  step counts from 1

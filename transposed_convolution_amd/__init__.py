@@ -1060,7 +1060,9 @@ def adamw_nd(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], ms: 
 
     params: float32/float16/bfloat16, grads: any of these, all dense and of one type each.  ms, vs: the
     moments, float32; or float8_e4m3fn with ``m_scales`` and ``v_scales``, a float32 for each 256
-    consecutive elements (m = value * scale, sqrt(v) = value * scale), all zeros at the start.
+    consecutive elements (m = value * scale, sqrt(v) = value * scale), all zeros at the start.  8 bits are for
+    ``betas[1]`` up to 0.95: at 0.99 and more a second moment that falls beside others of its 256 does not
+    follow, since a step changes it by less than half a code.
     ``step``: the number of the step, from 1.  ``weight_decay``: one number, or one a tensor.
     ``grad_scale``: multiplies the gradients (one over a loss scale).  ``copies``: float16 or bfloat16
     tensors (or None) that receive the updated parameters too.  ``lr``, ``step`` and ``grad_scale`` may be
