@@ -8,7 +8,7 @@ import torch
 
 import attention_refs as A
 import layer_refs as R
-from test_gpu_attention import DT, T, host, inputs  # noqa: F401  (T: the fixture)
+from test_gpu_attention import DT, T, dev, host, inputs  # noqa: F401  (T: the fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -91,3 +91,43 @@ def test_they_take_no_longer(T, where):  # noqa: F811
     plain, odd = micros(*tensors[:3]), micros(q, k, v)
     print(f"{where}: {odd:.0f} us, {plain:.0f} without")
     assert odd <= 4 * plain
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("shape", [(200, 2, 1, 40), (600, 24, 24, 64), (600, 24, 12, 128)], ids=str)
+@pytest.mark.parametrize("which", ["k", "v", "q", "do"])
+def test_gradients_are_right_or_not_finite(T, shape, dtype, which):  # noqa: F811
+    """A value that is not finite may reach the gradients of its image and key head, as NaN or infinities: what is
+    finite is right.  NaN is there where its sums are.  Other images and key heads are right."""
+    t, h, hk, d = shape
+    seen = A.visible(2, t, t, True, None, None)
+    tensors, arrays = inputs(dtype, 2, t, t, h, hk, d, seed=97)
+    (o, l), _ = A.attend(*arrays[:3], d ** -0.5, seen, dtype)
+    out, o = dev(o, dtype)
+    lse, l = dev(l, "f32")
+    want, tol = A.attend_grad(arrays[3], *arrays[:3], o, l, d ** -0.5, seen, dtype)
+    at, g = t // 3, h // hk
+    rows = slice(at, at + 1) if which in ("q", "do") else slice(at, None)  # the tokens that it is in
+    for bad in (float("nan"), float("inf")):
+        q, k, v, do = (x.clone() for x in tensors)
+        dict(q=q, k=k, v=v, do=do)[which][1, at, 0, 2] = bad
+        given = (out.clone(), lse.clone())
+        if which != "do":  # those tokens' out and lse are what the forward call leaves
+            made = T.attention_nd(q, k, v, causal=True)
+            given[0][1, rows, :g], given[1][1, :g, rows] = made[0][1, rows, :g], made[1][1, :g, rows]
+        grads = T.attention_backward_nd(do, q, k, v, *given, causal=True)
+        torch.cuda.synchronize()
+        for name, got, w, bound in zip(("dq", "dk", "dv"), map(host, grads), want, tol):
+            mine, sums = np.zeros(got.shape, bool), np.zeros(got.shape, bool)
+            mine[1, :, :g if name == "dq" else 1] = True
+            if name == "dq":  # the sums that it is in
+                sums[1, rows, :g] = True
+            elif name == "dk" or which != "v":
+                sums[1, :, 0] = True
+            assert np.isfinite(got[~mine]).all(), (name, bad)
+            if bad != bad and name == "dq":
+                assert np.isnan(got[1, rows, 0]).any(-1).all(), name
+            elif bad != bad and sums.any():
+                assert np.isnan(got[1, :at + 1, 0]).any(-1).all(), name
+            fine = np.isfinite(got) & ~sums
+            R.assert_close(np.where(fine, got, 0.0), np.where(fine, w, 0.0), bound, dtype, f"{name} {bad}")

@@ -86,7 +86,8 @@ __global__ __launch_bounds__(256) void stat_kernel(Attention a, RowStat *stat, f
         if (kHalf<T>) {
 #pragma unroll
             for (int s = LANES / 2; s; s >>= 1) sq += __shfl_xor(sq, s);
-            most = fmaxf(most, sq);
+            // one that is not finite says nothing about the others, whose score gradients would become zeros
+            most = fmaxf(most, sq < INFINITY ? sq : 0.0f);
         }
     }
     if constexpr (kHalf<T>) {
@@ -126,7 +127,7 @@ __device__ __forceinline__ float uniform(float x)
     return __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, x)));
 }
 // The power of two by which dS is held whose magnitude has log2 below `bound`.  2^60 is enough for any: what is below
-// 2^-25 there is 2^-85 and nothing in float16, however many are summed.  (Values that are not finite end at 200.)
+// 2^-25 there is 2^-85 and nothing in float16, however many are summed.  (A row that is not finite ends at one of both: its score gradients are not finite then.)
 __device__ __forceinline__ int grad_shift(float bound)
 {
     return kHalfBias - int(ceilf(fminf(fmaxf(bound, float(kHalfBias - 60)), 200.0f)));
