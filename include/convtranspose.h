@@ -560,9 +560,10 @@ ct_status attention_nd(ct_dtype dtype, const int64_t *q_shape, int64_t kv_tokens
  * dS = scale * P * (dP - delta):
  *   dv_j = sum of P_ij dout_i,  dk_j = sum of dS_ij q_i,  dq_i = sum of dS_ij k_j,
  * the sums for keys over the tokens and heads that see them.  P is computed again, nothing of
- * size Tq * kv_tokens is stored; lse is a float32, so P is off by up to 2^-22 |lse| of itself.  Keys
- * at or behind lengths[n] get zeros, so do tokens that see nothing (whatever dout and q hold there).  One value that is not finite where something is seen may
- * make all gradients of its image and key head NaN.
+ * size Tq * kv_tokens is stored; lse is a float32, so P is off by up to 2^-22 |lse| of itself (beyond
+ * |lse| = 2^21 float16 gradients may not be finite).  Keys at or behind lengths[n] get zeros, so do
+ * tokens that see nothing (whatever dout and q hold there).  One value that is not finite where
+ * something is seen may make all gradients of its image and key head NaN.
  *   dout, out      (N, Tq, H, D) with strides like q's; out and lse are what attention_nd wrote
  *   dq, dk, dv     dense (N, Tq, H, D), (N, kv_tokens, kv_heads, D) twice, of dtype, not
  *                  overlapping anything else

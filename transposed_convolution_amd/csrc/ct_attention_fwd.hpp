@@ -182,8 +182,8 @@ __device__ __forceinline__ void add_not_finite(f32x16 (&o)[DB], const T *v, int6
 }
 
 // A wave holds 32 rows, a block goes through the keys KT at a time; the next tile is on its way while one
-// is worked on.  8 x 4096 tokens, 8 heads of 64, float16: 405 us, 680 TFLOP/s; 2 x 8191 causal tokens, 16 heads over 4
-// of 128, bfloat16: 685 us, 800 TFLOP/s; heads of 256, 2 x 4096 tokens, 4 heads, float16: 350 us, 390 TFLOP/s (one
+// is worked on.  8 x 4096 tokens, 8 heads of 64, float16: 400 to 433 us by card, 635 to 690 TFLOP/s; 2 x 8191 causal
+// tokens, 16 heads over 4 of 128, bfloat16: 666 to 695 us; heads of 256, 2 x 4096 tokens, 4 heads, float16: 350 us, 390 (one
 // wave a SIMD).  Bound by the vector unit beside the matrix unit: a score takes 6 vector instructions, one of them the
 // exponential at a half of their rate, so that 32 x 32 scores take 500 cycles of them and, with heads of 64, 256 of matrix
 // instructions; the two are busy 60 and 30 % of the time (heads of 128: 44 and 34 %), the rest is steps that wait for

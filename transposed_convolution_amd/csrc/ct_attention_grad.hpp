@@ -8,15 +8,17 @@
 // and sums dk and dv over the rows, those of all query heads of its key head among them; the other
 // holds a block of rows and sums dq over the keys.  That is 7 products where one kernel that also
 // added into dq would take 5, but every sum has one owner and a fixed order: no atomics, the
-// same bits every time.  8 x 4096 tokens, 8 heads of 64, float16: 1210 us, 22 of them for the rows'
-// statistics, 750 for the keys (matrix unit busy 35 %), 490 for the rows (41 %); 570 TFLOP/s of the 5 products, 800
+// same bits every time.  8 x 4096 tokens, 8 heads of 64, float16: 1230 us, 22 of them for the rows'
+// statistics, 764 for the keys (matrix unit busy 33 %), 496 for the rows (41 %); 560 TFLOP/s of the 5 products, 780
 // of the 7.  Both kernels are bound as the forward one is, by the vector instructions of a score (8 here) and
 // by waiting between dependent steps at two or three waves a SIMD.
 //
 // float16 has few exponents, and P is about 1 / Tk: P is held 2^15 times larger, and dS by a power of two
 // that takes its largest possible value, scale * 2 |do| max|v|, to 2^15: of its row in the sum for dq, of its tile of
 // rows in the sum for dk, which is scaled where that power changes.  So a row's gradient keeps its digits whatever
-// size that of other rows has.  Both powers are taken out of the float32 sums at the end.
+// size that of other rows has.  Both powers are taken out of the float32 sums at the end.  (One power for a whole
+// head took 1217 us in the call above, and 1156 for 1207 with 4 x 4096 tokens and heads of 128; rows 2^22 smaller
+// than another lost all digits.)
 #pragma once
 
 #include "ct_attention.hpp"
@@ -33,8 +35,8 @@ struct RowStat {
     float lse2, delta;
 };
 
-// Operands asked for ahead.  Gradient with heads of 64 / 128 / 256 (float16, 4096 tokens), 2: 1242 / 1204 / 1280 us,
-// 3: 1240 / 1140 / 1424, 4: 1230 / 1180 / 1305; registers are short in long heads.
+// Operands asked for ahead.  Gradient with heads of 64 / 128 / 256 (float16, 4096 tokens; with one power of dS a head), 2:
+// 1242 / 1204 / 1280 us, 3: 1240 / 1140 / 1424, 4: 1230 / 1180 / 1305; registers are short in long heads.
 template <class T, int DP>
 constexpr int kAhead = DP * sizeof(T) > 256 ? 2 : DP * sizeof(T) > 128 ? 3 : 4;
 
@@ -127,7 +129,8 @@ __device__ __forceinline__ float uniform(float x)
     return __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, x)));
 }
 // The power of two by which dS is held whose magnitude has log2 below `bound`.  2^60 is enough for any: what is below
-// 2^-25 there is 2^-85 and nothing in float16, however many are summed.  (A row that is not finite ends at one of both: its score gradients are not finite then.)
+// 2^-25 there is 2^-85 and nothing in float16, however many are summed.  (A row that is not finite ends at either end;
+// its score gradients are not finite then.)
 __device__ __forceinline__ int grad_shift(float bound)
 {
     return kHalfBias - int(ceilf(fminf(fmaxf(bound, float(kHalfBias - 60)), 200.0f)));
@@ -160,7 +163,7 @@ struct Share {
 // too: 8 waves share the rows' tile then, so that one block of 16-bit heads of 128 has 147 KB (4096 tokens, 4 x 8
 // heads, float16: 1410 us with 4 waves and the keys in registers, some of them in scratch, 1325 with 8, 1204 with the keys
 // in LDS).  At 256 elements of 16 bits two waves share the 32 keys, each with half of the columns: both make all
-// scores, 6 products for 4, but one wave kept 900 bytes in scratch (2 x 4096 tokens, 4 heads, float16: 3927 us, now 1290).
+// scores, 6 products for 4, but one wave kept 900 bytes in scratch (2 x 4096 tokens, 4 heads, float16: 3927 us, now 1326).
 template <class T, int DP>
 struct KeyPlan {
     static constexpr int kBytes = DP * int(sizeof(T));
