@@ -350,21 +350,32 @@ struct Mover {
             r[i] = load_chunk<T>(p + column, p ? D - column : 0, D % L::kChunk);
         }
     }
-    // Values that are not finite become zeros; were there any?
+    // Values that are not finite become zeros; were there any in the wave?  Their exponent is all ones: one more at its
+    // lowest bit carries into the sign's, two elements a word where they have 16 bits.
     __device__ __forceinline__ bool drop_not_finite()
     {
         using U = std::conditional_t<sizeof(T) == 2, unsigned short, unsigned>;
-        constexpr U ONES = std::is_same_v<T, _Float16> ? 0x7c00 : sizeof(T) == 2 ? 0x7f80 : U(0x7f800000);  // the exponent's
-        bool found = false;
+        constexpr U ONES = std::is_same_v<T, _Float16> ? 0x7c00 : sizeof(T) == 2 ? 0x7f80 : U(0x7f800000);
+        constexpr U LOWEST = std::is_same_v<T, _Float16> ? 0x0400 : sizeof(T) == 2 ? 0x0080 : U(0x00800000);
+        constexpr unsigned TWICE = sizeof(T) == 2 ? 0x10001u : 1u;
+        using Words = unsigned __attribute__((ext_vector_type(4)));
+        unsigned carry = 0;
 #pragma unroll
-        for (int i = 0; i < kPieces; ++i)
+        for (int i = 0; i < kPieces; ++i) {
+            const Words w = __builtin_bit_cast(Words, r[i]);
 #pragma unroll
-            for (int j = 0; j < L::kChunk; ++j) {
-                const T x = r[i][j];
-                const bool odd = (__builtin_bit_cast(U, x) & ONES) == ONES;
-                r[i][j] = odd ? T(0.0f) : x;
-                found |= odd;
-            }
+            for (int j = 0; j < 4; ++j) carry |= (w[j] & ONES * TWICE) + LOWEST * TWICE;
+        }
+        const bool found = __any(carry & (sizeof(T) == 2 ? 0x80008000u : 0x80000000u));
+        if (found) {
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i)
+#pragma unroll
+                for (int j = 0; j < L::kChunk; ++j) {
+                    const T x = r[i][j];
+                    r[i][j] = (__builtin_bit_cast(U, x) & ONES) == ONES ? T(0.0f) : x;
+                }
+        }
         return found;
     }
     __device__ __forceinline__ void store(T *tile) const

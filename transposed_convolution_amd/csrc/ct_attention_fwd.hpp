@@ -183,7 +183,7 @@ __device__ __forceinline__ void add_not_finite(f32x16 (&o)[DB], const T *v, int6
 
 // A wave holds 32 rows, a block goes through the keys KT at a time; the next tile is on its way while one
 // is worked on.  8 x 4096 tokens, 8 heads of 64, float16: 400 to 433 us by card, 635 to 690 TFLOP/s; 2 x 8191 causal
-// tokens, 16 heads over 4 of 128, bfloat16: 666 to 695 us; heads of 256, 2 x 4096 tokens, 4 heads, float16: 350 us, 390 (one
+// tokens, 16 heads over 4 of 128, bfloat16: 656 to 695 us; heads of 256, 2 x 4096 tokens, 4 heads, float16: 350 us, 390 (one
 // wave a SIMD).  Bound by the vector unit beside the matrix unit: a score takes 6 vector instructions, one of them the
 // exponential at a half of their rate, so that 32 x 32 scores take 500 cycles of them and, with heads of 64, 256 of matrix
 // instructions; the two are busy 60 and 30 % of the time (heads of 128: 44 and 34 %), the rest is steps that wait for
@@ -241,7 +241,10 @@ __global__ __launch_bounds__(WAVES * 64, DP * sizeof(T) <= 64 ? 4 : DP * sizeof(
     };
     int found = 0;  // did this wave bring values that are not finite in such tiles
     auto store = [&](int buf, int kt) {
-        if (kt >= mixed) found |= __any(vm.drop_not_finite());
+        if (kt >= mixed) {
+            found |= vm.drop_not_finite();
+            if (lane == 0) odd[wave] = found;
+        }
         km.store(lds[buf][0]);
         vm.store(lds[buf][1]);
     };
@@ -284,10 +287,8 @@ __global__ __launch_bounds__(WAVES * 64, DP * sizeof(T) <= 64 ? 4 : DP * sizeof(
     }
     const int odd0 = max(mixed, kt0);
     if (odd0 < kt1) {
-        if (lane == 0) odd[wave] = found;
-        __syncthreads();
 #pragma unroll
-        for (int i = 0; i < WAVES; ++i) found |= odd[i];
+        for (int i = 0; i < WAVES; ++i) found |= odd[i];  // complete since the last tile's barrier
         if (__builtin_amdgcn_readfirstlane(found))
             add_not_finite<T, DB>(o, vp + int64_t(odd0) * KT * a.v.t, a.v.t, min(kt1 * KT, len) - odd0 * KT, seen - odd0 * KT, a.D, lane);
     }
@@ -360,7 +361,7 @@ __global__ __launch_bounds__(WAVES * 64, DP * sizeof(T) <= 256 ? 2 : 1) void att
         if (kt >= whole) hide(s, seen - kt * 32, half);
         run.template look<T>(s, o, c);
         run.weigh<T>(s, c);
-        if (kt >= mixed) odd |= __any(mv.drop_not_finite());
+        if (kt >= mixed) odd |= mv.drop_not_finite();
         mv.store(vl);
         const int next = kt + WAVES;
         if (next < kt1) mv.load(kp + int64_t(next) * 32 * a.k.t, a.k.t, len - next * 32, a.D);
