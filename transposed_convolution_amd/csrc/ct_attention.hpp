@@ -367,7 +367,7 @@ struct Mover {
             for (int j = 0; j < 4; ++j) carry |= (w[j] & ONES * TWICE) + LOWEST * TWICE;
         }
         const bool found = __any(carry & (sizeof(T) == 2 ? 0x80008000u : 0x80000000u));
-        if (found) {
+        if (__builtin_expect(found, 0)) {
 #pragma unroll
             for (int i = 0; i < kPieces; ++i)
 #pragma unroll

@@ -66,7 +66,7 @@ struct Running {
     {
         const float base = m == -INFINITY ? 0.0f : m;
         float by = c;
-        if (__any(fabsf(base) >= kFar)) {
+        if (__builtin_expect(__any(fabsf(base) >= kFar), 0)) {
             far(s, c);
             by = 1.0f;
         }
@@ -133,7 +133,8 @@ __device__ __forceinline__ void finish(const Attention &a, float *part, int spli
 // otherwise.  In tiles that every row sees it takes part as it is.
 //
 // This happens only where such a value was found: a lane looks at one of 64 keys, then those that have any are taken
-// from memory, several at a time where heads are short.  `end`: how many of the keys the lane's row sees.
+// from memory, several at a time where heads are short.  `end`: how many of the keys the lane's row sees.  2048 causal
+// tokens, 4 heads of 64, float16: 35 us, as many with a NaN that all rows see, 100 with nothing but infinities.
 template <class T, int DB>
 __device__ __forceinline__ void add_not_finite(f32x16 (&o)[DB], const T *v, int64_t stride, int keys, int end, int D, int lane)
 {
@@ -157,12 +158,13 @@ __device__ __forceinline__ void add_not_finite(f32x16 (&o)[DB], const T *v, int6
                 for (int key = 0; key < K; ++key)
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
+                        // every lane loads, whatever its row sees: no load is in a branch of its own
                         const int d = db * 32 + 8 * k + 4 * half;
-                        const T *p = v + (j + key) * stride + d;
+                        const T *p = v + min(j + key, keys - 1) * stride + d;
                         x[key][k] = Raw<T, 4>{};
-                        if (j + key < end && d + 4 <= D) {
+                        if (D == DB * 32 || d + 4 <= D) {
                             x[key][k] = *reinterpret_cast<const Raw<T, 4> *>(p);
-                        } else if (j + key < end) {
+                        } else {
 #pragma unroll
                             for (int i = 0; i < 3; ++i)
                                 if (d + i < D) x[key][k][i] = p[i];
@@ -171,9 +173,13 @@ __device__ __forceinline__ void add_not_finite(f32x16 (&o)[DB], const T *v, int6
 #pragma unroll
                 for (int key = 0; key < K; ++key)
 #pragma unroll
-                    for (int r = 0; r < 16; ++r) {
-                        const float f = float(x[key][r / 4][r % 4]);
-                        o[db][r] += finite(f) ? 0.0f : f;
+                    for (int k = 0; k < 4; ++k) {
+                        const Raw<T, 4> seen = j + key < end ? x[key][k] : Raw<T, 4>{};
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float f = float(seen[i]);
+                            o[db][4 * k + i] += finite(f) ? 0.0f : f;
+                        }
                     }
                 __builtin_amdgcn_sched_barrier(0);
             }
@@ -289,7 +295,7 @@ __global__ __launch_bounds__(WAVES * 64, DP * sizeof(T) <= 64 ? 4 : DP * sizeof(
     if (odd0 < kt1) {
 #pragma unroll
         for (int i = 0; i < WAVES; ++i) found |= odd[i];  // complete since the last tile's barrier
-        if (__builtin_amdgcn_readfirstlane(found))
+        if (__builtin_expect(__builtin_amdgcn_readfirstlane(found), 0))
             add_not_finite<T, DB>(o, vp + int64_t(odd0) * KT * a.v.t, a.v.t, min(kt1 * KT, len) - odd0 * KT, seen - odd0 * KT, a.D, lane);
     }
     const float l = half_sum(run.l);
